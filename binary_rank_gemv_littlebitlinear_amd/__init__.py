@@ -18,6 +18,8 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblb.so")
 
+LB_F16, LB_F32 = 0, 1
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 LB_OK, LB_EINVAL, LB_ENOMEM, LB_EHIP, LB_ENOTREADY, LB_EUNSUPPORTED, LB_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
 
 
@@ -69,6 +71,14 @@ def load_library(path: str = LIB_PATH):
         "lb_stack_test_delay": ([vp, C.c_uint32, C.c_uint32], i32),
         "lb_stack_timeline": ([vp, vp, i64, P(i64)], i32),
         "lb_stack_destroy": ([vp], i32),
+        "lb_bank_create": ([vp, vp, i32, P(vp)], i32),
+        "lb_bank_reserve": ([vp, i64], i32),
+        "lb_bank_forward": ([vp, i32, vp, i64, vp, i64, i32, i64, i32, vp, vp, vp, i64, vp], i32),
+        "lb_bank_grouped": ([vp, vp, i64, i64, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp], i32),
+        "lb_bank_destroy": ([vp], i32),
+        "lb_route_ws_bytes": ([i64, i32, i32, P(u64)], i32),
+        "lb_route": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, u64, vp], i32),
+        "lb_route_combine": ([vp, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp, i64, i32, vp], i32),
         "lb_status_str": ([i32], C.c_char_p),
         "lb_last_error": ([], C.c_char_p),
         "lb_version": ([], i32),
@@ -88,7 +98,9 @@ EXPORTED = ("lb_create", "lb_pack_signs", "lb_set_scales", "lb_forward", "lb_for
             "lb_eff_bits", "lb_rank_for_bpw", "lb_stack_create", "lb_stack_forward",
             "lb_stack_trace_elems", "lb_stack_reserve", "lb_stack_set_mode", "lb_stack_check",
             "lb_stack_test_wait_failure", "lb_stack_test_delay",
-            "lb_stack_timeline", "lb_stack_destroy", "lb_status_str", "lb_last_error", "lb_version")
+            "lb_stack_timeline", "lb_stack_destroy",
+            "lb_bank_create", "lb_bank_reserve", "lb_bank_forward", "lb_bank_grouped", "lb_bank_destroy",
+            "lb_route_ws_bytes", "lb_route", "lb_route_combine", "lb_status_str", "lb_last_error", "lb_version")
 
 
 def _status_name(st: int) -> str:
@@ -304,6 +316,148 @@ def lb_stack_destroy(stack: int):
     _check(load_library().lb_stack_destroy(stack))
 
 
+def lb_bank_create(layers, gates=None) -> int:
+    arr = (C.c_void_p * len(layers))(*layers)
+    if gates is not None and len(gates) != len(layers):
+        raise ValueError("a bank needs as many gates as layers")
+    gar = (C.c_void_p * len(gates))(*gates) if gates is not None else None
+    out = C.c_void_p()
+    _check(load_library().lb_bank_create(C.cast(arr, C.c_void_p), C.cast(gar, C.c_void_p) if gar else None,
+                                         len(layers), C.byref(out)))
+    return out.value
+
+
+def lb_bank_reserve(bank: int, rows: int):
+    _check(load_library().lb_bank_reserve(bank, int(rows)))
+
+
+def _rows(name, t, width, dtypes, device):
+    """Row stride of a 2-d device tensor with unit column stride."""
+    if t.dim() != 2 or t.shape[1] != width or t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{name} must be a 2-d tensor of {width} columns on {device}, of {dtypes}, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.stride(1) != 1 and width > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    # a single row's stride is never used; torch leaves it arbitrary
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def _flat(name, t, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
+                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _stream_of(stream, device):
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _act(name) -> int:
+    try:
+        return ACTIVATIONS[name or "none"]
+    except KeyError:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {name!r}") from None
+
+
+def _epilogue(bank, y, act, bias, gate_bias, residual):
+    """The arguments that lb_bank_forward and lb_bank_grouped share."""
+    import torch
+    dev, b, n = y.device, bank.b, bank.n
+    if dev.type != "cuda":
+        raise ValueError("y must be a device tensor")
+    f16, f32 = torch.float16, torch.float32
+    ldy = _rows("y", y, b, (f16, f32), dev)
+    pb = _flat("bias", bias, (n, b), f16, dev) if bias is not None else None
+    pg = _flat("gate_bias", gate_bias, (n, b), f16, dev) if gate_bias is not None else None
+    pr, ldr = None, 0
+    if residual is not None:
+        ldr = _rows("residual", residual, b, (y.dtype,), dev)
+        if residual.shape[0] != y.shape[0]:
+            raise ValueError("residual must have y's rows")
+        pr = residual.data_ptr()
+    return y.data_ptr(), ldy, LB_F32 if y.dtype == f32 else LB_F16, _act(act), pb, pg, pr, ldr
+
+
+def lb_bank_forward(bank, x, y, expert: int = 0, act=None, bias=None, gate_bias=None, residual=None, stream=None):
+    """``Bank`` owner and tensors: y = act(layer(x) + bias) + residual (see include/lb.h)."""
+    import torch
+    py, ldy, yt, a, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
+    ldx = _rows("x", x, bank.a, (torch.float16,), y.device)
+    if x.shape[0] != y.shape[0]:
+        raise ValueError("x and y must have the same number of rows")
+    _check(load_library().lb_bank_forward(bank.handle, expert, x.data_ptr(), ldx, py, ldy, yt, x.shape[0], a, pb, pg,
+                                          pr, ldr, _stream_of(stream, y.device)))
+
+
+def lb_bank_grouped(bank, x, offsets, y, index=None, act=None, bias=None, gate_bias=None, residual=None,
+                    stream=None):
+    """``Bank`` owner and tensors: rows offsets[e]..offsets[e+1]-1 through layer e (see include/lb.h)."""
+    import torch
+    py, ldy, yt, a, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
+    rows, i32 = y.shape[0], torch.int32
+    ldx = _rows("x", x, bank.a, (torch.float16,), y.device)
+    po = _flat("offsets", offsets, (bank.n + 1,), i32, y.device)
+    pi = _flat("index", index, (rows,), i32, y.device) if index is not None else None
+    _check(load_library().lb_bank_grouped(bank.handle, x.data_ptr(), x.shape[0], ldx, pi, po, rows, py, ldy, yt, a, pb,
+                                          pg, pr, ldr, _stream_of(stream, y.device)))
+
+
+def lb_bank_destroy(bank: int):
+    _check(load_library().lb_bank_destroy(bank))
+
+
+def lb_route_ws_bytes(tokens: int, experts: int, k: int) -> int:
+    n = C.c_uint64()
+    _check(load_library().lb_route_ws_bytes(int(tokens), int(experts), int(k), C.byref(n)))
+    return n.value
+
+
+def lb_route(logits, k: int, renormalise: bool, ids, weights, offsets, token, row, ws, stream=None):
+    """Tensors of include/lb.h's lb_route; ws is a device byte tensor of lb_route_ws_bytes bytes, or None."""
+    import torch
+    if logits.dim() != 2 or logits.device.type != "cuda":
+        raise ValueError("logits must be a 2-d device tensor")
+    t, e = logits.shape
+    dev, i32 = logits.device, torch.int32
+    ld = _rows("logits", logits, e, (torch.float16, torch.float32), dev)
+    args = [_flat("ids", ids, (t, k), i32, dev), _flat("weights", weights, (t, k), torch.float32, dev),
+            _flat("offsets", offsets, (e + 1,), i32, dev), _flat("token", token, (t * k,), i32, dev),
+            _flat("row", row, (t, k), i32, dev)]
+    n = 0
+    if ws is not None:
+        n = ws.numel()
+        _flat("ws", ws, (n,), torch.uint8, dev)
+    with torch.cuda.device(dev):
+        _check(load_library().lb_route(logits.data_ptr(), LB_F32 if logits.dtype == torch.float32 else LB_F16, ld, t, e,
+                                       k, int(bool(renormalise)), *args, _ptr(ws), n, _stream_of(stream, dev)))
+
+
+def lb_route_combine(y, row, weights, out, residual=None, stream=None):
+    """out[t] = residual[t] + sum_j weights[t, j] * y[row[t, j]] (see include/lb.h)."""
+    import torch
+    if out.dim() != 2 or out.device.type != "cuda" or row.dim() != 2:
+        raise ValueError("out must be a 2-d device tensor and row a 2-d tensor")
+    t, width = out.shape
+    k, dev = row.shape[1], out.device
+    ldo = _rows("out", out, width, (torch.float16, torch.float32), dev)
+    ldy = _rows("y", y, width, (torch.float16,), dev)
+    pr, ldr = None, 0
+    if residual is not None:
+        ldr = _rows("residual", residual, width, (out.dtype,), dev)
+        if residual.shape[0] != t:
+            raise ValueError("residual must have out's rows")
+        pr = residual.data_ptr()
+    pw, pi = _flat("weights", weights, (t, k), torch.float32, dev), _flat("row", row, (t, k), torch.int32, dev)
+    with torch.cuda.device(dev):
+        _check(load_library().lb_route_combine(y.data_ptr(), y.shape[0], ldy, pi, pw, t, k, width, pr, ldr,
+                                               out.data_ptr(), ldo, LB_F32 if out.dtype == torch.float32 else LB_F16,
+                                               _stream_of(stream, dev)))
+
+
 # --------------------------------------------------------------- owners
 class Layer:
     """Owner of one lb_layer handle."""
@@ -376,6 +530,73 @@ class Stack:
             self.close()
         except Exception:
             pass
+
+
+class Bank:
+    """Owner of one lb_bank handle (keeps its layers alive).
+
+    ``layers`` and ``gates`` are ``Layer`` objects of one shape; without gates a call computes
+    act(layer(x) + bias) + residual, with them act(gate(x) + gate_bias) * (layer(x) + bias) + residual.
+    Biases are fp16 tensors of (layers, b).
+    """
+
+    def __init__(self, layers, gates=None):
+        self.handle = None
+        self.layers = list(layers)
+        self.gates = list(gates) if gates is not None else None
+        if not self.layers:
+            raise ValueError("a bank needs at least one layer")
+        self.n, self.a, self.b = len(self.layers), self.layers[0].a, self.layers[0].b
+        self.handle = lb_bank_create([L.handle for L in self.layers],
+                                     [L.handle for L in self.gates] if self.gates is not None else None)
+
+    def reserve(self, rows: int):
+        lb_bank_reserve(self.handle, rows)
+
+    def forward(self, x, y, expert: int = 0, act=None, bias=None, gate_bias=None, residual=None, stream=None):
+        lb_bank_forward(self, x, y, expert, act, bias, gate_bias, residual, stream)
+
+    def grouped(self, x, offsets, y, index=None, act=None, bias=None, gate_bias=None, residual=None, stream=None):
+        lb_bank_grouped(self, x, offsets, y, index, act, bias, gate_bias, residual, stream)
+
+    def close(self):
+        if self.handle:
+            lb_bank_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Route:
+    """The routing of a fixed number of tokens: owner of lb_route's outputs and scratch.
+
+    After ``run(logits)`` the device tensors ``experts``, ``weights`` and ``row`` (tokens, k), ``offsets``
+    (experts + 1) and ``token`` (tokens * k) hold the result; a later run overwrites them.
+    """
+
+    def __init__(self, tokens: int, experts: int, k: int, renormalise: bool = True, device=None):
+        import torch
+        self.k, self.renormalise = int(k), bool(renormalise)
+        n = lb_route_ws_bytes(tokens, experts, k)
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.experts = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+        self.weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+        self.offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        self.token = torch.empty(tokens * k, dtype=torch.int32, device=dev)
+        self.row = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+    def run(self, logits, stream=None) -> "Route":
+        lb_route(logits, self.k, self.renormalise, self.experts, self.weights, self.offsets, self.token, self.row,
+                 self.ws, stream)
+        return self
+
+    def combine(self, y, out, residual=None, stream=None):
+        lb_route_combine(y, self.row, self.weights, out, residual, stream)
 
 
 def lb_status_str(status: int) -> str:

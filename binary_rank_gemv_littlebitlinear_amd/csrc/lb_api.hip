@@ -73,19 +73,6 @@ lb_status get_dev(int device, DevCtx **out) {
   return LB_OK;
 }
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    if (prev != dev) ok = hipSetDevice(dev) == hipSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
 }  // namespace
 
 static inline DevCtx *ctx_of(const lb_layer *L) { return static_cast<DevCtx *>(L->ctx); }
@@ -500,11 +487,6 @@ extern "C" lb_status lb_joint_itq(const float *U, const float *V, int64_t a, int
 }
 
 // ------------------------------------------------------------- forward
-static bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
-  const char *a = (const char *)p, *b = (const char *)q;
-  return a < b + nq && b < a + np;
-}
-
 static lb_status check_io(const Layer &Ly, const void *x, const void *y, int64_t M,
                           const char *who) {
   if (M < 0) return fail(LB_EINVAL, std::string(who) + ": M < 0");
@@ -620,6 +602,7 @@ lb_status lbi::forward_checks(const lb_layer *L, const void *x, const void *y, i
 
 lb_status lbi::set_error(lb_status st, const std::string &msg) { return fail(st, msg); }
 const void *lbi::device_zero(const lb_layer *L) { return ctx_of(L)->zero; }
+const DeviceInfo &lbi::device_info(const lb_layer *L) { return ctx_of(L)->info; }
 
 extern "C" lb_status lb_forward(const lb_layer *L, const void *x, void *y, int64_t M, void *stream) {
   lb_status st = forward_checks(L, x, y, M, "lb_forward");

@@ -40,6 +40,26 @@ struct DeviceInfo {
   int max_wg_per_cu = 0;  // for the persistent kernel (filled lazily)
 };
 
+// Makes a device current and restores the caller's at scope end.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceGuard(int dev) {
+    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
+    if (prev != dev) ok = hipSetDevice(dev) == hipSuccess;
+  }
+  ~DeviceGuard() {
+    int cur = -1;
+    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+  }
+};
+
+// Whether the np bytes at p and the nq bytes at q share any.
+inline bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
+  const char *a = (const char *)p, *b = (const char *)q;
+  return a < b + nq && b < a + np;
+}
+
 struct Layer {
   int64_t a = 0, b = 0, s = 0;
   int P = 1;
@@ -206,6 +226,7 @@ lb_status forward_ws(const lb_layer *L, const uint16_t *x, uint16_t *y, int64_t 
 lb_status forward_checks(const lb_layer *L, const void *x, const void *y, int64_t M, const char *who);
 lb_status set_error(lb_status st, const std::string &msg);
 const void *device_zero(const lb_layer *L);
+const DeviceInfo &device_info(const lb_layer *L);
 // The matrix-core sign copies of a layer, built if missing when may_alloc
 // and the stream is not capturing (allocates, synchronises the device);
 // LB_ENOTREADY otherwise.

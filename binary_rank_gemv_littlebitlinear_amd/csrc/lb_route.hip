@@ -1,0 +1,470 @@
+// Routing of tokens to the layers of a bank and the way back: lb_route
+// chooses every token's experts and sorts the (token, choice) rows by expert
+// for lb_bank_grouped; lb_route_combine adds the experts' outputs up.
+//
+// For token t with logits z_t (NaN counts as -inf) the choices are the k
+// largest logits, equal ones by the lowest expert; p_te = exp(z_te - max z_t);
+// weight = p_te / sum over the choices (renormalise) or over all experts.
+// Experts at -inf are never chosen: a choice that finds none has expert -1,
+// row -1 and weight 0.  The rows of expert e are offsets[e] ..
+// offsets[e + 1] - 1, in the order of the tokens.
+//
+// Choosing takes a wave per token: each lane holds its experts' keys (the
+// logit's order as an unsigned number, then the lowest index) and the wave
+// takes the largest k times.  Sorting is counting: rows per expert of every
+// block of tokens, then each block places its own rows behind those of the
+// blocks before it, 64 rows of a wave at a time (lanes with the same expert
+// find one another by ballots over the bits of its number).  Counts are
+// integers and every place is computed, so nothing depends on timing.  Up to
+// kOneBlock tokens one workgroup does it all in one launch; more take two.
+#include <hip/hip_fp16.h>
+
+#include <algorithm>
+#include <string>
+
+#include "lb_internal.h"
+
+namespace {
+
+using namespace lbi;
+
+constexpr int kWaves = 16, kThreads = kWaves * 64;
+constexpr int kMaxE = 1024, kMaxK = 64;
+constexpr int kOneBlock = 64;   // tokens that one workgroup routes alone
+constexpr int kBlocks = 256;    // at most this many blocks of tokens otherwise
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
+struct RouteArgs {
+  const void *logits;
+  int64_t ld;
+  int T, E, k, renorm, f32, tb;  // tb: tokens per block
+  int *ids;
+  float *weights;
+  int *offsets, *token, *row;
+  int *hist;  // [block][E]
+};
+
+__device__ __forceinline__ float h2f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+
+// One wave: the choices of token t.
+template <int NV>
+__device__ __forceinline__ void choose(const RouteArgs &A, int t) {
+  const int lane = threadIdx.x & 63;
+  float z[NV];
+  uint32_t key[NV];  // order-preserving; 0 for what cannot be chosen
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = i * 64 + lane;
+    float v = -INFINITY;
+    if (e < A.E) {
+      const int64_t o = (int64_t)t * A.ld + e;
+      v = A.f32 ? ((const float *)A.logits)[o] : h2f(((const uint16_t *)A.logits)[o]);
+    }
+    if (v != v) v = -INFINITY;
+    z[i] = v;
+    if (v == 0.f) v = 0.f;  // -0 and 0 are equal
+    const uint32_t u = __float_as_uint(v);
+    key[i] = v == -INFINITY ? 0u : (u & 0x80000000u ? ~u : u | 0x80000000u);
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  float all = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    z[i] = key[i] ? (z[i] == top ? 1.f : expf(z[i] - top)) : 0.f;
+    all += z[i];
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d);
+  float mine = 0.f, sum = 0.f;
+  int my_id = -1;
+  for (int j = 0; j < A.k; ++j) {
+    uint64_t best = 0;
+    float p = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint64_t c = key[i] ? ((uint64_t)key[i] << 32) | (uint32_t)(kMaxE - 1 - (i * 64 + lane)) : 0ull;
+      if (c > best) {
+        best = c;
+        p = z[i];
+      }
+    }
+    uint64_t win = best;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)win, d);
+      win = o > win ? o : win;
+    }
+    const bool found = win != 0;
+    const int id = found ? kMaxE - 1 - (int)(uint32_t)win : -1;
+    p = __shfl(p, id & 63);
+    if (!found) p = 0.f;
+    sum += p;
+    if (lane == j) {
+      mine = p;
+      my_id = id;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (found && i * 64 + lane == id) key[i] = 0u;
+  }
+  if (lane < A.k) {
+    const float den = A.renorm ? sum : all;
+    A.ids[(int64_t)t * A.k + lane] = my_id;
+    A.weights[(int64_t)t * A.k + lane] = my_id >= 0 ? mine / den : 0.f;
+  }
+}
+
+__device__ __forceinline__ void choose_any(const RouteArgs &A, int t) {
+  if (A.E <= 64)
+    choose<1>(A, t);
+  else if (A.E <= 256)
+    choose<4>(A, t);
+  else
+    choose<16>(A, t);
+}
+
+// The lanes whose id equals this lane's (id >= 0), by ballots over its bits.
+__device__ __forceinline__ unsigned long long same_id(int id) {
+  unsigned long long m = __ballot(id >= 0);
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
+    const unsigned long long v = __ballot((id >> b) & 1);
+    m &= (id >> b) & 1 ? v : ~v;
+  }
+  return m;
+}
+
+// The workgroup places the rows of tokens [t0, t1).  before[e]: rows of
+// expert e in earlier blocks; total[e]: in all blocks; both in LDS and both
+// given unless `alone` (then counted here).
+__device__ void place(const RouteArgs &A, int t0, int t1, int *cnt, int *start, int *total, bool alone, bool first) {
+  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
+  const int64_t n0 = (int64_t)t0 * A.k;
+  const int N = (t1 - t0) * A.k;
+  const int per = ((N + kWaves - 1) / kWaves + 63) & ~63;
+  const int lo = min(N, w * per), hi = min(N, lo + per);
+  for (int i = tid; i < kWaves * A.E; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  for (int i = lo; i < hi; i += 64) {
+    const int id = i + lane < hi ? A.ids[n0 + i + lane] : -1;
+    const unsigned long long m = same_id(id);
+    if (id >= 0 && (m & ((1ull << lane) - 1)) == 0) cnt[w * A.E + id] += __popcll(m);
+  }
+  __syncthreads();
+  if (alone) {
+    for (int e = tid; e < A.E; e += kThreads) {
+      int s = 0;
+      for (int q = 0; q < kWaves; ++q) s += cnt[q * A.E + e];
+      total[e] = s;
+      start[e] = 0;
+    }
+    __syncthreads();
+  }
+  // offsets: an exclusive scan of the totals by the first wave
+  __shared__ int s_sum;
+  if (w == 0) {
+    int base = 0;
+    for (int eb = 0; eb < A.E; eb += 64) {
+      const int e = eb + lane;
+      const int c = e < A.E ? total[e] : 0;
+      int inc = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(inc, d);
+        if (lane >= d) inc += v;
+      }
+      if (e < A.E) {
+        const int o = base + inc - c;
+        if (first) A.offsets[e] = o;
+        int at = o + start[e];
+        for (int q = 0; q < kWaves; ++q) {  // where each wave's rows begin
+          const int v = cnt[q * A.E + e];
+          cnt[q * A.E + e] = at;
+          at += v;
+        }
+      }
+      base += __shfl(inc, 63);
+    }
+    if (lane == 0) {
+      s_sum = base;
+      if (first) A.offsets[A.E] = base;
+    }
+  }
+  __syncthreads();
+  for (int i = lo; i < hi; i += 64) {
+    const int64_t at = n0 + i + lane;
+    const bool in = i + lane < hi;
+    const int id = in ? A.ids[at] : -1;
+    const unsigned long long m = same_id(id), less = m & ((1ull << lane) - 1);
+    int r = -1;
+    if (id >= 0) {
+      r = cnt[w * A.E + id] + __popcll(less);
+      A.token[r] = (int)(at / A.k);
+    }
+    if (in) A.row[at] = r;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0 && less == 0) cnt[w * A.E + id] += __popcll(m);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // places that no row took
+  const int64_t all = (int64_t)A.T * A.k;
+  for (int64_t i = s_sum + (int64_t)blockIdx.x * kThreads + tid; i < all; i += (int64_t)gridDim.x * kThreads)
+    A.token[i] = -1;
+}
+
+__global__ void __launch_bounds__(kThreads) k_route_one(RouteArgs A) {
+  extern __shared__ int sh[];  // cnt [16][E], start [E], total [E]
+  for (int t = threadIdx.x >> 6; t < A.T; t += kWaves) choose_any(A, t);
+  __threadfence_block();
+  __syncthreads();
+  place(A, 0, A.T, sh, sh + kWaves * A.E, sh + (kWaves + 1) * A.E, true, true);
+}
+
+__global__ void __launch_bounds__(kThreads) k_route_choose(RouteArgs A) {
+  extern __shared__ int sh[];  // [E]
+  const int t0 = blockIdx.x * A.tb, t1 = min(A.T, t0 + A.tb);
+  for (int e = threadIdx.x; e < A.E; e += kThreads) sh[e] = 0;
+  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kWaves) choose_any(A, t);
+  __threadfence_block();
+  __syncthreads();
+  const int64_t n0 = (int64_t)t0 * A.k;
+  for (int i = threadIdx.x; i < (t1 - t0) * A.k; i += kThreads) {
+    const int id = A.ids[n0 + i];
+    if (id >= 0) atomicAdd(&sh[id], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < A.E; e += kThreads) A.hist[(int64_t)blockIdx.x * A.E + e] = sh[e];
+}
+
+__global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs A) {
+  extern __shared__ int sh[];
+  int *start = sh + kWaves * A.E, *total = start + A.E;
+  const int b = blockIdx.x, nb = gridDim.x;
+  for (int e = threadIdx.x; e < A.E; e += kThreads) start[e] = total[e] = 0;
+  __syncthreads();
+  const int ng = max(1, kThreads / A.E), e0 = threadIdx.x % A.E, gq = threadIdx.x / A.E;
+  if (gq < ng) {
+    int before = 0, all = 0;
+    for (int q = gq; q < nb; q += ng) {
+      const int v = A.hist[(int64_t)q * A.E + e0];
+      all += v;
+      if (q < b) before += v;
+    }
+    atomicAdd(&start[e0], before);
+    atomicAdd(&total[e0], all);
+  }
+  __syncthreads();
+  const int t0 = b * A.tb;
+  place(A, t0, min(A.T, t0 + A.tb), sh, start, total, false, b == 0);
+}
+
+// ------------------------------------------------------------- combining
+// out[t] = residual[t] + sum_j weights[t, j] y[row[t, j]] in the order of j,
+// fp32, rounded once.  Bound by reading y and writing out.  A thread takes V
+// neighbouring columns (16 bytes of y) of one token.
+struct CombineArgs {
+  const uint16_t *y;
+  const int *row;
+  const float *weights;
+  const void *res;
+  void *out;
+  int64_t ldy, ldr, ldo, width;
+  int y_rows, T, k, f32, nb;  // nb: workgroups per token
+};
+
+template <int V>
+__global__ void __launch_bounds__(256) k_route_combine(CombineArgs A) {
+  const int t = blockIdx.x / A.nb, c = ((blockIdx.x - t * A.nb) * 256 + threadIdx.x) * V;
+  if (c >= A.width) return;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int j = 0; j < A.k; ++j) {
+    const int r = A.row[(int64_t)t * A.k + j];
+    if (r < 0 || r >= A.y_rows) continue;
+    const float w = A.weights[(int64_t)t * A.k + j];
+    const uint16_t *src = A.y + (int64_t)r * A.ldy + c;
+    if constexpr (V == 8) {
+      const uint4 q = *reinterpret_cast<const uint4 *>(src);
+      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * i] = fmaf(w, h2f((uint16_t)(u[i] & 0xffffu)), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w, h2f((uint16_t)(u[i] >> 16)), acc[2 * i + 1]);
+      }
+    } else {
+      acc[0] = fmaf(w, h2f(*src), acc[0]);
+    }
+  }
+  const int64_t ro = (int64_t)t * A.ldr + c, oo = (int64_t)t * A.ldo + c;
+  if constexpr (V == 8) {
+    if (A.f32) {
+      if (A.res) {
+        const float4 *r = reinterpret_cast<const float4 *>((const float *)A.res + ro);
+        const float4 r0 = r[0], r1 = r[1];
+        acc[0] += r0.x; acc[1] += r0.y; acc[2] += r0.z; acc[3] += r0.w;
+        acc[4] += r1.x; acc[5] += r1.y; acc[6] += r1.z; acc[7] += r1.w;
+      }
+      float4 *o = reinterpret_cast<float4 *>((float *)A.out + oo);
+      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      return;
+    }
+    if (A.res) {
+      const uint4 q = *reinterpret_cast<const uint4 *>((const uint16_t *)A.res + ro);
+      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[2 * i] += h2f((uint16_t)(u[i] & 0xffffu));
+        acc[2 * i + 1] += h2f((uint16_t)(u[i] >> 16));
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = __half_as_ushort(__float2half_rn(acc[2 * i])) |
+             ((uint32_t)__half_as_ushort(__float2half_rn(acc[2 * i + 1])) << 16);
+    *reinterpret_cast<uint4 *>((uint16_t *)A.out + oo) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else if (A.f32) {
+    ((float *)A.out)[oo] = acc[0] + (A.res ? ((const float *)A.res)[ro] : 0.f);
+  } else {
+    ((uint16_t *)A.out)[oo] =
+        __half_as_ushort(__float2half_rn(acc[0] + (A.res ? h2f(((const uint16_t *)A.res)[ro]) : 0.f)));
+  }
+}
+
+// ------------------------------------------------------------------ host
+int tokens_per_block(int64_t T) { return (int)std::max<int64_t>(kOneBlock, (T + kBlocks - 1) / kBlocks); }
+
+lb_status route_sizes(int64_t tokens, int experts, int k, const char *who) {
+  const std::string pre = std::string(who) + ": ";
+  if (experts < 1 || experts > kMaxE) return set_error(LB_EINVAL, pre + "need 1 to 1024 experts");
+  if (k < 1 || k > kMaxK || k > experts) return set_error(LB_EINVAL, pre + "need 1 <= k <= min(64, experts)");
+  if (tokens < 0 || tokens > kMaxRows / k) return set_error(LB_EINVAL, pre + "tokens * k must be in [0, 2^30]");
+  return LB_OK;
+}
+
+}  // namespace
+
+extern "C" lb_status lb_route_ws_bytes(int64_t tokens, int experts, int k, uint64_t *bytes) {
+  if (!bytes) return set_error(LB_EINVAL, "lb_route_ws_bytes: NULL output");
+  const lb_status st = route_sizes(tokens, experts, k, "lb_route_ws_bytes");
+  if (st != LB_OK) return st;
+  const int tb = tokens_per_block(tokens);
+  *bytes = tokens <= kOneBlock ? 0 : (uint64_t)((tokens + tb - 1) / tb) * experts * 4;
+  return LB_OK;
+}
+
+extern "C" lb_status lb_route(const void *logits, int logits_type, int64_t ld, int64_t tokens, int experts, int k,
+                              int renormalise, int32_t *ids, float *weights, int32_t *offsets, int32_t *token,
+                              int32_t *row, void *ws, uint64_t ws_bytes, void *stream) {
+  uint64_t need = 0;
+  lb_status st = route_sizes(tokens, experts, k, "lb_route");
+  if (st == LB_OK) st = lb_route_ws_bytes(tokens, experts, k, &need);
+  if (st != LB_OK) return st;
+  if (logits_type != LB_F16 && logits_type != LB_F32)
+    return set_error(LB_EINVAL, "lb_route: logits_type must be LB_F16 or LB_F32");
+  if (!offsets || (tokens && (!logits || !ids || !weights || !token || !row)))
+    return set_error(LB_EINVAL, "lb_route: NULL argument");
+  if (ld < experts) return set_error(LB_EINVAL, "lb_route: the row stride is smaller than the row");
+  if (ws_bytes < need || (need && !ws))
+    return set_error(LB_EINVAL, "lb_route: workspace too small (needs " + std::to_string(need) + " bytes)");
+  if ((uintptr_t)logits % (logits_type == LB_F32 ? 4 : 2) ||
+      ((uintptr_t)ids | (uintptr_t)weights | (uintptr_t)offsets | (uintptr_t)token | (uintptr_t)row | (uintptr_t)ws) % 4)
+    return set_error(LB_EINVAL, "lb_route: misaligned pointer");
+  RouteArgs A = {};
+  A.logits = logits;
+  A.ld = ld;
+  A.T = (int)tokens; A.E = experts; A.k = k;
+  A.renorm = renormalise != 0;
+  A.f32 = logits_type == LB_F32;
+  A.tb = tokens_per_block(tokens);
+  A.ids = ids; A.weights = weights; A.offsets = offsets; A.token = token; A.row = row;
+  A.hist = (int *)ws;
+  const size_t lds = (size_t)(kWaves + 2) * experts * 4;
+  hipStream_t s = (hipStream_t)stream;
+  if (lds > 65536) {
+    hipError_t e = hipFuncSetAttribute((const void *)k_route_one, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e == hipSuccess)
+      e = hipFuncSetAttribute((const void *)k_route_place, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_route: ") + hipGetErrorString(e));
+  }
+  if (tokens <= kOneBlock) {
+    k_route_one<<<dim3(1), dim3(kThreads), lds, s>>>(A);
+  } else {
+    const dim3 grid((unsigned)((tokens + A.tb - 1) / A.tb));
+    k_route_choose<<<grid, dim3(kThreads), (size_t)experts * 4, s>>>(A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_route: ") + hipGetErrorString(e));
+    k_route_place<<<grid, dim3(kThreads), lds, s>>>(A);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_route: ") + hipGetErrorString(e));
+  return LB_OK;
+}
+
+extern "C" lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy, const int32_t *row,
+                                      const float *weights, int64_t tokens, int k, int64_t width,
+                                      const void *residual, int64_t ldr, void *out, int64_t ldo, int out_type,
+                                      void *stream) {
+  if (out_type != LB_F16 && out_type != LB_F32)
+    return set_error(LB_EINVAL, "lb_route_combine: out_type must be LB_F16 or LB_F32");
+  if (k < 1 || k > kMaxK) return set_error(LB_EINVAL, "lb_route_combine: need 1 <= k <= 64");
+  if (tokens < 0 || tokens > kMaxRows / k || y_rows < 0 || y_rows > kMaxRows)
+    return set_error(LB_EINVAL, "lb_route_combine: tokens * k and y_rows must be in [0, 2^30]");
+  if (width < 1 || width > (1 << 24)) return set_error(LB_EINVAL, "lb_route_combine: need 1 <= width <= 2^24");
+  if (tokens == 0) return LB_OK;
+  if (!row || !weights || !out || (y_rows && !y)) return set_error(LB_EINVAL, "lb_route_combine: NULL argument");
+  if ((y_rows && ldy < width) || ldo < width || (residual && ldr < width))
+    return set_error(LB_EINVAL, "lb_route_combine: a row stride is smaller than the row");
+  const int64_t most = (int64_t)1 << 31;
+  if (ldy > most || ldo > most || ldr > most)
+    return set_error(LB_EINVAL, "lb_route_combine: a row stride exceeds 2^31");
+  const int os = out_type == LB_F32 ? 4 : 2;
+  if ((uintptr_t)y % 2 || ((uintptr_t)row | (uintptr_t)weights) % 4 || ((uintptr_t)out | (uintptr_t)residual) % os)
+    return set_error(LB_EINVAL, "lb_route_combine: misaligned pointer");
+  const size_t on = (size_t)((tokens - 1) * ldo + width) * os;
+  if ((y_rows && overlaps(y, (size_t)((y_rows - 1) * ldy + width) * 2, out, on)) ||
+      overlaps(row, (size_t)tokens * k * 4, out, on) || overlaps(weights, (size_t)tokens * k * 4, out, on))
+    return set_error(LB_EINVAL, "lb_route_combine: an input and out overlap");
+  if (residual && !(residual == out && ldr == ldo) &&
+      overlaps(residual, (size_t)((tokens - 1) * ldr + width) * os, out, on))
+    return set_error(LB_EINVAL, "lb_route_combine: residual and out overlap (they may be the same rows)");
+  CombineArgs A = {};
+  A.y = (const uint16_t *)y;
+  A.row = row;
+  A.weights = weights;
+  A.res = residual;
+  A.out = out;
+  A.ldy = ldy; A.ldr = ldr; A.ldo = ldo; A.width = width;
+  A.y_rows = (int)y_rows; A.k = k;
+  A.f32 = out_type == LB_F32;
+  const int wide = A.f32 ? 4 : 8;
+  const bool vec = width % 8 == 0 && ldy % 8 == 0 && (uintptr_t)y % 16 == 0 && ldo % wide == 0 &&
+                   (uintptr_t)out % 16 == 0 && (!residual || (ldr % wide == 0 && (uintptr_t)residual % 16 == 0));
+  const int per = vec ? 2048 : 256;
+  A.nb = (int)((width + per - 1) / per);
+  // windows of tokens keep the grid below 2^31 threads
+  const int64_t window = std::max<int64_t>(1, (int64_t)0x7fffffff / 256 / A.nb);
+  for (int64_t t0 = 0; t0 < tokens; t0 += window) {
+    CombineArgs W = A;
+    const int64_t n = std::min(window, tokens - t0);
+    W.T = (int)n;
+    W.row += t0 * k;
+    W.weights += t0 * k;
+    W.out = (char *)out + (size_t)t0 * ldo * os;
+    if (residual) W.res = (const char *)residual + (size_t)t0 * ldr * os;
+    if (vec)
+      k_route_combine<8><<<dim3((unsigned)(n * A.nb)), dim3(256), 0, (hipStream_t)stream>>>(W);
+    else
+      k_route_combine<1><<<dim3((unsigned)(n * A.nb)), dim3(256), 0, (hipStream_t)stream>>>(W);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_route_combine: ") + hipGetErrorString(e));
+  }
+  return LB_OK;
+}

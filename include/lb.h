@@ -69,6 +69,7 @@ extern "C" {
 
 typedef struct lb_layer lb_layer; /* opaque, library-owned */
 typedef struct lb_stack lb_stack; /* opaque, library-owned */
+typedef struct lb_bank lb_bank;   /* opaque, library-owned */
 
 typedef enum {
   LB_OK = 0,
@@ -373,6 +374,119 @@ lb_status lb_stack_test_delay(lb_stack *S, uint32_t seed, uint32_t max_ticks);
 lb_status lb_stack_set_mode(lb_stack *S, int mode);
 
 lb_status lb_stack_destroy(lb_stack *S);
+
+/* --------------------------------------------------------------- banks */
+/* A bank is n layers of one shape (a, b, s, paths) on one device, each with
+ * or without a gate layer of that shape.  It computes, for rows x of fp16,
+ *
+ *     y = act(L(x) + bias) + residual                      without gates
+ *     y = act(G(x) + gate_bias) * (L(x) + bias) + residual     with gates
+ *
+ * for one of its layers (lb_bank_forward) or for rows sorted by layer, each
+ * run of rows with its own (lb_bank_grouped: the experts of a mixture).
+ * Accumulation is fp32 and the latent vector keeps 22 bits, at every row
+ * count; y is rounded once.  (|l_k t_k| must stay below 65504, fp16's
+ * largest number, or y is not finite.)
+ *
+ * Layers stay owned by the caller and must outlive the bank; their signs
+ * and scales must be set before lb_bank_create, which builds their
+ * matrix-core sign copies (as lb_prepare), allocates and synchronises the
+ * device.  Later lb_pack_signs and lb_set_scales calls on them are seen by
+ * later forwards.  A layer may appear more than once.
+ *
+ * The bank's calls share its workspace (the latent rows, at most 256 MB or
+ * one 64-row slot; longer calls run in windows): order them on one stream.
+ * They launch kernels only, unless a call has more rows than were reserved
+ * or used before: then the workspace grows (allocates without
+ * synchronising; the old one is retired, not freed, until lb_bank_destroy),
+ * or, under capture, the call returns LB_ENOTREADY.                      */
+
+/* Element types of y, residual and logits. */
+typedef enum { LB_F16 = 0, LB_F32 = 1 } lb_type;
+
+/* Activations; GELU is v/2 (1 + erf(v / sqrt 2)), GELU_TANH its tanh form
+ * v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))), SILU v / (1 + exp(-v)). */
+typedef enum {
+  LB_ACT_NONE = 0,
+  LB_ACT_RELU = 1,
+  LB_ACT_GELU = 2,
+  LB_ACT_GELU_TANH = 3,
+  LB_ACT_SILU = 4
+} lb_act;
+
+/* A bank of layers[0..n-1] (1 <= n <= 1024) with gates[0..n-1], or without
+ * gates when gates is NULL. */
+lb_status lb_bank_create(lb_layer *const *layers, lb_layer *const *gates, int n, lb_bank **out);
+
+/* Workspace for calls of up to `rows` rows, now. */
+lb_status lb_bank_reserve(lb_bank *B, int64_t rows);
+
+/* M rows through layer `expert` (0 for a bank of one).
+ *   x         device fp16, M x a, row stride ldx >= a elements
+ *   y         device, M x b of y_type (lb_type), row stride ldy >= b
+ *   bias, gate_bias   device fp16, n x b (row e belongs to layer e), or
+ *             NULL; a gate_bias needs a bank with gates
+ *   residual  device, M x b of y_type, row stride ldr >= b, or NULL; it may
+ *             be y itself with the same stride (y is then added to)
+ * Pointers need the alignment of their elements only; rows whose pointers,
+ * strides and widths are multiples of 16 bytes are read and written in
+ * 16-byte pieces (faster).  y must not overlap the other arrays.  M = 0 is
+ * a no-op; M <= 2^30. */
+lb_status lb_bank_forward(lb_bank *B, int expert, const void *x, int64_t ldx, void *y, int64_t ldy,
+                          int y_type, int64_t M, int act, const void *bias, const void *gate_bias,
+                          const void *residual, int64_t ldr, void *stream);
+
+/* Rows offsets[e] .. offsets[e + 1] - 1 of y through layer e, for every e.
+ *   offsets   device int32, n + 1 non-decreasing values in [0, rows]; an
+ *             empty run is a layer without rows.  Read on the device only.
+ *             Rows of y outside [offsets[0], offsets[n]) are left as they
+ *             were.  (Values out of range are clamped to it; with decreasing
+ *             ones the rows concerned are undefined.)
+ *   index     device int32, `rows` values: row i reads x row index[i] (a
+ *             row may be read any number of times), or NULL: row i of x.  An
+ *             index outside [0, x_rows) reads a row of zeros.
+ * The other arguments are as in lb_bank_forward, residual and y by row. */
+lb_status lb_bank_grouped(lb_bank *B, const void *x, int64_t x_rows, int64_t ldx, const int32_t *index,
+                          const int32_t *offsets, int64_t rows, void *y, int64_t ldy, int y_type,
+                          int act, const void *bias, const void *gate_bias, const void *residual,
+                          int64_t ldr, void *stream);
+
+lb_status lb_bank_destroy(lb_bank *B);
+
+/* ------------------------------------------------------------- routing */
+/* Choose k of `experts` layers (1 <= k <= min(64, experts), experts <= 1024)
+ * for every token and sort the chosen rows by expert, on the current device:
+ *   logits    device fp16 or fp32 (logits_type), tokens x experts, row
+ *             stride ld >= experts.  NaN counts as -inf.
+ *   ids       tokens x k: the experts with the largest logits, largest
+ *             first, equal ones by the lowest number.  Experts at -inf are
+ *             never chosen: a choice without one has id -1, row -1, weight 0
+ *   weights   tokens x k: softmax probabilities (fp32) of the choices, over
+ *             all experts, or over the token's choices when renormalise
+ *   offsets   experts + 1: where each expert's rows begin (for
+ *             lb_bank_grouped); offsets[experts] rows in all
+ *   token     tokens * k: the token of every row (lb_bank_grouped's index);
+ *             an expert's rows are in the order of the tokens.  -1 behind
+ *             the last row
+ *   row       tokens x k: the row of every choice
+ * ws is device scratch of at least lb_route_ws_bytes bytes (none for 64
+ * tokens or fewer), not shared with calls that may run at the same time.  Only
+ * launches kernels; with no tokens it writes offsets alone. */
+lb_status lb_route_ws_bytes(int64_t tokens, int experts, int k, uint64_t *bytes);
+lb_status lb_route(const void *logits, int logits_type, int64_t ld, int64_t tokens, int experts, int k,
+                   int renormalise, int32_t *ids, float *weights, int32_t *offsets, int32_t *token,
+                   int32_t *row, void *ws, uint64_t ws_bytes, void *stream);
+
+/* out[t] = residual[t] + sum_j weights[t, j] * y[row[t, j]] (fp32, in the
+ * order of j, rounded once), on the current device.  y is fp16, y_rows x
+ * width; row and weights are tokens x k (k <= 64); residual (or NULL) and
+ * out are of out_type; ldy, ldr and ldo are row strides.  Rows outside
+ * [0, y_rows) add nothing.  residual may be out itself with the same
+ * stride; out must not overlap the other arrays. */
+lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy, const int32_t *row,
+                           const float *weights, int64_t tokens, int k, int64_t width,
+                           const void *residual, int64_t ldr, void *out, int64_t ldo, int out_type,
+                           void *stream);
 
 /* ---------------------------------------------------------- diagnostics */
 const char *lb_status_str(lb_status st);
