@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <new>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "lb_internal.h"
@@ -54,10 +55,17 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
+// Pointers read from memory say themselves that they are global: through
+// generic ones every load would count as an LDS access too and be waited for
+// by the next LDS read.
+typedef const uint32_t __attribute__((address_space(1))) *gu32;
+typedef const uint16_t __attribute__((address_space(1))) *gu16;
+typedef const u32x4 __attribute__((address_space(1))) *gu128;
+
 // One layer of the bank: its matrix-core sign copies and scales.
 struct LayerDesc {
-  const uint32_t *sv, *su;
-  const uint16_t *g, *l, *h;
+  gu32 sv, su;
+  gu16 g, l, h;
 };
 
 struct BankArgs {
@@ -76,6 +84,8 @@ struct BankArgs {
   int tm, slot0;  // rows per slot, first slot of this launch
   int act, f32, xvec, yvec;
 };
+
+#define LB_G(T, p) ((T)(uintptr_t)(p))
 
 __device__ __forceinline__ float h2f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
 __device__ __forceinline__ uint16_t f2h(float v) { return __half_as_ushort(__float2half_rn(v)); }
@@ -146,14 +156,12 @@ __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, i
 template <bool XV>
 __device__ __forceinline__ u32x4 load_x(const BankArgs &A, const uint16_t *row, bool ok, int i) {
   if constexpr (XV) {
-    const void *src = ok && i < A.a ? (const void *)(row + i) : A.zero;
-    return *reinterpret_cast<const u32x4 *>(src);
+    return *LB_G(gu128, ok && i < A.a ? (const void *)(row + i) : A.zero);
   } else {
     uint32_t v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint16_t *src = ok && i + e < A.a ? row + i + e : (const uint16_t *)A.zero;
-      v[e] = *src;
+      v[e] = *LB_G(gu16, ok && i + e < A.a ? (const void *)(row + i + e) : A.zero);
     }
     u32x4 o;
     o.x = v[0] | (v[1] << 16);
@@ -191,8 +199,8 @@ k_bank_first(BankArgs A) {
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   const int k = ct * 32 + lr;
   const bool cval = k < A.s;
-  const uint32_t *bw = D.sv + (size_t)p * A.s + k;
-  const uint16_t *g = D.g + (size_t)p * A.a16;
+  const gu32 bw = D.sv + (size_t)p * A.s + k;
+  const gu16 g = D.g + (size_t)p * A.a16;
   bool rv = lr < n;
   int64_t r = row0 + lr;
   if (A.index && rv) {
@@ -211,11 +219,11 @@ k_bank_first(BankArgs A) {
     for (int u = 0; u < kN1U; ++u) {
       const int c = c0 + u * kN1Waves;
       const bool ok = c < A.R1;
-      wd[u] = *(ok && cval ? bw + (size_t)c * A.L : (const uint32_t *)A.zero);
+      wd[u] = *(ok && cval ? bw + (size_t)c * A.L : LB_G(gu32, A.zero));
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const int i = c * 32 + st * 16 + lh * 8;
-        gv[u][st] = *reinterpret_cast<const u32x4 *>(i < A.a16 ? (const void *)(g + i) : A.zero);
+        gv[u][st] = *(i < A.a16 ? (gu128)(g + i) : LB_G(gu128, A.zero));
         xv[u][st] = load_x<XV>(A, xr, rv, i);
       }
     }
@@ -251,16 +259,291 @@ k_bank_first(BankArgs A) {
   }
 }
 
-// ------------------------------------------------------ second product
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case LB_ACT_RELU: return v > 0.f || v != v ? v : 0.f;
-    case LB_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    // 1 + tanh(u) = 2 / (1 + exp(-2u)): no cancellation for negative u
-    case LB_ACT_GELU_TANH: return v / (1.f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-    case LB_ACT_SILU: return v / (1.f + expf(-v));
-    default: return v;
+// Workgroup barrier for LDS alone: global loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Many rows: a workgroup of 8 waves computes 32 RT rows x 32 CT columns of one
+// segment over the whole input dimension, wave w on the blocks of 64 inputs
+// w, w + 8, ...  A wave shares its x values with no other, so it stages them
+// itself, without barriers: rows as whole 128-byte lines into registers one
+// block ahead, then through its own LDS into operand order (piece c of row r
+// in slot c ^ (r & 7): no bank conflicts either way), the block's g behind
+// them.  One expanded sign operand serves RT products.  The waves' sums are
+// added in wave order through LDS, 32 columns at a time.  The workgroups of
+// one slot run on one XCD (workgroup i runs on XCD i % 8) one after another,
+// so its x rows come from that XCD's L2 after the first.
+constexpr int kW1Waves = 8;
+template <int RT>
+constexpr int w1_stage() { return RT * 4096 + 128; }  // bytes per wave
+template <int RT>
+constexpr int w1_lds() {
+  return std::max(kW1Waves * w1_stage<RT>(), RT * (kW1Waves * 4096 + 4096));
+}
+
+template <int RT, int CT, bool XV>
+__global__ void __launch_bounds__(kW1Waves * 64)
+k_bank_first_wide(BankArgs A, int slots, int ncs) {
+  extern __shared__ __align__(16) unsigned char sm[];
+  const int ncg = A.G * A.P * ncs;
+  const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;
+  const int slot = (jj / ncg) * 8 + xcd, cg = jj % ncg;
+  int e, row0, n;
+  if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
+  const int seg = cg / ncs, ct0 = (cg - seg * ncs) * CT;
+  const int side = seg / A.P, p = seg - side * A.P;
+  const LayerDesc D = A.desc[side * A.E + e];
+
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  unsigned char *stage = sm + w * w1_stage<RT>();
+  const gu16 g = D.g + (size_t)p * A.a16;
+  const gu32 bw = D.sv + (size_t)p * A.s;  // uniform
+  unsigned col[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) col[ct] = min((ct0 + ct) * 32 + lr, A.s - 1);
+  // the lane's rows: 8 u + lane / 8, 16 bytes of each
+  const int piece = lane & 7;
+  int xrow[4 * RT];
+#pragma unroll
+  for (int u = 0; u < 4 * RT; ++u) {
+    const int r = 8 * u + (lane >> 3);
+    int v = r < n ? row0 + r : -1;
+    if (A.index && v >= 0) {
+      v = A.index[v];
+      if (v >= A.x_rows) v = -1;
+    }
+    xrow[u] = v;
   }
+
+  float16_t acc[RT][CT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
+
+  struct Block {
+    u32x4 x[4 * RT], g;
+    uint32_t wd[2][CT];
+  };
+  auto fetch = [&](int kb, Block &o) {
+    const int i = kb * 64 + piece * 8;
+#pragma unroll
+    for (int u = 0; u < 4 * RT; ++u)
+      o.x[u] = load_x<XV>(A, A.x + (int64_t)xrow[u] * A.ldx, xrow[u] >= 0, i);
+    o.g = *(i < A.a16 ? (gu128)(g + i) : LB_G(gu128, A.zero));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const gu32 row = bw + (size_t)min(2 * kb + h, A.R1 - 1) * A.L;  // past the end x and g are zero
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) o.wd[h][ct] = row[col[ct]];
+    }
+  };
+  const int nkb = (A.a + 63) >> 6;
+  if (w < nkb) {
+    Block c;
+    fetch(w, c);
+    for (int kb = w; kb < nkb; kb += kW1Waves) {
+      u32x4 *st = reinterpret_cast<u32x4 *>(stage);
+#pragma unroll
+      for (int u = 0; u < 4 * RT; ++u) {
+        const int r = 8 * u + (lane >> 3);
+        st[r * 8 + (piece ^ (r & 7))] = c.x[u];
+      }
+      if (lane < 8) st[RT * 256 + lane] = c.g;
+      uint32_t wd[2][CT];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) wd[h][ct] = c.wd[h][ct] << (4 * lh);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      fetch(min(kb + kW1Waves, nkb - 1), c);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const u32x4 gv = st[RT * 256 + 2 * t + lh];
+        u32x4 xv[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) xv[rt] = st[(rt * 32 + lr) * 8 + ((2 * t + lh) ^ (lr & 7))];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const half8_t b = flip(gv, wd[t >> 1][ct] << (8 * (t & 1)));
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            acc[rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(xv[rt]), b, acc[rt][ct], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  // sums over the waves and w = l t, a column tile at a time
+  float *red = reinterpret_cast<float *>(sm);                                       // [wave][rt][register][lane]
+  uint16_t *tl = reinterpret_cast<uint16_t *>(sm + RT * kW1Waves * 4096);           // [rt][2048]
+  const int nseg = A.G * A.P;
+  __syncthreads();
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int tile = ct0 + ct;
+    if (tile >= A.Wk) break;  // uniform
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) red[((w * RT + rt) * 16 + i) * 64 + lane] = acc[rt][ct][i];
+    __syncthreads();
+    const int k = tile * 32 + lr;
+    const float lk = k < A.s ? h2f(D.l[(size_t)p * ((A.s + 7) / 8 * 8) + k]) : 0.f;
+#pragma unroll
+    for (int q = 0; q < 2 * RT; ++q) {
+      const int idx = q * 512 + threadIdx.x, rt = idx >> 10, i = (idx >> 6) & 15;
+      float v = 0.f;
+#pragma unroll
+      for (int z = 0; z < kW1Waves; ++z) v += red[z * RT * 1024 + idx];
+      v = k < A.s ? v * lk : 0.f;
+      const int row = 8 * (i >> 2) + 4 * lh + (i & 3);
+      const int o = rt * 2048 + (lr >> 4) * 1024 + (((lr >> 3) & 1) * 32 + row) * 8 + (lr & 7);
+      const uint16_t hi = f2h(v);
+      const float hf = h2f(hi);
+      tl[o] = hi;
+      tl[o + 512] = isinf(hf) ? (uint16_t)0 : f2h((v - hf) * 2048.f);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < RT * 256; i += 512) {
+      const int rt = i >> 8;
+      u32x4 *dst = reinterpret_cast<u32x4 *>(A.T + (((size_t)(slot * RT + rt) * nseg + seg) * A.Wk + tile) * 2048);
+      dst[i & 255] = reinterpret_cast<const u32x4 *>(tl)[i];
+    }
+  }
+}
+
+// ------------------------------------------------------ second product
+// Activations in fp32 on the hardware's exp2 and reciprocal (a step of error
+// each): v / (1 + exp(-c)) takes six instructions, where expf and a division
+// take some forty, and a wave has 64 of them against 288 matrix products.
+__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == LB_ACT_RELU) {
+    return v > 0.f || v != v ? v : 0.f;
+  } else if constexpr (ACT == LB_ACT_GELU) {
+    // v/2 erfc(-v / sqrt 2), erfc by Abramowitz and Stegun 7.1.26 (within 1.5e-7)
+    const float z = fabsf(v) * 0.70710678118654752f;
+    const float t = rcp_hw(fmaf(0.3275911f, z, 1.f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f) * t * exp2_hw(-kLog2e * z * z);  // erfc(z)
+    return 0.5f * v * (v > 0.f ? 2.f - q : q);
+  } else if constexpr (ACT == LB_ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)): no cancellation for negative u
+    return v * rcp_hw(1.f + exp2_hw(-2.f * 0.79788456080286536f * kLog2e * fmaf(0.044715f * v * v, v, v)));
+  } else if constexpr (ACT == LB_ACT_SILU) {
+    return v * rcp_hw(1.f + exp2_hw(-kLog2e * v));
+  } else {
+    return v;
+  }
+}
+
+// Calls f with the activation as a compile-time constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+  switch (act) {
+    case LB_ACT_RELU: return f(std::integral_constant<int, LB_ACT_RELU>());
+    case LB_ACT_GELU: return f(std::integral_constant<int, LB_ACT_GELU>());
+    case LB_ACT_GELU_TANH: return f(std::integral_constant<int, LB_ACT_GELU_TANH>());
+    case LB_ACT_SILU: return f(std::integral_constant<int, LB_ACT_SILU>());
+    default: return f(std::integral_constant<int, LB_ACT_NONE>());
+  }
+}
+
+template <int CT>
+constexpr int pitch2() { return 32 * CT + 4; }
+
+// The epilogue of one 32-row tile (rows 32 rt .. of the slot) and 32 CT columns
+// from j0 on: up and gate hold the wave's accumulators (gate unused unless
+// G = 2), lds 32 x (32 CT + 4) floats of the wave's own.
+template <int G, int CT>
+__device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n, int rt, int j0,
+                                       const float16_t (&up)[CT], const float16_t (&gate)[CT], float *lds) {
+  constexpr int kPitch = pitch2<CT>();
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  float bu[CT], bg[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int j = j0 + ct * 32 + lr;
+    bu[ct] = A.bias[0] && j < A.b ? h2f(A.bias[0][(size_t)e * A.b + j]) : 0.f;
+    bg[ct] = G == 2 && A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
+  }
+  with_act(A.act, [&](auto act) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float v = up[ct][i] + bu[ct];
+        if constexpr (G == 2)
+          v = activate<decltype(act)::value>(gate[ct][i] + bg[ct]) * v;
+        else
+          v = activate<decltype(act)::value>(v);
+        lds[(8 * (i >> 2) + 4 * lh + (i & 3)) * kPitch + ct * 32 + lr] = v;
+      }
+  });
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int u = 0; u < 2 * CT; ++u) {
+    const int at = u * 64 + lane, row = at / (4 * CT), c8 = at % (4 * CT);
+    const int j = j0 + c8 * 8, rr = rt * 32 + row;
+    if (rr >= n || j >= A.b) continue;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lds[row * kPitch + c8 * 8 + i];
+    const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
+    if (A.yvec && j + 8 <= A.b) {
+      if (A.f32) {
+        if (A.res) {
+          const float4 r0 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[0];
+          const float4 r1 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[1];
+          v[0] += r0.x; v[1] += r0.y; v[2] += r0.z; v[3] += r0.w;
+          v[4] += r1.x; v[5] += r1.y; v[6] += r1.z; v[7] += r1.w;
+        }
+        float4 *dst = reinterpret_cast<float4 *>((float *)A.y + yo);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        if (A.res) {
+          const u32x4 r = *reinterpret_cast<const u32x4 *>((const uint16_t *)A.res + ro);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] += h2f((uint16_t)(r[i] & 0xffffu));
+            v[2 * i + 1] += h2f((uint16_t)(r[i] >> 16));
+          }
+        }
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = f2h(v[2 * i]) | ((uint32_t)f2h(v[2 * i + 1]) << 16);
+        *reinterpret_cast<u32x4 *>((uint16_t *)A.y + yo) = o;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (j + i >= A.b) break;
+        if (A.f32) {
+          ((float *)A.y)[yo + i] = v[i] + (A.res ? ((const float *)A.res)[ro + i] : 0.f);
+        } else {
+          ((uint16_t *)A.y)[yo + i] = f2h(v[i] + (A.res ? h2f(((const uint16_t *)A.res)[ro + i]) : 0.f));
+        }
+      }
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // A workgroup of 4 waves, each 32 RT rows of one slot x 32 CT outputs of all G
@@ -268,9 +551,6 @@ __device__ __forceinline__ float activate(float v, int act) {
 // word per column and 32 latent columns); the workgroups of a slot lie side
 // by side.  The epilogue turns each 32-row tile through the wave's own LDS,
 // so that residual loads and y stores are whole 16-byte pieces of rows.
-template <int CT>
-constexpr int pitch2() { return 32 * CT + 4; }
-
 template <int G, int RT, int CT>
 __global__ void __launch_bounds__(256)
 k_bank_second(BankArgs A) {
@@ -352,79 +632,141 @@ k_bank_second(BankArgs A) {
     }
   }
 
-  // epilogue
-  float bu[CT], bg[CT];
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int j = j0 + ct * 32 + lr;
-    bu[ct] = A.bias[0] && j < A.b ? h2f(A.bias[0][(size_t)e * A.b + j]) : 0.f;
-    bg[ct] = G == 2 && A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
-  }
   float *lds = smem + w * 32 * kPitch;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (rt * 32 >= n) break;
+  for (int rt = 0; rt < RT; ++rt)
+    if (rt * 32 < n) finish<G, CT>(A, e, row0, n, rt, j0, acc[0][rt], acc[G - 1][rt], lds);
+}
+
+// Many rows: a workgroup of 4 waves, 64 rows of one slot, every wave 32 CT
+// columns of all G sides.  The slot's T goes through LDS in chunks of 64
+// latent columns (16 KB, two buffers, the next chunk's values in registers
+// meanwhile), where one operand read serves CT expanded sign operands and
+// one of those two row tiles, hi and lo.
+constexpr int kW2It = 2;  // 32-column words per chunk
+
+template <int G, int CT>
+__global__ void __launch_bounds__(256, 2)
+k_bank_second_wide(BankArgs A, int slots) {
+  constexpr int kPitch = 68, kChunk = 2 * kW2It * 256;  // chunk in 16-byte pieces
+  extern __shared__ __align__(16) unsigned char sm[];
+  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
+  const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;  // a slot's workgroups on one XCD, as in the first product
+  const int slot = (jj / ncb) * 8 + xcd, cb = jj % ncb;
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  const int j0 = (cb * 4 + w) * 32 * CT;
+  int e, row0, n;
+  if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
+
+  const int nit = A.P * A.Wk, nch = (A.Wk + kW2It - 1) / kW2It;  // chunks per path
+  float16_t acc[G][2][CT];
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+  for (int q = 0; q < G; ++q)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float v = acc[0][rt][ct][i] + bu[ct];
-        if constexpr (G == 2)
-          v = activate(acc[G - 1][rt][ct][i] + bg[ct], A.act) * v;
-        else
-          v = activate(v, A.act);
-        lds[(8 * (i >> 2) + 4 * lh + (i & 3)) * kPitch + ct * 32 + lr] = v;
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[q][rt][ct][i] = 0.f;
+  int jc[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) jc[ct] = min(j0 + ct * 32 + lr, A.b16 - 1);
+
+  u32x4 *buf = reinterpret_cast<u32x4 *>(sm);
+  const u32x4 *tb = reinterpret_cast<const u32x4 *>(A.T) + (size_t)slot * 2 * G * nit * 256 + threadIdx.x;
+  u32x4 tn[2 * kW2It];
+  uint32_t wn[kW2It][CT];
+  // chunk c of path pp, side q
+  auto fetch = [&](int q, int pp, int c, gu32 su) {
+#pragma unroll
+    for (int i = 0; i < kW2It; ++i) {
+      const int it = pp * A.Wk + min(c * kW2It + i, A.Wk - 1);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) tn[rt * kW2It + i] = tb[(size_t)((rt * G + q) * nit + it) * 256];
+      const gu32 row = su + (size_t)it * A.b16;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) wn[i][ct] = row[jc[ct]];
+    }
+  };
+  uint16_t hn[CT];
+  auto fetch_h = [&](gu16 h) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) hn[ct] = h[jc[ct]];
+  };
+  fetch_h(A.desc[e].h);
+  fetch(0, 0, 0, A.desc[e].su);
+  int turn = 0;
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const LayerDesc D = A.desc[q * A.E + e];
+    for (int pp = 0; pp < A.P; ++pp) {
+      uint32_t hh[CT], hl[CT];  // the path's h (and 2^-11 h): two copies per register
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint16_t h = hn[ct];
+        const uint16_t hs = f2h(h2f(h) * 0x1p-11f);
+        hh[ct] = h | ((uint32_t)h << 16);
+        hl[ct] = hs | ((uint32_t)hs << 16);
       }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+      if (pp + 1 < A.P)
+        fetch_h(D.h + A.b16);
+      else if (q + 1 < G)
+        fetch_h(A.desc[(q + 1) * A.E + e].h);
+      for (int c = 0; c < nch; ++c, turn ^= 1) {
+        u32x4 *b = buf + turn * kChunk;
+        uint32_t wd[kW2It][CT];
 #pragma unroll
-    for (int u = 0; u < 2 * CT; ++u) {
-      const int at = u * 64 + lane, row = at / (4 * CT), c8 = at % (4 * CT);
-      const int j = j0 + c8 * 8, rr = rt * 32 + row;
-      if (rr >= n || j >= A.b) continue;
-      float v[8];
+        for (int i = 0; i < 2 * kW2It; ++i) b[i * 256 + threadIdx.x] = tn[i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = lds[row * kPitch + c8 * 8 + i];
-      const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
-      if (A.yvec && j + 8 <= A.b) {
-        if (A.f32) {
-          if (A.res) {
-            const float4 r0 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[0];
-            const float4 r1 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[1];
-            v[0] += r0.x; v[1] += r0.y; v[2] += r0.z; v[3] += r0.w;
-            v[4] += r1.x; v[5] += r1.y; v[6] += r1.z; v[7] += r1.w;
-          }
-          float4 *dst = reinterpret_cast<float4 *>((float *)A.y + yo);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-          if (A.res) {
-            const u32x4 r = *reinterpret_cast<const u32x4 *>((const uint16_t *)A.res + ro);
+        for (int i = 0; i < kW2It; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] += h2f((uint16_t)(r[i] & 0xffffu));
-              v[2 * i + 1] += h2f((uint16_t)(r[i] >> 16));
+          for (int ct = 0; ct < CT; ++ct) wd[i][ct] = wn[i][ct] << (4 * lh);
+        if (c + 1 < nch)
+          fetch(q, pp, c + 1, D.su);
+        else if (pp + 1 < A.P)
+          fetch(q, pp + 1, 0, D.su);
+        else if (q + 1 < G)
+          fetch(q + 1, 0, 0, A.desc[(q + 1) * A.E + e].su);
+        lds_barrier();
+        const int steps = (A.s - 32 * kW2It * c + 15) >> 4;  // blocks of 16 left in the path
+        u32x4 t[2][2][2];  // [turn][rt][plane], the next block's read during this one's products
+        auto read = [&](int st) {
+#pragma unroll
+          for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl)
+              t[st & 1][rt][pl] = b[(rt * kW2It + (st >> 1)) * 256 + ((st & 1) * 2 + pl) * 64 + lane];
+        };
+        read(0);
+#pragma unroll
+        for (int st = 0; st < 2 * kW2It; ++st) {
+          if (st >= steps) break;
+          if (st + 1 < 2 * kW2It) read(st + 1);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const uint32_t wl = wd[st >> 1][ct] << (8 * (st & 1));
+            const half8_t bh = flip(splat(hh[ct]), wl), bl = flip(splat(hl[ct]), wl);
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+              acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][0]), bh, acc[q][rt][ct], 0, 0, 0);
+              acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][1]), bl, acc[q][rt][ct], 0, 0, 0);
             }
-          }
-          u32x4 o;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = f2h(v[2 * i]) | ((uint32_t)f2h(v[2 * i + 1]) << 16);
-          *reinterpret_cast<u32x4 *>((uint16_t *)A.y + yo) = o;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (j + i >= A.b) break;
-          if (A.f32) {
-            ((float *)A.y)[yo + i] = v[i] + (A.res ? ((const float *)A.res)[ro + i] : 0.f);
-          } else {
-            ((uint16_t *)A.y)[yo + i] = f2h(v[i] + (A.res ? h2f(((const uint16_t *)A.res)[ro + i]) : 0.f));
           }
         }
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  float *lds = reinterpret_cast<float *>(sm) + w * 32 * kPitch;
+#pragma unroll
+  for (int rt = 0; rt < 2; ++rt) {
+    if (rt * 32 >= n) break;
+#pragma unroll
+    for (int cp = 0; cp < CT; cp += 2) {
+      const float16_t up[2] = {acc[0][rt][cp], acc[0][rt][cp + 1]};
+      const float16_t gate[2] = {acc[G - 1][rt][cp], acc[G - 1][rt][cp + 1]};
+      if (j0 + cp * 32 < A.b) finish<G, 2>(A, e, row0, n, rt, j0 + cp * 32, up, gate, lds);
+    }
   }
 }
 
@@ -503,6 +845,44 @@ hipError_t launch_second(const BankArgs &A, int slots, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int RT, int CT>
+hipError_t launch_first_wide(const BankArgs &A, int slots, int ncs, hipStream_t st) {
+  const dim3 grid((unsigned)((slots + 7) / 8 * 8 * A.G * A.P * ncs));
+  constexpr int lds = w1_lds<RT>();
+  const void *f = A.xvec ? (const void *)k_bank_first_wide<RT, CT, true> : (const void *)k_bank_first_wide<RT, CT, false>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  if (A.xvec)
+    k_bank_first_wide<RT, CT, true><<<grid, dim3(kW1Waves * 64), lds, st>>>(A, slots, ncs);
+  else
+    k_bank_first_wide<RT, CT, false><<<grid, dim3(kW1Waves * 64), lds, st>>>(A, slots, ncs);
+  return hipGetLastError();
+}
+
+// Column tiles per workgroup: a segment's tiles in the fewest groups of at
+// most five (160 of 256 registers are sums then), spread evenly.
+template <int RT>
+hipError_t launch_first_wide(const BankArgs &A, int slots, hipStream_t st) {
+  const int ncs = (A.Wk + 4) / 5;
+  switch ((A.Wk + ncs - 1) / ncs) {
+    case 1: return launch_first_wide<RT, 1>(A, slots, ncs, st);
+    case 2: return launch_first_wide<RT, 2>(A, slots, ncs, st);
+    case 3: return launch_first_wide<RT, 3>(A, slots, ncs, st);
+    case 4: return launch_first_wide<RT, 4>(A, slots, ncs, st);
+    default: return launch_first_wide<RT, 5>(A, slots, ncs, st);
+  }
+}
+
+template <int G, int CT>
+hipError_t launch_second_wide(const BankArgs &A, int slots, hipStream_t st) {
+  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
+  const size_t lds = std::max<size_t>(2 * 2 * kW2It * 4096, 4 * 32 * 68 * sizeof(float));
+  k_bank_second_wide<G, CT><<<dim3((unsigned)((slots + 7) / 8 * 8 * ncb)), dim3(256), lds, st>>>(A, slots);
+  return hipGetLastError();
+}
+
 lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   const Layer &Ly = B->first->ly;
   const int cus = device_info(B->first).cu_count > 0 ? device_info(B->first).cu_count : 256;
@@ -530,16 +910,19 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
     const int ns = (int)std::min<int64_t>(window, slots - s0);
     A.slot0 = (int)s0;
     const dim3 grid((unsigned)(ns * per * ntile));
-    if (A.xvec)
+    hipError_t e = hipSuccess;
+    if (big)
+      e = launch_first_wide<2>(A, ns, st);
+    else if (A.xvec)
       k_bank_first<true><<<grid, dim3(kN1Waves * 64), 0, st>>>(A);
     else
       k_bank_first<false><<<grid, dim3(kN1Waves * 64), 0, st>>>(A);
-    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = hipGetLastError();
     if (e == hipSuccess) {
       if (A.G == 1)
-        e = big ? launch_second<1, 2, 4>(A, ns, st) : launch_second<1, 1, 1>(A, ns, st);
+        e = big ? launch_second_wide<1, 4>(A, ns, st) : launch_second<1, 1, 1>(A, ns, st);
       else
-        e = big ? launch_second<2, 2, 2>(A, ns, st) : launch_second<2, 1, 1>(A, ns, st);
+        e = big ? launch_second_wide<2, 2>(A, ns, st) : launch_second<2, 1, 1>(A, ns, st);
     }
     if (e != hipSuccess) return set_error(LB_EHIP, std::string(who) + ": " + hipGetErrorString(e));
   }
@@ -619,7 +1002,7 @@ extern "C" lb_status lb_bank_create(lb_layer *const *layers, lb_layer *const *ga
       lb_bank_destroy(B);
       return st;
     }
-    desc[i] = {L->ly.sv1m, L->ly.su2m, L->ly.g, L->ly.l, L->ly.h};
+    desc[i] = {LB_G(gu32, L->ly.sv1m), LB_G(gu32, L->ly.su2m), LB_G(gu16, L->ly.g), LB_G(gu16, L->ly.l), LB_G(gu16, L->ly.h)};
   }
   hipError_t e = hipMalloc(&B->desc, desc.size() * sizeof(LayerDesc));
   if (e != hipSuccess) {
