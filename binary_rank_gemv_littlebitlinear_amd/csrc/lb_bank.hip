@@ -47,6 +47,15 @@
 
 #include "lb_internal.h"
 
+#ifndef SD1
+#define SD1 3
+#endif
+#ifndef SD2
+#define SD2 4
+#endif
+#ifndef SCT
+#define SCT 4
+#endif
 namespace {
 
 using namespace lbi;
@@ -266,28 +275,43 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Copies straight into LDS: lane i's 16 (4) bytes land at dst + 16 i (4 i).
+__device__ __forceinline__ void dma16(const void *src, void *dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(const void *src, void *dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 4, 0, 0);
+}
+// Waits until at most N of the wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // Many rows: a workgroup of 8 waves computes 32 RT rows x 32 CT columns of one
-// segment over the whole input dimension, wave w on the blocks of 64 inputs
-// w, w + 8, ...  A wave shares its x values with no other, so it stages them
-// itself, without barriers: rows as whole 128-byte lines into registers one
-// block ahead, then through its own LDS into operand order (piece c of row r
-// in slot c ^ (r & 7): no bank conflicts either way), the block's g behind
-// them.  One expanded sign operand serves RT products.  The waves' sums are
+// segment over the whole input dimension, wave w on the blocks of 32 inputs
+// 2 w, 2 w + 1, 2 w + 16, ... (pairs: whole 128-byte lines of x).  A wave
+// shares its operands with no other, so it stages them itself, without
+// barriers: x rows, the block's g and its columns' sign words are copied into
+// a ring of kW1Ring blocks in the wave's own LDS, all but one in flight (piece
+// c of row r in slot c ^ (r / 2) % 4, so that the operand reads meet no bank
+// twice).  One expanded sign operand serves RT products.  The waves' sums are
 // added in wave order through LDS, 32 columns at a time.  The workgroups of
 // one slot run on one XCD (workgroup i runs on XCD i % 8) one after another,
 // so its x rows come from that XCD's L2 after the first.
-constexpr int kW1Waves = 8;
-template <int RT>
-constexpr int w1_stage() { return RT * 4096 + 128; }  // bytes per wave
-template <int RT>
+constexpr int kW1Waves = 8, kW1Ring = 4;
+template <int RT, int CT>
+constexpr int w1_block() { return RT * 2048 + (CT + 1) / 2 * 256 + 64; }  // x, words, g
+template <int RT, int CT>
 constexpr int w1_lds() {
-  return std::max(kW1Waves * w1_stage<RT>(), RT * (kW1Waves * 4096 + 4096));
+  return std::max(kW1Waves * kW1Ring * w1_block<RT, CT>(), RT * (kW1Waves * 4096 + 4096));
 }
 
 template <int RT, int CT, bool XV>
 __global__ void __launch_bounds__(kW1Waves * 64)
 k_bank_first_wide(BankArgs A, int slots, int ncs) {
   extern __shared__ __align__(16) unsigned char sm[];
+  constexpr int kBlock = w1_block<RT, CT>(), kWords = RT * 2048, kG = kBlock - 64, kPer = 2 * RT + (CT + 1) / 2 + 1;
   const int ncg = A.G * A.P * ncs;
   const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;
   const int slot = (jj / ncg) * 8 + xcd, cg = jj % ncg;
@@ -298,18 +322,18 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
   const LayerDesc D = A.desc[side * A.E + e];
 
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  unsigned char *stage = sm + w * w1_stage<RT>();
+  unsigned char *ring = sm + w * kW1Ring * kBlock;
   const gu16 g = D.g + (size_t)p * A.a16;
   const gu32 bw = D.sv + (size_t)p * A.s;  // uniform
-  unsigned col[CT];
+  unsigned col[(CT + 1) / 2];              // the columns whose words the lane copies
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) col[ct] = min((ct0 + ct) * 32 + lr, A.s - 1);
-  // the lane's rows: 8 u + lane / 8, 16 bytes of each
-  const int piece = lane & 7;
-  int xrow[4 * RT];
+  for (int q = 0; q < (CT + 1) / 2; ++q) col[q] = min(ct0 * 32 + q * 64 + lane, A.s - 1);
+  // the lane's rows: 16 u + lane / 4, 16 bytes of each
+  const int piece = (lane & 3) ^ ((lane >> 3) & 3);
+  int xrow[2 * RT];
 #pragma unroll
-  for (int u = 0; u < 4 * RT; ++u) {
-    const int r = 8 * u + (lane >> 3);
+  for (int u = 0; u < 2 * RT; ++u) {
+    const int r = 16 * u + (lane >> 2);
     int v = r < n ? row0 + r : -1;
     if (A.index && v >= 0) {
       v = A.index[v];
@@ -326,60 +350,67 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
 
-  struct Block {
-    u32x4 x[4 * RT], g;
-    uint32_t wd[2][CT];
-  };
-  auto fetch = [&](int kb, Block &o) {
-    const int i = kb * 64 + piece * 8;
+  // the wave's block number i is block 16 (i / 2) + 2 w + i % 2 of the input
+  auto block_of = [&](int i) { return 16 * (i >> 1) + 2 * w + (i & 1); };
+  const int nblk = A.R1;
+  const int mine = max(0, (nblk - 2 * w + 15) / 16 * 2 - ((nblk - 2 * w) % 16 == 1 ? 1 : 0));
+  // copies block i of the wave (kPer loads)
+  auto issue = [&](int i) {
+    const int kb = block_of(i);
+    unsigned char *dst = ring + (i & (kW1Ring - 1)) * kBlock;
+    const int k0 = kb * 32 + piece * 8;
 #pragma unroll
-    for (int u = 0; u < 4 * RT; ++u)
-      o.x[u] = load_x<XV>(A, A.x + (int64_t)xrow[u] * A.ldx, xrow[u] >= 0, i);
-    o.g = *(i < A.a16 ? (gu128)(g + i) : LB_G(gu128, A.zero));
+    for (int u = 0; u < 2 * RT; ++u) {
+      const uint16_t *row = A.x + (int64_t)xrow[u] * A.ldx;
+      if constexpr (XV)
+        dma16(xrow[u] >= 0 && k0 < A.a ? (const void *)(row + k0) : A.zero, dst + u * 1024);
+      else
+        *reinterpret_cast<u32x4 *>(dst + u * 1024 + lane * 16) = load_x<false>(A, row, xrow[u] >= 0, k0);
+    }
+    const gu32 wrow = bw + (size_t)kb * A.L;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const gu32 row = bw + (size_t)min(2 * kb + h, A.R1 - 1) * A.L;  // past the end x and g are zero
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) o.wd[h][ct] = row[col[ct]];
+    for (int q = 0; q < (CT + 1) / 2; ++q) dma4((const void *)(wrow + col[q]), dst + kWords + q * 256);
+    if (lane < 4) {
+      const int i8 = kb * 32 + lane * 8;
+      dma16(i8 < A.a16 ? (const void *)(g + i8) : A.zero, dst + kG);
     }
   };
-  const int nkb = (A.a + 63) >> 6;
-  if (w < nkb) {
-    Block c;
-    fetch(w, c);
-    for (int kb = w; kb < nkb; kb += kW1Waves) {
-      u32x4 *st = reinterpret_cast<u32x4 *>(stage);
 #pragma unroll
-      for (int u = 0; u < 4 * RT; ++u) {
-        const int r = 8 * u + (lane >> 3);
-        st[r * 8 + (piece ^ (r & 7))] = c.x[u];
-      }
-      if (lane < 8) st[RT * 256 + lane] = c.g;
-      uint32_t wd[2][CT];
+  for (int i = 0; i < kW1Ring - 1; ++i)
+    if (i < mine) issue(i);
+  for (int i = 0; i < mine; ++i) {
+    // block i has landed; the later ones may be in flight
+    if (XV && i + 2 < mine)
+      wait_loads<2 * kPer>();
+    else if (XV && i + 1 < mine)
+      wait_loads<kPer>();
+    else
+      wait_loads<0>();
+    const unsigned char *blk = ring + (i & (kW1Ring - 1)) * kBlock;
+    const u32x4 *xs = reinterpret_cast<const u32x4 *>(blk);
+    const uint32_t *ws = reinterpret_cast<const uint32_t *>(blk + kWords);
+    const u32x4 *gs = reinterpret_cast<const u32x4 *>(blk + kG);
+    uint32_t wd[CT];
+    u32x4 gv[2], xv[2][RT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int t = 0; t < 2; ++t) {
+      gv[t] = gs[2 * t + lh];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) wd[h][ct] = c.wd[h][ct] << (4 * lh);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      fetch(min(kb + kW1Waves, nkb - 1), c);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const u32x4 gv = st[RT * 256 + 2 * t + lh];
-        u32x4 xv[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) xv[rt] = st[(rt * 32 + lr) * 8 + ((2 * t + lh) ^ (lr & 7))];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const half8_t b = flip(gv, wd[t >> 1][ct] << (8 * (t & 1)));
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            acc[rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(xv[rt]), b, acc[rt][ct], 0, 0, 0);
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      for (int rt = 0; rt < RT; ++rt) xv[t][rt] = xs[(rt * 32 + lr) * 4 + ((2 * t + lh) ^ ((lr >> 1) & 3))];
     }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) wd[ct] = ws[ct * 32 + lr] << (4 * lh);
+    // into the block read in the round before this
+    if (i + kW1Ring - 1 < mine) issue(i + kW1Ring - 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const half8_t b = flip(gv[t], wd[ct] << (8 * t));
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          acc[rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(xv[t][rt]), b, acc[rt][ct], 0, 0, 0);
+      }
   }
   // sums over the waves and w = l t, a column tile at a time
   float *red = reinterpret_cast<float *>(sm);                                       // [wave][rt][register][lane]
@@ -639,16 +670,20 @@ k_bank_second(BankArgs A) {
 }
 
 // Many rows: a workgroup of 4 waves, 64 rows of one slot, every wave 32 CT
-// columns of all G sides.  The slot's T goes through LDS in chunks of 64
-// latent columns (16 KB, two buffers, the next chunk's values in registers
-// meanwhile), where one operand read serves CT expanded sign operands and
-// one of those two row tiles, hi and lo.
-constexpr int kW2It = 2;  // 32-column words per chunk
+// columns of all G sides.  T and the sign words are copied into a ring of
+// chunks of 64 latent columns in LDS, D - 1 of them in flight: T once for the
+// workgroup (a wave a 32-column part of one row tile), a wave's words by
+// itself.  An operand read serves CT expanded sign operands, one of those two
+// row tiles.
+template <int CT>
+constexpr int w2_chunk() { return 16384 + CT * 1024; }
+template <int CT, int D>
+constexpr int w2_lds() { return std::max(D * w2_chunk<CT>(), 4 * 32 * 68 * 4); }
 
-template <int G, int CT>
+template <int G, int CT, int D>
 __global__ void __launch_bounds__(256, 2)
 k_bank_second_wide(BankArgs A, int slots) {
-  constexpr int kPitch = 68, kChunk = 2 * kW2It * 256;  // chunk in 16-byte pieces
+  constexpr int kPitch = 68, kPer = 4 + CT;
   extern __shared__ __align__(16) unsigned char sm[];
   const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
   const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;  // a slot's workgroups on one XCD, as in the first product
@@ -658,7 +693,21 @@ k_bank_second_wide(BankArgs A, int slots) {
   int e, row0, n;
   if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
 
-  const int nit = A.P * A.Wk, nch = (A.Wk + kW2It - 1) / kW2It;  // chunks per path
+  const int nit = A.P * A.Wk, nch = (nit + 1) / 2, total = G * nch;  // words, chunks of a side, chunks
+  const LayerDesc D0 = A.desc[e], D1 = A.desc[(G - 1) * A.E + e];
+  // h (and 2^-11 h) of the lane's columns, two copies per register
+  uint32_t hh[G][2][CT], hl[G][2][CT];
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+#pragma unroll
+    for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint16_t h = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
+        const uint16_t hs = f2h(h2f(h) * 0x1p-11f);
+        hh[q][pp][ct] = h | ((uint32_t)h << 16);
+        hl[q][pp][ct] = hs | ((uint32_t)hs << 16);
+      }
   float16_t acc[G][2][CT];
 #pragma unroll
   for (int q = 0; q < G; ++q)
@@ -668,89 +717,78 @@ k_bank_second_wide(BankArgs A, int slots) {
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[q][rt][ct][i] = 0.f;
-  int jc[CT];
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) jc[ct] = min(j0 + ct * 32 + lr, A.b16 - 1);
 
-  u32x4 *buf = reinterpret_cast<u32x4 *>(sm);
-  const u32x4 *tb = reinterpret_cast<const u32x4 *>(A.T) + (size_t)slot * 2 * G * nit * 256 + threadIdx.x;
-  u32x4 tn[2 * kW2It];
-  uint32_t wn[kW2It][CT];
-  // chunk c of path pp, side q
-  auto fetch = [&](int q, int pp, int c, gu32 su) {
+  const uint16_t *tb = A.T + ((size_t)(slot * 2 + (w >> 1)) * G) * nit * 2048 + lane * 8;
+  unsigned jw[CT / 2];  // the columns whose words the lane copies
 #pragma unroll
-    for (int i = 0; i < kW2It; ++i) {
-      const int it = pp * A.Wk + min(c * kW2It + i, A.Wk - 1);
+  for (int c = 0; c < CT / 2; ++c) jw[c] = min(j0 + c * 64 + lane, A.b16 - 1);
+  int fq = 0, fc = 0, fslot = 0;  // the next chunk to be copied, and where to
+  auto issue = [&]() {  // kPer loads
+    unsigned char *dst = sm + fslot * w2_chunk<CT>();
+    const uint16_t *src = tb + ((size_t)fq * nit + min(2 * fc + (w & 1), nit - 1)) * 2048;
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) tn[rt * kW2It + i] = tb[(size_t)((rt * G + q) * nit + it) * 256];
-      const gu32 row = su + (size_t)it * A.b16;
+    for (int f = 0; f < 4; ++f) dma16(src + f * 512, dst + (w * 4 + f) * 1024);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) wn[i][ct] = row[jc[ct]];
+    for (int i = 0; i < 2; ++i) {
+      const gu32 row = (fq ? D1.su : D0.su) + (size_t)min(2 * fc + i, nit - 1) * A.b16;
+#pragma unroll
+      for (int c = 0; c < CT / 2; ++c)
+        dma4((const void *)(row + jw[c]), dst + 16384 + (w * 2 + i) * CT * 128 + c * 256);
     }
+    if (++fc == nch) {
+      fc = 0;
+      ++fq;
+    }
+    if (++fslot == D) fslot = 0;
   };
-  uint16_t hn[CT];
-  auto fetch_h = [&](gu16 h) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) hn[ct] = h[jc[ct]];
-  };
-  fetch_h(A.desc[e].h);
-  fetch(0, 0, 0, A.desc[e].su);
-  int turn = 0;
+  for (int i = 0; i < D - 1; ++i)
+    if (i < total) issue();
+  int at = 0, done = 0;
 #pragma unroll
   for (int q = 0; q < G; ++q) {
-    const LayerDesc D = A.desc[q * A.E + e];
-    for (int pp = 0; pp < A.P; ++pp) {
-      uint32_t hh[CT], hl[CT];  // the path's h (and 2^-11 h): two copies per register
+    for (int c = 0; c < nch; ++c, ++done) {
+      // chunk `done` has landed (this wave's part, then everybody's)
+      if (D > 2 && done + D - 2 < total)
+        wait_loads<(D - 2) * kPer>();
+      else if (D > 3 && done + D - 3 < total)
+        wait_loads<(D > 3 ? D - 3 : 0) * kPer>();
+      else
+        wait_loads<0>();
+      lds_barrier();
+      if (done + D - 1 < total) issue();  // into the chunk that all have left behind
+      const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at * w2_chunk<CT>());
+      const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at * w2_chunk<CT>() + 16384) + w * CT * 64 + lr;
+      if (++at == D) at = 0;
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const uint16_t h = hn[ct];
-        const uint16_t hs = f2h(h2f(h) * 0x1p-11f);
-        hh[ct] = h | ((uint32_t)h << 16);
-        hl[ct] = hs | ((uint32_t)hs << 16);
-      }
-      if (pp + 1 < A.P)
-        fetch_h(D.h + A.b16);
-      else if (q + 1 < G)
-        fetch_h(A.desc[(q + 1) * A.E + e].h);
-      for (int c = 0; c < nch; ++c, turn ^= 1) {
-        u32x4 *b = buf + turn * kChunk;
-        uint32_t wd[kW2It][CT];
+      for (int i = 0; i < 2; ++i) {
+        const int it = 2 * c + i;
+        if (it >= nit) break;
+        const int pp = it >= A.Wk;
+        uint32_t wd[CT], ph[CT], pl[CT];
 #pragma unroll
-        for (int i = 0; i < 2 * kW2It; ++i) b[i * 256 + threadIdx.x] = tn[i];
+        for (int ct = 0; ct < CT; ++ct) {
+          wd[ct] = wl[i * CT * 32 + ct * 32] << (4 * lh);
+          ph[ct] = pp ? hh[q][1][ct] : hh[q][0][ct];
+          pl[ct] = pp ? hl[q][1][ct] : hl[q][0][ct];
+        }
 #pragma unroll
-        for (int i = 0; i < kW2It; ++i)
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) wd[i][ct] = wn[i][ct] << (4 * lh);
-        if (c + 1 < nch)
-          fetch(q, pp, c + 1, D.su);
-        else if (pp + 1 < A.P)
-          fetch(q, pp + 1, 0, D.su);
-        else if (q + 1 < G)
-          fetch(q + 1, 0, 0, A.desc[(q + 1) * A.E + e].su);
-        lds_barrier();
-        const int steps = (A.s - 32 * kW2It * c + 15) >> 4;  // blocks of 16 left in the path
-        u32x4 t[2][2][2];  // [turn][rt][plane], the next block's read during this one's products
-        auto read = [&](int st) {
+        for (int st = 0; st < 2; ++st) {
+          if (st == 1 && A.s - 32 * (it - pp * A.Wk) <= 16) break;  // the word's second half is padding
+          u32x4 t[2][2];
 #pragma unroll
           for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-            for (int pl = 0; pl < 2; ++pl)
-              t[st & 1][rt][pl] = b[(rt * kW2It + (st >> 1)) * 256 + ((st & 1) * 2 + pl) * 64 + lane];
-        };
-        read(0);
-#pragma unroll
-        for (int st = 0; st < 2 * kW2It; ++st) {
-          if (st >= steps) break;
-          if (st + 1 < 2 * kW2It) read(st + 1);
+            for (int k = 0; k < 2; ++k) t[rt][k] = tl[(rt * 2 + i) * 256 + (st * 2 + k) * 64 + lane];
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
-            const uint32_t wl = wd[st >> 1][ct] << (8 * (st & 1));
-            const half8_t bh = flip(splat(hh[ct]), wl), bl = flip(splat(hl[ct]), wl);
+            const half8_t bh = flip(splat(ph[ct]), wd[ct] << (8 * st)), bl = flip(splat(pl[ct]), wd[ct] << (8 * st));
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) {
-              acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][0]), bh, acc[q][rt][ct], 0, 0, 0);
-              acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][1]), bl, acc[q][rt][ct], 0, 0, 0);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int rt = 0; rt < 2; ++rt)
+                acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[rt][k]), k ? bl : bh, acc[q][rt][ct],
+                                                                        0, 0, 0);
           }
         }
       }
@@ -848,7 +886,7 @@ hipError_t launch_second(const BankArgs &A, int slots, hipStream_t st) {
 template <int RT, int CT>
 hipError_t launch_first_wide(const BankArgs &A, int slots, int ncs, hipStream_t st) {
   const dim3 grid((unsigned)((slots + 7) / 8 * 8 * A.G * A.P * ncs));
-  constexpr int lds = w1_lds<RT>();
+  constexpr int lds = w1_lds<RT, CT>();
   const void *f = A.xvec ? (const void *)k_bank_first_wide<RT, CT, true> : (const void *)k_bank_first_wide<RT, CT, false>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -875,11 +913,16 @@ hipError_t launch_first_wide(const BankArgs &A, int slots, hipStream_t st) {
   }
 }
 
-template <int G, int CT>
+template <int G, int CT, int D>
 hipError_t launch_second_wide(const BankArgs &A, int slots, hipStream_t st) {
   const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
-  const size_t lds = std::max<size_t>(2 * 2 * kW2It * 4096, 4 * 32 * 68 * sizeof(float));
-  k_bank_second_wide<G, CT><<<dim3((unsigned)((slots + 7) / 8 * 8 * ncb)), dim3(256), lds, st>>>(A, slots);
+  constexpr int lds = w2_lds<CT, D>();
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute((const void *)k_bank_second_wide<G, CT, D>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  k_bank_second_wide<G, CT, D><<<dim3((unsigned)((slots + 7) / 8 * 8 * ncb)), dim3(256), lds, st>>>(A, slots);
   return hipGetLastError();
 }
 
@@ -920,9 +963,9 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
     if (e == hipSuccess) e = hipGetLastError();
     if (e == hipSuccess) {
       if (A.G == 1)
-        e = big ? launch_second_wide<1, 4>(A, ns, st) : launch_second<1, 1, 1>(A, ns, st);
+        e = big ? launch_second_wide<1, SCT, SD1>(A, ns, st) : launch_second<1, 1, 1>(A, ns, st);
       else
-        e = big ? launch_second_wide<2, 2>(A, ns, st) : launch_second<2, 1, 1>(A, ns, st);
+        e = big ? launch_second_wide<2, 2, SD2>(A, ns, st) : launch_second<2, 1, 1>(A, ns, st);
     }
     if (e != hipSuccess) return set_error(LB_EHIP, std::string(who) + ": " + hipGetErrorString(e));
   }
