@@ -331,79 +331,103 @@ def lb_bank_reserve(bank: int, rows: int):
     _check(load_library().lb_bank_reserve(bank, int(rows)))
 
 
-def _rows(name, t, width, dtypes, device):
-    """Row stride of a 2-d device tensor with unit column stride."""
-    if t.dim() != 2 or t.shape[1] != width or t.dtype not in dtypes or t.device != device:
-        raise ValueError(f"{name} must be a 2-d tensor of {width} columns on {device}, of {dtypes}, "
-                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.stride(1) != 1 and width > 1:
-        raise ValueError(f"{name} must have unit column stride")
+def _say(t) -> str:
+    return f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}"
+
+
+# The checks below run on every call of operators that take microseconds: they read each attribute once, compare
+# device numbers (-1: not on a GPU) and leave the wording of errors to the failing case.
+def _rows(name, t, width, dtypes, dev):
+    """(rows, row stride) of a 2-d tensor of `width` columns with unit column stride on GPU `dev`."""
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or t.dtype not in dtypes or t.get_device() != dev or (
+            st[1] != 1 and width > 1):
+        raise ValueError(f"{name} must be 2-d with {width} unit-stride columns, of {dtypes}, on GPU {dev}, not {_say(t)}")
     # a single row's stride is never used; torch leaves it arbitrary
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    return (shape[0], st[0]) if shape[0] > 1 else (shape[0], width)
 
 
-def _flat(name, t, shape, dtype, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
-                         f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+def _flat(name, t, shape, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on GPU {dev}, not {_say(t)}")
     return t.data_ptr()
 
 
-def _stream_of(stream, device):
+def _stream_of(stream, dev):
     if stream is None:
         import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _act(name) -> int:
-    try:
-        return ACTIVATIONS[name or "none"]
-    except KeyError:
-        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {name!r}") from None
+def _on_device(dev, fn, *args):
+    """Calls the library with GPU `dev` current (for calls that have no object to take the device from)."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        return _check(fn(*args))
+    with torch.cuda.device(dev):
+        _check(fn(*args))
+
+
+_f16 = _f32 = _i32 = _f16_f32 = _only_f16 = None
+
+
+def _types():
+    global _f16, _f32, _i32, _f16_f32, _only_f16
+    if _f16 is None:
+        import torch
+        _f16, _f32, _i32 = torch.float16, torch.float32, torch.int32
+        _f16_f32, _only_f16 = (_f16, _f32), (_f16,)
 
 
 def _epilogue(bank, y, act, bias, gate_bias, residual):
-    """The arguments that lb_bank_forward and lb_bank_grouped share."""
-    import torch
-    dev, b, n = y.device, bank.b, bank.n
-    if dev.type != "cuda":
+    """The arguments that lb_bank_forward and lb_bank_grouped share: GPU, rows, then in the C order."""
+    _types()
+    dev, b, n = y.get_device(), bank.b, bank.n
+    if dev < 0:
         raise ValueError("y must be a device tensor")
-    f16, f32 = torch.float16, torch.float32
-    ldy = _rows("y", y, b, (f16, f32), dev)
-    pb = _flat("bias", bias, (n, b), f16, dev) if bias is not None else None
-    pg = _flat("gate_bias", gate_bias, (n, b), f16, dev) if gate_bias is not None else None
-    pr, ldr = None, 0
+    rows, ldy = _rows("y", y, b, _f16_f32, dev)
+    dtype = y.dtype
+    if act is None:
+        act = 0
+    else:
+        try:
+            act = ACTIVATIONS[act]
+        except KeyError:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}") from None
+    pb = pg = pr = None
+    ldr = 0
+    if bias is not None:
+        pb = _flat("bias", bias, (n, b), _f16, dev)
+    if gate_bias is not None:
+        pg = _flat("gate_bias", gate_bias, (n, b), _f16, dev)
     if residual is not None:
-        ldr = _rows("residual", residual, b, (y.dtype,), dev)
-        if residual.shape[0] != y.shape[0]:
+        rr, ldr = _rows("residual", residual, b, (dtype,), dev)
+        if rr != rows:
             raise ValueError("residual must have y's rows")
         pr = residual.data_ptr()
-    return y.data_ptr(), ldy, LB_F32 if y.dtype == f32 else LB_F16, _act(act), pb, pg, pr, ldr
+    return dev, rows, y.data_ptr(), ldy, LB_F32 if dtype is _f32 else LB_F16, act, pb, pg, pr, ldr
 
 
 def lb_bank_forward(bank, x, y, expert: int = 0, act=None, bias=None, gate_bias=None, residual=None, stream=None):
     """``Bank`` owner and tensors: y = act(layer(x) + bias) + residual (see include/lb.h)."""
-    import torch
-    py, ldy, yt, a, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
-    ldx = _rows("x", x, bank.a, (torch.float16,), y.device)
-    if x.shape[0] != y.shape[0]:
+    dev, rows, py, ldy, yt, act, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
+    xr, ldx = _rows("x", x, bank.a, _only_f16, dev)
+    if xr != rows:
         raise ValueError("x and y must have the same number of rows")
-    _check(load_library().lb_bank_forward(bank.handle, expert, x.data_ptr(), ldx, py, ldy, yt, x.shape[0], a, pb, pg,
-                                          pr, ldr, _stream_of(stream, y.device)))
+    _check(_lib.lb_bank_forward(bank.handle, expert, x.data_ptr(), ldx, py, ldy, yt, rows, act, pb, pg, pr, ldr,
+                                _stream_of(stream, dev)))
 
 
 def lb_bank_grouped(bank, x, offsets, y, index=None, act=None, bias=None, gate_bias=None, residual=None,
                     stream=None):
     """``Bank`` owner and tensors: rows offsets[e]..offsets[e+1]-1 through layer e (see include/lb.h)."""
-    import torch
-    py, ldy, yt, a, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
-    rows, i32 = y.shape[0], torch.int32
-    ldx = _rows("x", x, bank.a, (torch.float16,), y.device)
-    po = _flat("offsets", offsets, (bank.n + 1,), i32, y.device)
-    pi = _flat("index", index, (rows,), i32, y.device) if index is not None else None
-    _check(load_library().lb_bank_grouped(bank.handle, x.data_ptr(), x.shape[0], ldx, pi, po, rows, py, ldy, yt, a, pb,
-                                          pg, pr, ldr, _stream_of(stream, y.device)))
+    dev, rows, py, ldy, yt, act, pb, pg, pr, ldr = _epilogue(bank, y, act, bias, gate_bias, residual)
+    xr, ldx = _rows("x", x, bank.a, _only_f16, dev)
+    po = _flat("offsets", offsets, (bank.n + 1,), _i32, dev)
+    pi = _flat("index", index, (rows,), _i32, dev) if index is not None else None
+    _check(_lib.lb_bank_grouped(bank.handle, x.data_ptr(), xr, ldx, pi, po, rows, py, ldy, yt, act, pb, pg, pr, ldr,
+                                _stream_of(stream, dev)))
 
 
 def lb_bank_destroy(bank: int):
@@ -418,44 +442,41 @@ def lb_route_ws_bytes(tokens: int, experts: int, k: int) -> int:
 
 def lb_route(logits, k: int, renormalise: bool, ids, weights, offsets, token, row, ws, stream=None):
     """Tensors of include/lb.h's lb_route; ws is a device byte tensor of lb_route_ws_bytes bytes, or None."""
-    import torch
-    if logits.dim() != 2 or logits.device.type != "cuda":
+    _types()
+    dev = logits.get_device()
+    if logits.dim() != 2 or dev < 0:
         raise ValueError("logits must be a 2-d device tensor")
-    t, e = logits.shape
-    dev, i32 = logits.device, torch.int32
-    ld = _rows("logits", logits, e, (torch.float16, torch.float32), dev)
-    args = [_flat("ids", ids, (t, k), i32, dev), _flat("weights", weights, (t, k), torch.float32, dev),
-            _flat("offsets", offsets, (e + 1,), i32, dev), _flat("token", token, (t * k,), i32, dev),
-            _flat("row", row, (t, k), i32, dev)]
-    n = 0
+    e = logits.shape[1]
+    t, ld = _rows("logits", logits, e, _f16_f32, dev)
+    n, pw = 0, None
     if ws is not None:
+        import torch
         n = ws.numel()
-        _flat("ws", ws, (n,), torch.uint8, dev)
-    with torch.cuda.device(dev):
-        _check(load_library().lb_route(logits.data_ptr(), LB_F32 if logits.dtype == torch.float32 else LB_F16, ld, t, e,
-                                       k, int(bool(renormalise)), *args, _ptr(ws), n, _stream_of(stream, dev)))
+        pw = _flat("ws", ws, (n,), torch.uint8, dev)
+    _on_device(dev, load_library().lb_route, logits.data_ptr(), LB_F32 if logits.dtype is _f32 else LB_F16, ld, t, e, k,
+               1 if renormalise else 0, _flat("ids", ids, (t, k), _i32, dev), _flat("weights", weights, (t, k), _f32, dev),
+               _flat("offsets", offsets, (e + 1,), _i32, dev), _flat("token", token, (t * k,), _i32, dev),
+               _flat("row", row, (t, k), _i32, dev), pw, n, _stream_of(stream, dev))
 
 
 def lb_route_combine(y, row, weights, out, residual=None, stream=None):
     """out[t] = residual[t] + sum_j weights[t, j] * y[row[t, j]] (see include/lb.h)."""
-    import torch
-    if out.dim() != 2 or out.device.type != "cuda" or row.dim() != 2:
+    _types()
+    dev = out.get_device()
+    if out.dim() != 2 or row.dim() != 2 or dev < 0:
         raise ValueError("out must be a 2-d device tensor and row a 2-d tensor")
-    t, width = out.shape
-    k, dev = row.shape[1], out.device
-    ldo = _rows("out", out, width, (torch.float16, torch.float32), dev)
-    ldy = _rows("y", y, width, (torch.float16,), dev)
+    width, k, dtype = out.shape[1], row.shape[1], out.dtype
+    t, ldo = _rows("out", out, width, _f16_f32, dev)
+    yr, ldy = _rows("y", y, width, _only_f16, dev)
     pr, ldr = None, 0
     if residual is not None:
-        ldr = _rows("residual", residual, width, (out.dtype,), dev)
-        if residual.shape[0] != t:
+        rr, ldr = _rows("residual", residual, width, (dtype,), dev)
+        if rr != t:
             raise ValueError("residual must have out's rows")
         pr = residual.data_ptr()
-    pw, pi = _flat("weights", weights, (t, k), torch.float32, dev), _flat("row", row, (t, k), torch.int32, dev)
-    with torch.cuda.device(dev):
-        _check(load_library().lb_route_combine(y.data_ptr(), y.shape[0], ldy, pi, pw, t, k, width, pr, ldr,
-                                               out.data_ptr(), ldo, LB_F32 if out.dtype == torch.float32 else LB_F16,
-                                               _stream_of(stream, dev)))
+    _on_device(dev, load_library().lb_route_combine, y.data_ptr(), yr, ldy, _flat("row", row, (t, k), _i32, dev),
+               _flat("weights", weights, (t, k), _f32, dev), t, k, width, pr, ldr, out.data_ptr(), ldo,
+               LB_F32 if dtype is _f32 else LB_F16, _stream_of(stream, dev))
 
 
 # --------------------------------------------------------------- owners

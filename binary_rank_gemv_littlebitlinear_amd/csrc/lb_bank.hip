@@ -47,20 +47,12 @@
 
 #include "lb_internal.h"
 
-#ifndef SD1
-#define SD1 3
-#endif
-#ifndef SD2
-#define SD2 4
-#endif
-#ifndef SCT
-#define SCT 4
-#endif
 namespace {
 
 using namespace lbi;
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
@@ -79,6 +71,7 @@ struct LayerDesc {
 
 struct BankArgs {
   const LayerDesc *desc;  // [side][expert], side 0 = the layers, 1 = the gates
+  LayerDesc one[2];       // those of expert e0, when offsets is null: no load to wait for
   const uint16_t *x;
   const int *index;    // x row of every grouped row, or null
   const int *offsets;  // E + 1 row offsets, or null (every row belongs to expert e0)
@@ -90,8 +83,9 @@ struct BankArgs {
   int64_t ldx, ldy, ldr;
   int rows, x_rows, E, e0;
   int a, a16, b, b16, s, L, P, G, R1, Wk;
-  int tm, slot0;  // rows per slot, first slot of this launch
-  int act, f32, xvec, yvec;
+  int lg, slot0;  // rows per slot are 2^lg; first slot of this launch
+  int span;       // neighbouring tiles that go to one XCD (many-row kernels)
+  int act, f32, xvec, yvec, pair;  // pair: y rows take stores of two elements
 };
 
 #define LB_G(T, p) ((T)(uintptr_t)(p))
@@ -122,11 +116,11 @@ __device__ __forceinline__ u32x4 splat(uint32_t v) {
 // [0, rows], so no row outside the call is touched whatever they hold.
 __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, int &row0, int &n) {
   if (!A.offsets) {
-    const int64_t r = (int64_t)slot * A.tm;
+    const int64_t r = (int64_t)slot << A.lg;
     if (r >= A.rows) return false;
     e = A.e0;
     row0 = (int)r;
-    n = min(A.tm, A.rows - row0);
+    n = min(1 << A.lg, A.rows - row0);
     return true;
   }
   const int lane = threadIdx.x & 63;
@@ -138,7 +132,7 @@ __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, i
       lo = min(max(A.offsets[ee], 0), A.rows);
       c = max(min(max(A.offsets[ee + 1], 0), A.rows) - lo, 0);
     }
-    const int t = (c + A.tm - 1) / A.tm;
+    const int t = (c + (1 << A.lg) - 1) >> A.lg;
     int inc = t;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -151,8 +145,8 @@ __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, i
       const int src = __ffsll(hit) - 1;
       const int ks = __shfl(k, src);
       e = __builtin_amdgcn_readfirstlane(eb + src);
-      row0 = __builtin_amdgcn_readfirstlane(__shfl(lo, src) + ks * A.tm);
-      n = __builtin_amdgcn_readfirstlane(min(A.tm, __shfl(c, src) - ks * A.tm));
+      row0 = __builtin_amdgcn_readfirstlane(__shfl(lo, src) + (ks << A.lg));
+      n = __builtin_amdgcn_readfirstlane(min(1 << A.lg, __shfl(c, src) - (ks << A.lg)));
       return true;
     }
     base += __shfl(inc, 63);
@@ -160,119 +154,62 @@ __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, i
   return false;
 }
 
-// 8 fp16 of an x row from element i on; zeros past a or for a row that is
-// not there.
-template <bool XV>
-__device__ __forceinline__ u32x4 load_x(const BankArgs &A, const uint16_t *row, bool ok, int i) {
-  if constexpr (XV) {
-    return *LB_G(gu128, ok && i < A.a ? (const void *)(row + i) : A.zero);
-  } else {
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = *LB_G(gu16, ok && i + e < A.a ? (const void *)(row + i + e) : A.zero);
-    }
-    u32x4 o;
-    o.x = v[0] | (v[1] << 16);
-    o.y = v[2] | (v[3] << 16);
-    o.z = v[4] | (v[5] << 16);
-    o.w = v[6] | (v[7] << 16);
-    return o;
-  }
+__device__ __forceinline__ LayerDesc layer_of(const BankArgs &A, int side, int e) {
+  return A.offsets ? A.desc[side * A.E + e] : A.one[side];
 }
 
-// ------------------------------------------------------- first product
-// One workgroup of 16 waves: 32 rows x 32 latent columns over the whole
-// input dimension, wave w on the 32-row chunks w, w + 16, ...; the waves'
-// sums are added in wave order through LDS.  Four chunks' operands are
-// requested together.
-constexpr int kN1Waves = 16, kN1U = 4;
-
+// 8 fp16 of an x row from element i on (any 2-byte alignment unless XV);
+// zeros past a.
 template <bool XV>
-__global__ void __launch_bounds__(kN1Waves * 64)
-k_bank_first(BankArgs A) {
-  __shared__ __align__(16) float red[kN1Waves * 1024];
-  const int ntile = A.G * A.P * A.Wk;
-  const int sub = blockIdx.x / ntile, tile = blockIdx.x - sub * ntile;
-  const int per = A.tm >> 5;
-  int e, row0, n;
-  if (!find_slot(A, A.slot0 + sub / per, e, row0, n)) return;
-  const int part = sub % per;
-  row0 += 32 * part;
-  n = min(n - 32 * part, 32);
-  if (n <= 0) return;
-  const int seg = tile / A.Wk, ct = tile - seg * A.Wk;
-  const int side = seg / A.P, p = seg - side * A.P;
-  const LayerDesc D = A.desc[side * A.E + e];
-
-  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  const int k = ct * 32 + lr;
-  const bool cval = k < A.s;
-  const gu32 bw = D.sv + (size_t)p * A.s + k;
-  const gu16 g = D.g + (size_t)p * A.a16;
-  bool rv = lr < n;
-  int64_t r = row0 + lr;
-  if (A.index && rv) {
-    r = A.index[r];
-    rv = r >= 0 && r < A.x_rows;
-  }
-  const uint16_t *xr = A.x + (rv ? r * A.ldx : 0);
-
-  float16_t acc;
+__device__ __forceinline__ u32x4 load8(const uint16_t *p) {
+  typedef u32x4 __attribute__((aligned(2))) loose;
+  typedef const loose __attribute__((address_space(1))) *gloose;
+  if constexpr (XV)
+    return *LB_G(gu128, p);
+  else
+    return *LB_G(gloose, p);
+}
+template <bool XV>
+__device__ __forceinline__ u32x4 load_x(const BankArgs &A, const uint16_t *row, int i) {
+  if (i + 8 <= A.a) return load8<XV>(row + i);
+  uint32_t v[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int c0 = w; c0 < A.R1; c0 += kN1Waves * kN1U) {
-    uint32_t wd[kN1U];
-    u32x4 xv[kN1U][2], gv[kN1U][2];
-#pragma unroll
-    for (int u = 0; u < kN1U; ++u) {
-      const int c = c0 + u * kN1Waves;
-      const bool ok = c < A.R1;
-      wd[u] = *(ok && cval ? bw + (size_t)c * A.L : LB_G(gu32, A.zero));
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const int i = c * 32 + st * 16 + lh * 8;
-        gv[u][st] = *(i < A.a16 ? (gu128)(g + i) : LB_G(gu128, A.zero));
-        xv[u][st] = load_x<XV>(A, xr, rv, i);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kN1U; ++u)
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            as_h8(xv[u][st]), flip(gv[u][st], (wd[u] << (4 * lh)) << (8 * st)), acc, 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) red[(w * 16 + i) * 64 + lane] = acc[i];
-  __syncthreads();
-  // thread (w, lane) finishes register w of the tile
-  float v = 0.f;
-#pragma unroll
-  for (int q = 0; q < kN1Waves; ++q) v += red[(q * 16 + w) * 64 + lane];
-  __syncthreads();
-  v = cval ? v * h2f(D.l[(size_t)p * ((A.s + 7) / 8 * 8) + k]) : 0.f;
-  uint16_t *tl = reinterpret_cast<uint16_t *>(red);  // [k16 2][plane 2][c8 2][row 32][8]
-  {
-    const int row = 8 * (w >> 2) + 4 * lh + (w & 3);
-    const int o = (lr >> 4) * 1024 + (((lr >> 3) & 1) * 32 + row) * 8 + (lr & 7);
-    const uint16_t hi = f2h(v);
-    const float hf = h2f(hi);
-    tl[o] = hi;
-    tl[o + 512] = isinf(hf) ? (uint16_t)0 : f2h((v - hf) * 2048.f);
-  }
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    u32x4 *dst = reinterpret_cast<u32x4 *>(A.T + ((size_t)sub * (A.G * A.P) * A.Wk + tile) * 2048);
-    dst[threadIdx.x] = reinterpret_cast<const u32x4 *>(red)[threadIdx.x];
-  }
+  for (int e = 0; e < 8; ++e) v[e] = i + e < A.a ? *LB_G(gu16, row + i + e) : (uint16_t)0;
+  u32x4 o;
+  o.x = v[0] | (v[1] << 16);
+  o.y = v[2] | (v[3] << 16);
+  o.z = v[4] | (v[5] << 16);
+  o.w = v[6] | (v[7] << 16);
+  return o;
 }
 
-// Workgroup barrier for LDS alone: global loads in flight stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+// The tile of a workgroup: workgroup i runs on XCD i % 8, and each XCD takes
+// runs of `span` neighbouring tiles, which share their operands in its L2.
+__device__ __forceinline__ int xcd_tile(int span) {
+  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3, run = i / span;
+  return (run * 8 + xcd) * span + (i - run * span);
+}
+
+// The x row that row r of the slot reads: its own or its index's, and
+// whether there is one.  Rows past the slot's end and bad indexes read a row
+// that is there; the first are dropped with y's rows, the second zeroed in T.
+__device__ __forceinline__ int64_t x_row(const BankArgs &A, int row0, int n, int r, bool &ok) {
+  int64_t v = row0 + min(r, n - 1);
+  ok = true;
+  if (A.index) {
+    v = A.index[v];
+    ok = v >= 0 && v < A.x_rows;
+    if (!ok) v = 0;
+  }
+  return v;
+}
+
+// w as hi and lo halves at o and o + 512 of a T block.
+__device__ __forceinline__ void put_w(uint16_t *t, int o, float v) {
+  const uint16_t hi = f2h(v);
+  const float hf = h2f(hi);
+  t[o] = hi;
+  t[o + 512] = isinf(hf) ? (uint16_t)0 : f2h((v - hf) * 2048.f);
 }
 
 // Copies straight into LDS: lane i's 16 (4) bytes land at dst + 16 i (4 i).
@@ -288,6 +225,100 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// ------------------------------------------------------- first product
+// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 16 latent
+// columns over the whole input dimension, wave w on the blocks of 32 inputs w,
+// w + NW, ...; the waves' sums are added in wave order through LDS.  Bound by
+// latency and by what one CU can issue, hence the small tile (a 32 x 32 one
+// took 6.5 us for one row of a 4096-wide layer, two thirds of it on the four
+// waves a SIMD that wanted to expand signs at once), operands of kF1U blocks requested
+// together, and g (the same for all columns) straight into the wave's LDS.
+// v_mfma_f32_16x16x32_f16: A[i][k] in lane i + 16 (k / 8), B[k][j] in lane
+// j + 16 (k / 8), D[i][j] in lane j + 16 (i / 4), register i % 4.
+constexpr int kF1U = 16;
+
+template <int NW, bool XV>
+__global__ void __launch_bounds__(NW * 64)
+k_bank_first16(BankArgs A) {
+  __shared__ __align__(16) float red[NW * 256];
+  const int tile = blockIdx.x, slot = blockIdx.y, W2 = 2 * A.Wk;
+  int seg = 0;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) seg += tile >= i * W2;
+  const int k16 = tile - seg * W2, side = A.P == 2 ? seg >> 1 : seg, p = A.P == 2 ? seg & 1 : 0;
+  int e, row0, n;
+  if (!find_slot(A, A.slot0 + slot, e, row0, n)) return;
+  const LayerDesc D = layer_of(A, side, e);
+
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, o = lane >> 4;
+  const int k = k16 * 16 + lr;
+  uint16_t *T = A.T + ((size_t)slot * A.G * A.P * W2 + tile) * 1024;
+  if (k16 * 16 >= A.s) {  // padding
+    if (threadIdx.x < 64) {
+      const int at = (threadIdx.x >> 4) * 256 + (threadIdx.x & 15) * 8;
+      *reinterpret_cast<u32x4 *>(T + at) = splat(0u);
+    }
+    return;
+  }
+  const unsigned col = min(k, A.s - 1);  // columns past s repeat the last and are zeroed below
+  bool ok;
+  const uint16_t *xr = A.x + x_row(A, row0, n, lr, ok) * A.ldx;
+  const unsigned there = (unsigned)__ballot(ok);  // lanes 0..15: the rows
+  const gu16 g = D.g + (size_t)p * A.a16;
+  const gu32 bw = D.sv + (size_t)p * A.s;
+  const float lk = h2f(D.l[(size_t)p * ((A.s + 7) / 8 * 8) + col]);
+
+  float4_t acc = {0.f, 0.f, 0.f, 0.f};
+  const int full = A.a >> 5;                                            // whole blocks
+  unsigned char *gl = reinterpret_cast<unsigned char *>(red + w * 256);  // the wave's own part of red
+  const u32x4 *gs = reinterpret_cast<const u32x4 *>(gl);
+  for (int c0 = w; c0 < full; c0 += NW * kF1U) {
+    uint32_t wd[kF1U];
+    u32x4 xv[kF1U];
+    dma16((const void *)(g + min(c0 + (lane >> 2) * NW, full - 1) * 32 + (lane & 3) * 8), gl);
+#pragma unroll
+    for (int u = 0; u < kF1U; ++u) {
+      const int c = min(c0 + u * NW, full - 1);  // past the end: read, not used
+      wd[u] = (bw + (size_t)c * A.L)[col];
+      xv[u] = load8<XV>(xr + c * 32 + o * 8);
+    }
+    wait_loads<0>();
+#pragma unroll
+    for (int u = 0; u < kF1U; ++u) {
+      if (c0 + u * NW >= full) break;
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(xv[u]), flip(gs[4 * u + o], wd[u] << (4 * o)), acc, 0, 0, 0);
+    }
+  }
+  if (full < A.R1 && w == NW - 1) {  // the last block is not whole
+    const int i = full * 32 + o * 8;
+    const u32x4 gv = *(i < A.a16 ? (gu128)(g + i) : LB_G(gu128, A.zero));
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(load_x<XV>(A, xr, i)),
+                                                 flip(gv, (bw + (size_t)full * A.L)[col] << (4 * o)), acc, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[(w * 4 + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  __shared__ __align__(16) uint16_t tl[1024];  // the T block
+  if (w < 4) {  // wave w finishes register w
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += red[(q * 4 + w) * 64 + lane];
+    const int row = 4 * o + w;
+    const bool keep = k < A.s && ((there >> row) & 1u);
+    put_w(tl, ((lr >> 3) * 32 + row) * 8 + (lr & 7), keep ? v * lk : 0.f);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int at = (threadIdx.x >> 4) * 256 + (threadIdx.x & 15) * 8;  // [plane, c8][row]
+    *reinterpret_cast<u32x4 *>(T + at) = *reinterpret_cast<const u32x4 *>(tl + at);
+  }
+}
+
+// Workgroup barrier for LDS alone: global loads in flight stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Many rows: a workgroup of 8 waves computes 32 RT rows x 32 CT columns of one
 // segment over the whole input dimension, wave w on the blocks of 32 inputs
 // 2 w, 2 w + 1, 2 w + 16, ... (pairs: whole 128-byte lines of x).  A wave
@@ -297,29 +328,28 @@ __device__ __forceinline__ void wait_loads() {
 // c of row r in slot c ^ (r / 2) % 4, so that the operand reads meet no bank
 // twice).  One expanded sign operand serves RT products.  The waves' sums are
 // added in wave order through LDS, 32 columns at a time.  The workgroups of
-// one slot run on one XCD (workgroup i runs on XCD i % 8) one after another,
-// so its x rows come from that XCD's L2 after the first.
-constexpr int kW1Waves = 8, kW1Ring = 4;
+// one slot lie side by side (xcd_tile), so its x rows come from an L2 after
+// the first.
+constexpr int kW1Ring = 4;
 template <int RT, int CT>
 constexpr int w1_block() { return RT * 2048 + (CT + 1) / 2 * 256 + 64; }  // x, words, g
-template <int RT, int CT>
+template <int RT, int CT, int NW>
 constexpr int w1_lds() {
-  return std::max(kW1Waves * kW1Ring * w1_block<RT, CT>(), RT * (kW1Waves * 4096 + 4096));
+  return std::max(NW * kW1Ring * w1_block<RT, CT>(), RT * (NW * 4096 + 4096));
 }
 
-template <int RT, int CT, bool XV>
-__global__ void __launch_bounds__(kW1Waves * 64)
+template <int RT, int CT, int NW, bool XV>
+__global__ void __launch_bounds__(NW * 64, 8 / NW)
 k_bank_first_wide(BankArgs A, int slots, int ncs) {
   extern __shared__ __align__(16) unsigned char sm[];
   constexpr int kBlock = w1_block<RT, CT>(), kWords = RT * 2048, kG = kBlock - 64, kPer = 2 * RT + (CT + 1) / 2 + 1;
-  const int ncg = A.G * A.P * ncs;
-  const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;
-  const int slot = (jj / ncg) * 8 + xcd, cg = jj % ncg;
+  const int ncg = A.G * A.P * ncs, at = xcd_tile(A.span);
+  const int slot = at / ncg, cg = at - slot * ncg;
   int e, row0, n;
   if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
   const int seg = cg / ncs, ct0 = (cg - seg * ncs) * CT;
   const int side = seg / A.P, p = seg - side * A.P;
-  const LayerDesc D = A.desc[side * A.E + e];
+  const LayerDesc D = layer_of(A, side, e);
 
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   unsigned char *ring = sm + w * kW1Ring * kBlock;
@@ -330,17 +360,12 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
   for (int q = 0; q < (CT + 1) / 2; ++q) col[q] = min(ct0 * 32 + q * 64 + lane, A.s - 1);
   // the lane's rows: 16 u + lane / 4, 16 bytes of each
   const int piece = (lane & 3) ^ ((lane >> 3) & 3);
-  int xrow[2 * RT];
+  const uint16_t *xrow[2 * RT];
+  bool ok;
 #pragma unroll
-  for (int u = 0; u < 2 * RT; ++u) {
-    const int r = 16 * u + (lane >> 2);
-    int v = r < n ? row0 + r : -1;
-    if (A.index && v >= 0) {
-      v = A.index[v];
-      if (v >= A.x_rows) v = -1;
-    }
-    xrow[u] = v;
-  }
+  for (int u = 0; u < 2 * RT; ++u) xrow[u] = A.x + x_row(A, row0, n, 16 * u + (lane >> 2), ok) * A.ldx;
+  (void)x_row(A, row0, n, lane & (32 * RT - 1), ok);
+  const unsigned long long there = __ballot(ok);
 
   float16_t acc[RT][CT];
 #pragma unroll
@@ -350,71 +375,98 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
 
-  // the wave's block number i is block 16 (i / 2) + 2 w + i % 2 of the input
-  auto block_of = [&](int i) { return 16 * (i >> 1) + 2 * w + (i & 1); };
-  const int nblk = A.R1;
-  const int mine = max(0, (nblk - 2 * w + 15) / 16 * 2 - ((nblk - 2 * w) % 16 == 1 ? 1 : 0));
-  // copies block i of the wave (kPer loads)
-  auto issue = [&](int i) {
-    const int kb = block_of(i);
-    unsigned char *dst = ring + (i & (kW1Ring - 1)) * kBlock;
-    const int k0 = kb * 32 + piece * 8;
+  // the wave's block number i is block 2 NW (i / 2) + 2 w + i % 2 of the input
+  const int behind = max(0, A.R1 - 2 * w);  // blocks from its first on
+  const int mine = (behind + 2 * NW - 1) / (2 * NW) * 2 - (behind % (2 * NW) == 1 ? 1 : 0);
+  // the next block to be copied: its number, place, and the addresses, which
+  // only advance
+  int kb = 2 * w, fs = 0;
+#pragma unroll
+  for (int u = 0; u < 2 * RT; ++u) xrow[u] += kb * 32 + piece * 8;
+  gu32 wrow = bw + (size_t)kb * A.L;
+  gu16 grow = g + kb * 32 + (lane & 3) * 8;
+  auto issue = [&]() {  // kPer loads
+    unsigned char *dst = ring + fs;
+    const bool whole = kb * 32 + 32 <= A.a;  // uniform
 #pragma unroll
     for (int u = 0; u < 2 * RT; ++u) {
-      const uint16_t *row = A.x + (int64_t)xrow[u] * A.ldx;
       if constexpr (XV)
-        dma16(xrow[u] >= 0 && k0 < A.a ? (const void *)(row + k0) : A.zero, dst + u * 1024);
+        dma16(whole || kb * 32 + piece * 8 < A.a ? (const void *)xrow[u] : A.zero, dst + u * 1024);
       else
-        *reinterpret_cast<u32x4 *>(dst + u * 1024 + lane * 16) = load_x<false>(A, row, xrow[u] >= 0, k0);
+        *reinterpret_cast<u32x4 *>(dst + u * 1024 + lane * 16) =
+            load_x<false>(A, xrow[u] - (kb * 32 + piece * 8), kb * 32 + piece * 8);
     }
-    const gu32 wrow = bw + (size_t)kb * A.L;
 #pragma unroll
     for (int q = 0; q < (CT + 1) / 2; ++q) dma4((const void *)(wrow + col[q]), dst + kWords + q * 256);
-    if (lane < 4) {
-      const int i8 = kb * 32 + lane * 8;
-      dma16(i8 < A.a16 ? (const void *)(g + i8) : A.zero, dst + kG);
+    if (lane < 4) dma16(whole || kb * 32 + lane * 8 < A.a16 ? (const void *)grow : A.zero, dst + kG);
+    const int step = kb & 1 ? 2 * NW - 1 : 1;
+    kb += step;
+#pragma unroll
+    for (int u = 0; u < 2 * RT; ++u) xrow[u] += step * 32;
+    wrow += (size_t)step * A.L;
+    grow += step * 32;
+    fs = fs + kBlock == kW1Ring * kBlock ? 0 : fs + kBlock;
+  };
+  // operands: half 0 of a block is read during the products of half 1 of the
+  // one before, half 1 during those of half 0
+  u32x4 gv[2], xv[2][RT];
+  uint32_t wd[CT], wn[CT];
+  auto read = [&](int t, const unsigned char *blk) {
+    gv[t] = reinterpret_cast<const u32x4 *>(blk + kG)[2 * t + lh];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+      xv[t][rt] = reinterpret_cast<const u32x4 *>(blk)[(rt * 32 + lr) * 4 + ((2 * t + lh) ^ ((lr >> 1) & 3))];
+  };
+  auto read_words = [&](uint32_t (&to)[CT], const unsigned char *blk) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) to[ct] = reinterpret_cast<const uint32_t *>(blk + kWords)[ct * 32 + lr];
+  };
+  auto multiply = [&](int t) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const half8_t b = flip(gv[t], wd[ct] << (8 * t));
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        acc[rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(xv[t][rt]), b, acc[rt][ct], 0, 0, 0);
     }
   };
 #pragma unroll
   for (int i = 0; i < kW1Ring - 1; ++i)
-    if (i < mine) issue(i);
-  for (int i = 0; i < mine; ++i) {
-    // block i has landed; the later ones may be in flight
-    if (XV && i + 2 < mine)
+    if (i < mine) issue();
+  if (mine > 0) {
+    if (XV && mine >= 3)
       wait_loads<2 * kPer>();
-    else if (XV && i + 1 < mine)
-      wait_loads<kPer>();
     else
       wait_loads<0>();
-    const unsigned char *blk = ring + (i & (kW1Ring - 1)) * kBlock;
-    const u32x4 *xs = reinterpret_cast<const u32x4 *>(blk);
-    const uint32_t *ws = reinterpret_cast<const uint32_t *>(blk + kWords);
-    const u32x4 *gs = reinterpret_cast<const u32x4 *>(blk + kG);
-    uint32_t wd[CT];
-    u32x4 gv[2], xv[2][RT];
+    read(0, ring);
+    read_words(wd, ring);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      gv[t] = gs[2 * t + lh];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) xv[t][rt] = xs[(rt * 32 + lr) * 4 + ((2 * t + lh) ^ ((lr >> 1) & 3))];
-    }
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) wd[ct] = ws[ct * 32 + lr] << (4 * lh);
-    // into the block read in the round before this
-    if (i + kW1Ring - 1 < mine) issue(i + kW1Ring - 1);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const half8_t b = flip(gv[t], wd[ct] << (8 * t));
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          acc[rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(xv[t][rt]), b, acc[rt][ct], 0, 0, 0);
-      }
+    for (int ct = 0; ct < CT; ++ct) wd[ct] <<= 4 * lh;
   }
+  int rs = 0;  // place of block i
+  auto round = [&](bool more, bool next, auto wait) {
+    const unsigned char *blk = ring + rs;
+    rs = rs + kBlock == kW1Ring * kBlock ? 0 : rs + kBlock;
+    read(1, blk);
+    if (more) issue();  // into the block read in the round before this
+    multiply(0);
+    if (next) {
+      wait();  // the next block has landed
+      read(0, ring + rs);
+      read_words(wn, ring + rs);
+    }
+    multiply(1);
+    if (next) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) wd[ct] = wn[ct] << (4 * lh);
+    }
+  };
+  int i = 0;
+  for (; i + 3 < mine; ++i) round(true, true, [] { wait_loads<XV ? 2 * kPer : 0>(); });
+  for (; i < mine; ++i) round(false, i + 1 < mine, [] { wait_loads<0>(); });
   // sums over the waves and w = l t, a column tile at a time
-  float *red = reinterpret_cast<float *>(sm);                                       // [wave][rt][register][lane]
-  uint16_t *tl = reinterpret_cast<uint16_t *>(sm + RT * kW1Waves * 4096);           // [rt][2048]
+  float4_t *red = reinterpret_cast<float4_t *>(sm);                         // [wave][rt][registers / 4][lane]
+  uint16_t *tl = reinterpret_cast<uint16_t *>(sm + RT * NW * 4096);  // [rt][2048]
   const int nseg = A.G * A.P;
   __syncthreads();
 #pragma unroll
@@ -424,26 +476,29 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) red[((w * RT + rt) * 16 + i) * 64 + lane] = acc[rt][ct][i];
+      for (int q = 0; q < 4; ++q) {
+        const float16_t &c = acc[rt][ct];
+        red[((w * RT + rt) * 4 + q) * 64 + lane] = float4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      }
     __syncthreads();
     const int k = tile * 32 + lr;
     const float lk = k < A.s ? h2f(D.l[(size_t)p * ((A.s + 7) / 8 * 8) + k]) : 0.f;
 #pragma unroll
-    for (int q = 0; q < 2 * RT; ++q) {
-      const int idx = q * 512 + threadIdx.x, rt = idx >> 10, i = (idx >> 6) & 15;
-      float v = 0.f;
+    for (int u = 0; u < (RT * 4 + NW - 1) / NW; ++u) {
+      const int idx = u * NW * 64 + threadIdx.x, rt = idx >> 8, q = (idx >> 6) & 3;
+      if (RT * 4 < NW && idx >= RT * 256) break;
+      float4_t v = red[idx];
 #pragma unroll
-      for (int z = 0; z < kW1Waves; ++z) v += red[z * RT * 1024 + idx];
-      v = k < A.s ? v * lk : 0.f;
-      const int row = 8 * (i >> 2) + 4 * lh + (i & 3);
-      const int o = rt * 2048 + (lr >> 4) * 1024 + (((lr >> 3) & 1) * 32 + row) * 8 + (lr & 7);
-      const uint16_t hi = f2h(v);
-      const float hf = h2f(hi);
-      tl[o] = hi;
-      tl[o + 512] = isinf(hf) ? (uint16_t)0 : f2h((v - hf) * 2048.f);
+      for (int z = 1; z < NW; ++z) v += red[z * RT * 256 + idx];
+      const int row = 8 * q + 4 * lh;
+      const unsigned here = (unsigned)(there >> (rt * 32 + row)) & 15u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        put_w(tl, rt * 2048 + (lr >> 4) * 1024 + (((lr >> 3) & 1) * 32 + row + i) * 8 + (lr & 7),
+              k < A.s && ((here >> i) & 1u) ? v[i] * lk : 0.f);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < RT * 256; i += 512) {
+    for (int i = threadIdx.x; i < RT * 256; i += NW * 64) {
       const int rt = i >> 8;
       u32x4 *dst = reinterpret_cast<u32x4 *>(A.T + (((size_t)(slot * RT + rt) * nseg + seg) * A.Wk + tile) * 2048);
       dst[i & 255] = reinterpret_cast<const u32x4 *>(tl)[i];
@@ -577,233 +632,302 @@ __device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n
   __builtin_amdgcn_wave_barrier();
 }
 
-// A workgroup of 4 waves, each 32 RT rows of one slot x 32 CT outputs of all G
-// sides, operands straight from T (1 KB contiguous per load) and su2m (one
-// word per column and 32 latent columns); the workgroups of a slot lie side
-// by side.  The epilogue turns each 32-row tile through the wave's own LDS,
-// so that residual loads and y stores are whole 16-byte pieces of rows.
-template <int G, int RT, int CT>
-__global__ void __launch_bounds__(256)
-k_bank_second(BankArgs A) {
-  constexpr int kPitch = pitch2<CT>();
-  extern __shared__ __align__(16) float smem[];
-  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
-  const int slot = blockIdx.x / ncb, cb = blockIdx.x - slot * ncb;
-  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  const int j0 = (cb * 4 + w) * 32 * CT;
-  if (j0 >= A.b) return;
+// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 32 columns
+// of all G sides, the waves interleaved over the (side, path, 32-column word)
+// parts of K, so that everything is requested at once; their sums are added in
+// wave order through LDS, where a thread finishes two neighbouring columns.
+template <int G, int CT, int NW, int U>
+__global__ void __launch_bounds__(NW * 64)
+k_bank_second16(BankArgs A) {
+  __shared__ __align__(16) float red[NW * G * CT * 256];  // [wave][side][column tile][register][lane]
+  const int slot = blockIdx.y, j0 = blockIdx.x * 16 * CT;
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, o = lane >> 4;
   int e, row0, n;
   if (!find_slot(A, A.slot0 + slot, e, row0, n)) return;
+  const LayerDesc D0 = layer_of(A, 0, e), D1 = layer_of(A, G - 1, e);
 
-  const int nit = A.P * A.Wk;
-  float16_t acc[G][RT][CT];
+  const int nit = A.P * A.Wk, items = G * nit;
+  unsigned jc[CT];
+  float4_t acc[G][CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    jc[c] = min(j0 + 16 * c + lr, A.b16 - 1);
+#pragma unroll
+    for (int q = 0; q < G; ++q) acc[q][c] = float4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  // the lane's 8 latent columns of a word: block o / 2, half o % 2
+  const uint16_t *tp = A.T + (size_t)slot * items * 2048 + (o >> 1) * 1024 + ((o & 1) * 32 + lr) * 8;
+  for (int x0 = w; x0 < items; x0 += U * NW) {
+    u32x4 t[U][2];  // [plane]
+    uint32_t wd[U][CT];
+    uint16_t hv[U][CT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = min(x0 + u * NW, items - 1);  // past the end: read, not used
+      const int q = G == 2 && x >= nit, it = x - q * nit, pp = it >= A.Wk;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) t[u][f] = *LB_G(gu128, tp + (size_t)x * 2048 + f * 512);
+      const gu32 row = (q ? D1.su : D0.su) + (size_t)it * A.b16;
+      const gu16 h = (q ? D1.h : D0.h) + (size_t)pp * A.b16;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        wd[u][c] = row[jc[c]];
+        hv[u][c] = h[jc[c]];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = x0 + u * NW;
+      if (x >= items) break;
+      auto mma = [&](float4_t (&c)[CT]) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const uint16_t hs = f2h(h2f(hv[u][ct]) * 0x1p-11f);
+          const uint32_t wl = wd[u][ct] << (4 * o);
+          c[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              as_h8(t[u][0]), flip(splat(hv[u][ct] | ((uint32_t)hv[u][ct] << 16)), wl), c[ct], 0, 0, 0);
+          c[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              as_h8(t[u][1]), flip(splat(hs | ((uint32_t)hs << 16)), wl), c[ct], 0, 0, 0);
+        }
+      };
+      if (G == 1 || x < nit)
+        mma(acc[0]);
+      else
+        mma(acc[G - 1]);
+    }
+  }
 #pragma unroll
   for (int q = 0; q < G; ++q)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[q][rt][ct][i] = 0.f;
-
-  int jc[CT];
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) jc[ct] = min(j0 + ct * 32 + lr, A.b16 - 1);
-#pragma unroll
-  for (int q = 0; q < G; ++q) {
-    const LayerDesc D = A.desc[q * A.E + e];
-    const u32x4 *tp[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      tp[rt] = reinterpret_cast<const u32x4 *>(A.T) + ((size_t)(slot * RT + rt) * G + q) * nit * 256 + lane;
-    struct Ops {
-      u32x4 t[RT][2][2];  // [k16][plane]
-      uint32_t wd[CT];
-    };
-    auto fetch = [&](int it, Ops &o) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int f = 0; f < 4; ++f) o.t[rt][f >> 1][f & 1] = tp[rt][it * 256 + f * 64];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) o.wd[ct] = D.su[(size_t)it * A.b16 + jc[ct]];
-    };
-    Ops c;
-    fetch(0, c);
-    uint32_t hh[CT], hl[CT];
-    for (int it = 0; it < nit; ++it) {
-      if (it == 0 || it == A.Wk) {  // a path's h: two copies of it per register
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const uint16_t h = D.h[(size_t)(it ? A.b16 : 0) + jc[ct]];
-          const uint16_t hs = f2h(h2f(h) * 0x1p-11f);
-          hh[ct] = h | ((uint32_t)h << 16);
-          hl[ct] = hs | ((uint32_t)hs << 16);
-        }
+      for (int i = 0; i < 4; ++i) red[(((w * G + q) * CT + ct) * 4 + i) * 64 + lane] = acc[q][ct][i];
+  __syncthreads();
+  for (int id = threadIdx.x; id < n * 8 * CT; id += NW * 64) {
+    const int row = id / (8 * CT), c = id % (8 * CT) * 2, j = j0 + c;
+    if (j >= A.b) continue;
+    const int at = ((c >> 4) * 4 + (row & 3)) * 64 + (c & 15) + 16 * (row >> 2);
+    const bool two = j + 1 < A.b;
+    float v[2], g[2];
+  #pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[i] = g[i] = 0.f;
+  #pragma unroll
+      for (int q = 0; q < NW; ++q) {
+        v[i] += red[q * G * CT * 256 + at + i];
+        if constexpr (G == 2) g[i] += red[(q * G + 1) * CT * 256 + at + i];
       }
-      Ops nx;
-      fetch(min(it + 1, nit - 1), nx);
-      const int left = A.s - 32 * (it < A.Wk ? it : it - A.Wk);
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        if (st == 1 && left <= 16) break;  // the block's second half is padding
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const uint32_t wl = (c.wd[ct] << (4 * lh)) << (8 * st);
-          const half8_t bh = flip(splat(hh[ct]), wl);
-          const half8_t bl = flip(splat(hl[ct]), wl);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(c.t[rt][st][0]), bh, acc[q][rt][ct], 0, 0, 0);
-            acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(c.t[rt][st][1]), bl, acc[q][rt][ct], 0, 0, 0);
-          }
-        }
+      const int ji = min(j + i, A.b - 1);
+      if (A.bias[0]) v[i] += h2f(A.bias[0][(size_t)e * A.b + ji]);
+      if (G == 2 && A.bias[1]) g[i] += h2f(A.bias[1][(size_t)e * A.b + ji]);
+    }
+    with_act(A.act, [&](auto act) {
+  #pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = G == 2 ? activate<decltype(act)::value>(g[i]) * v[i] : activate<decltype(act)::value>(v[i]);
+    });
+    const int64_t yo = (int64_t)(row0 + row) * A.ldy + j, ro = (int64_t)(row0 + row) * A.ldr + j;
+    if (A.f32) {
+      float *y = (float *)A.y + yo;
+      if (A.res) {
+        const float *r = (const float *)A.res + ro;
+        v[0] += r[0];
+        if (two) v[1] += r[1];
       }
-      c = nx;
+      if (A.pair && two) {
+        *reinterpret_cast<float2 *>(y) = make_float2(v[0], v[1]);
+      } else {
+        y[0] = v[0];
+        if (two) y[1] = v[1];
+      }
+    } else {
+      uint16_t *y = (uint16_t *)A.y + yo;
+      if (A.res) {
+        const uint16_t *r = (const uint16_t *)A.res + ro;
+        v[0] += h2f(r[0]);
+        if (two) v[1] += h2f(r[1]);
+      }
+      if (A.pair && two) {
+        *reinterpret_cast<uint32_t *>(y) = f2h(v[0]) | ((uint32_t)f2h(v[1]) << 16);
+      } else {
+        y[0] = f2h(v[0]);
+        if (two) y[1] = f2h(v[1]);
+      }
     }
   }
-
-  float *lds = smem + w * 32 * kPitch;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-    if (rt * 32 < n) finish<G, CT>(A, e, row0, n, rt, j0, acc[0][rt], acc[G - 1][rt], lds);
 }
 
-// Many rows: a workgroup of 4 waves, 64 rows of one slot, every wave 32 CT
-// columns of all G sides.  T and the sign words are copied into a ring of
-// chunks of 64 latent columns in LDS, D - 1 of them in flight: T once for the
-// workgroup (a wave a 32-column part of one row tile), a wave's words by
-// itself.  An operand read serves CT expanded sign operands, one of those two
+// More rows: a workgroup of NW waves, 32 RT rows of one slot, every wave 32 CT
+// columns of all G sides.  T and the sign words are copied into LDS in chunks
+// of KW 32-column words of a path, the next chunk during the products of one:
+// T once for the workgroup, a wave's words by itself.  (Three or four chunks
+// on their way changed nothing.)  With two waves on a SIMD a wave
+// issues an instruction every four or five cycles at best, so what bounds this is
+// the instructions a product needs: per 16 columns and column tile 4 shifts
+// and 8 sign flips (4 when hi and lo have sums of their own), shared by RT row
+// tiles, and everything that is not per product is kept out of the loop.  An operand read serves CT expanded sign operands, one of those two
 // row tiles.
-template <int CT>
-constexpr int w2_chunk() { return 16384 + CT * 1024; }
-template <int CT, int D>
-constexpr int w2_lds() { return std::max(D * w2_chunk<CT>(), 4 * 32 * 68 * 4); }
+template <int RT, int CT, int NW, int KW>
+constexpr int w2_chunk() { return KW * (RT * 4096 + NW * CT * 128); }
+template <int RT, int CT, int NW, int KW>
+constexpr int w2_lds() { return std::max(2 * w2_chunk<RT, CT, NW, KW>(), NW * 32 * pitch2<(CT > 1 ? 2 : 1)>() * 4); }
 
-template <int G, int CT, int D>
-__global__ void __launch_bounds__(256, 2)
+template <int G, int RT, int CT, int NW, int KW>
+__global__ void __launch_bounds__(NW * 64, G * RT * CT == 4 ? 4 : 2)
 k_bank_second_wide(BankArgs A, int slots) {
-  constexpr int kPitch = 68, kPer = 4 + CT;
+  constexpr int kT = RT * KW * 4 / NW;  // T copies of a wave per chunk
+  constexpr int kChunk = w2_chunk<RT, CT, NW, KW>(), kEp = CT > 1 ? 2 : 1;
+  constexpr bool kApart = RT * CT == 1;  // hi and lo products in sums of their own: lo needs no 2^-11 h
+  static_assert(kT * NW == RT * KW * 4 && (CT == 1 ? KW % 2 == 0 : CT % 2 == 0), "the copies below");
   extern __shared__ __align__(16) unsigned char sm[];
-  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
-  const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;  // a slot's workgroups on one XCD, as in the first product
-  const int slot = (jj / ncb) * 8 + xcd, cb = jj % ncb;
+  const int ncb = (A.b + NW * 32 * CT - 1) / (NW * 32 * CT);
+  const int tile = xcd_tile(A.span), slot = tile / ncb, cb = tile - slot * ncb;
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  const int j0 = (cb * 4 + w) * 32 * CT;
+  const int j0 = (cb * NW + w) * 32 * CT;
   int e, row0, n;
   if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
 
-  const int nit = A.P * A.Wk, nch = (nit + 1) / 2, total = G * nch;  // words, chunks of a side, chunks
-  const LayerDesc D0 = A.desc[e], D1 = A.desc[(G - 1) * A.E + e];
-  // h (and 2^-11 h) of the lane's columns, two copies per register
-  uint32_t hh[G][2][CT], hl[G][2][CT];
+  const int nch = (A.Wk + KW - 1) / KW;  // chunks of a path
+  const LayerDesc D0 = layer_of(A, 0, e), D1 = layer_of(A, G - 1, e);
+  float16_t acc[G][RT][CT], low[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      low[q][i] = 0.f;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) acc[q][rt][ct][i] = 0.f;
+    }
+  int jc[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) jc[ct] = min(j0 + ct * 32 + lr, A.b16 - 1);
+  uint16_t hv[G][2][CT];
 #pragma unroll
   for (int q = 0; q < G; ++q)
 #pragma unroll
     for (int pp = 0; pp < 2; ++pp)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const uint16_t h = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
-        const uint16_t hs = f2h(h2f(h) * 0x1p-11f);
-        hh[q][pp][ct] = h | ((uint32_t)h << 16);
-        hl[q][pp][ct] = hs | ((uint32_t)hs << 16);
-      }
-  float16_t acc[G][2][CT];
-#pragma unroll
-  for (int q = 0; q < G; ++q)
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[q][rt][ct][i] = 0.f;
+      for (int ct = 0; ct < CT; ++ct) hv[q][pp][ct] = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + jc[ct]];
 
-  const uint16_t *tb = A.T + ((size_t)(slot * 2 + (w >> 1)) * G) * nit * 2048 + lane * 8;
-  unsigned jw[CT / 2];  // the columns whose words the lane copies
+  // The wave's copies of a chunk, at addresses that only advance: kT KB of T
+  // from piece tu of the chunk on (past a path's last word they read on, T has
+  // room behind it), and its words (the last one again past it); with CT = 1
+  // two words of its 32 columns at once.
+  const int tu = w * kT;
+  const uint16_t *src[kT];
 #pragma unroll
-  for (int c = 0; c < CT / 2; ++c) jw[c] = min(j0 + c * 64 + lane, A.b16 - 1);
-  int fq = 0, fc = 0, fslot = 0;  // the next chunk to be copied, and where to
-  auto issue = [&]() {  // kPer loads
-    unsigned char *dst = sm + fslot * w2_chunk<CT>();
-    const uint16_t *src = tb + ((size_t)fq * nit + min(2 * fc + (w & 1), nit - 1)) * 2048;
+  for (int f = 0; f < kT; ++f) {
+    const int u = tu + f, rt = u / (KW * 4), piece = u % (KW * 4);
+    src[f] = A.T + ((size_t)(slot * RT + rt) * G * A.P * A.Wk) * 2048 + piece * 512 + lane * 8;
+  }
+  unsigned jw[(CT + 1) / 2];
 #pragma unroll
-    for (int f = 0; f < 4; ++f) dma16(src + f * 512, dst + (w * 4 + f) * 1024);
+  for (int c = 0; c < (CT + 1) / 2; ++c) jw[c] = min(j0 + c * 64 + (CT == 1 ? lr : lane), A.b16 - 1);
+  gu32 row = D0.su;             // of the next word
+  int fpath = 0, fc = 0, fs = 0;  // the next chunk's path (of all sides), number in it, and place
+  auto issue = [&]() {
+    unsigned char *dst = sm + fs;
+    const int left = A.Wk - fc * KW;  // words of the path from here on
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const gu32 row = (fq ? D1.su : D0.su) + (size_t)min(2 * fc + i, nit - 1) * A.b16;
+    for (int f = 0; f < kT; ++f) dma16(src[f], dst + (tu + f) * 1024);
+    unsigned char *wdst = dst + KW * RT * 4096 + w * KW * CT * 128;
 #pragma unroll
-      for (int c = 0; c < CT / 2; ++c)
-        dma4((const void *)(row + jw[c]), dst + 16384 + (w * 2 + i) * CT * 128 + c * 256);
+    for (int i = 0; i < KW; i += CT == 1 ? 2 : 1) {
+      const gu32 r = row + (size_t)min(i, left - 1) * A.b16;
+      if constexpr (CT == 1) {
+        dma4((const void *)(r + (lh && i + 1 < left ? A.b16 : 0) + jw[0]), wdst + i * 128);
+      } else {
+#pragma unroll
+        for (int c = 0; c < CT / 2; ++c) dma4((const void *)(r + jw[c]), wdst + i * CT * 128 + c * 256);
+      }
     }
+    const int step = min(KW, left);
+    row += (size_t)step * A.b16;
+#pragma unroll
+    for (int f = 0; f < kT; ++f) src[f] += step * 2048;
     if (++fc == nch) {
       fc = 0;
-      ++fq;
+      if (++fpath == A.P) row = D1.su;
     }
-    if (++fslot == D) fslot = 0;
+    fs ^= kChunk;
   };
+  issue();
+  const int paths = G * A.P;
+  int at = 0;
 #pragma unroll
-  for (int i = 0; i < D - 1; ++i)
-    if (i < total) issue();
-  int at = 0, done = 0;
+  for (int q = 0; q < G; ++q)
+    for (int pp = 0; pp < A.P; ++pp) {
+      uint32_t hh[CT], hl[CT];  // the path's h (and 2^-11 h): two copies per register
 #pragma unroll
-  for (int q = 0; q < G; ++q) {
-    for (int c = 0; c < nch; ++c, ++done) {
-      // chunk `done` has landed (this wave's part, then everybody's)
-      if (D > 2 && done + D - 2 < total)
-        wait_loads<(D - 2) * kPer>();
-      else if (D > 3 && done + D - 3 < total)
-        wait_loads<(D > 3 ? D - 3 : 0) * kPer>();
-      else
-        wait_loads<0>();
-      lds_barrier();
-      if (done + D - 1 < total) issue();  // into the chunk that all have left behind
-      const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at * w2_chunk<CT>());
-      const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at * w2_chunk<CT>() + 16384) + w * CT * 64 + lr;
-      if (++at == D) at = 0;
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint16_t h = pp ? hv[q][1][ct] : hv[q][0][ct], hs = f2h(h2f(h) * 0x1p-11f);
+        hh[ct] = h | ((uint32_t)h << 16);
+        hl[ct] = hs | ((uint32_t)hs << 16);
+      }
+      for (int c = 0; c < nch; ++c) {
+        wait_loads<0>();  // the chunk has landed: this wave's part, then everybody's
+        lds_barrier();
+        if (fpath < paths) issue();  // the next, into the place that all have left behind
+        const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at) + lane;
+        const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + KW * RT * 4096) + w * KW * CT * 32 + lr;
+        at ^= kChunk;
+        const int steps = (A.s - 32 * KW * c + 15) >> 4;  // blocks of 16 columns that are not padding
+        u32x4 t[2][RT][2];                                // [half][row tile][plane]
+        uint32_t wd[CT];
+        auto read = [&](int st) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int it = 2 * c + i;
-        if (it >= nit) break;
-        const int pp = it >= A.Wk;
-        uint32_t wd[CT], ph[CT], pl[CT];
+          for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          wd[ct] = wl[i * CT * 32 + ct * 32] << (4 * lh);
-          ph[ct] = pp ? hh[q][1][ct] : hh[q][0][ct];
-          pl[ct] = pp ? hl[q][1][ct] : hl[q][0][ct];
-        }
+            for (int k = 0; k < 2; ++k)
+              t[st & 1][rt][k] = tl[(rt * KW + (st >> 1)) * 256 + ((st & 1) * 2 + k) * 64];
+        };
+        auto multiply = [&](int st) {
+          if ((st & 1) == 0) {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          if (st == 1 && A.s - 32 * (it - pp * A.Wk) <= 16) break;  // the word's second half is padding
-          u32x4 t[2][2];
-#pragma unroll
-          for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) t[rt][k] = tl[(rt * 2 + i) * 256 + (st * 2 + k) * 64 + lane];
+            for (int ct = 0; ct < CT; ++ct) wd[ct] = wl[(st >> 1) * CT * 32 + ct * 32] << (4 * lh);
+          }
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
-            const half8_t bh = flip(splat(ph[ct]), wd[ct] << (8 * st)), bl = flip(splat(pl[ct]), wd[ct] << (8 * st));
+            const uint32_t sh = wd[ct] << (8 * (st & 1));
+            const half8_t bh = flip(splat(hh[ct]), sh), bl = kApart ? bh : flip(splat(hl[ct]), sh);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int rt = 0; rt < 2; ++rt)
-                acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[rt][k]), k ? bl : bh, acc[q][rt][ct],
-                                                                        0, 0, 0);
+              for (int rt = 0; rt < RT; ++rt) {
+                float16_t &a = kApart && k ? low[q] : acc[q][rt][ct];
+                a = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][k]), k ? bl : bh, a, 0, 0, 0);
+              }
           }
+        };
+        read(0);
+#pragma unroll
+        for (int st = 0; st < 2 * KW; ++st) {
+          if (st >= steps) break;
+          if (st + 1 < 2 * KW) read(st + 1);
+          multiply(st);
         }
       }
     }
+  if constexpr (kApart) {
+#pragma unroll
+    for (int q = 0; q < G; ++q) acc[q][0][0] += low[q] * 0x1p-11f;
   }
   __syncthreads();
-  float *lds = reinterpret_cast<float *>(sm) + w * 32 * kPitch;
+  float *lds = reinterpret_cast<float *>(sm) + w * 32 * pitch2<kEp>();
 #pragma unroll
-  for (int rt = 0; rt < 2; ++rt) {
+  for (int rt = 0; rt < RT; ++rt) {
     if (rt * 32 >= n) break;
 #pragma unroll
-    for (int cp = 0; cp < CT; cp += 2) {
-      const float16_t up[2] = {acc[0][rt][cp], acc[0][rt][cp + 1]};
-      const float16_t gate[2] = {acc[G - 1][rt][cp], acc[G - 1][rt][cp + 1]};
-      if (j0 + cp * 32 < A.b) finish<G, 2>(A, e, row0, n, rt, j0 + cp * 32, up, gate, lds);
+    for (int cp = 0; cp < CT; cp += kEp) {
+      float16_t up[kEp], gate[kEp];
+#pragma unroll
+      for (int i = 0; i < kEp; ++i) {
+        up[i] = acc[0][rt][cp + i];
+        gate[i] = acc[G - 1][rt][cp + i];
+      }
+      if (j0 + cp * 32 < A.b) finish<G, kEp>(A, e, row0, n, rt, j0 + cp * 32, up, gate, lds);
     }
   }
 }
@@ -820,7 +944,8 @@ struct lb_bank {
   int E = 0, G = 1, device = 0;
   lb_layer *first = nullptr;
   int64_t a = 0, b = 0;
-  LayerDesc *desc = nullptr;
+  LayerDesc *desc = nullptr;     // [side][layer], on the device
+  std::vector<LayerDesc> host;   // the same on the host
   uint16_t *T = nullptr;
   int64_t parts = 0;  // 32-row parts that T holds
   std::vector<void *> retired;
@@ -833,10 +958,12 @@ size_t part_bytes(const lb_bank *B) {
   return (size_t)B->G * Ly.P * Ly.Wk * 2048 * 2;
 }
 
-// The most 32-row parts a call of up to `rows` rows makes, at either slot
-// size, within the budget (at least one 64-row slot).
+// The most 32-row parts of T that a call of up to `rows` rows makes, at any
+// slot size (16-row slots take a part each), within the budget (at least one
+// 64-row slot).
 int64_t parts_for(const lb_bank *B, int64_t rows) {
-  const int64_t most = (rows / 64 + 1 + std::min<int64_t>(B->E, rows)) * 2;
+  const int64_t few = std::min<int64_t>(rows, 16 * (int64_t)B->E);  // 16-row slots are for no more rows
+  const int64_t most = std::max((rows / 64 + 1 + std::min<int64_t>(B->E, rows)) * 2, few / 16 + 1 + std::min<int64_t>(B->E, few));
   const int64_t cap = std::max<int64_t>(2, (int64_t)(kTBudget / part_bytes(B)) / 2 * 2);
   return std::min(most, cap);
 }
@@ -855,7 +982,8 @@ lb_status grow(lb_bank *B, int64_t rows, const char *who, bool in_call, hipStrea
   }
   const int64_t parts = std::max(need, std::min(2 * B->parts, parts_for(B, kMaxRows)));
   void *t = nullptr;
-  const hipError_t e = hipMalloc(&t, (size_t)parts * part_bytes(B));
+  // the many-row kernels read up to three words past a part's end
+  const hipError_t e = hipMalloc(&t, (size_t)parts * part_bytes(B) + 16384);
   if (e != hipSuccess) return set_error(LB_ENOMEM, pre + "hipMalloc: " + hipGetErrorString(e));
   if (B->T) {
     try {
@@ -870,59 +998,83 @@ lb_status grow(lb_bank *B, int64_t rows, const char *who, bool in_call, hipStrea
   return LB_OK;
 }
 
-template <int G, int RT, int CT>
-hipError_t launch_second(const BankArgs &A, int slots, hipStream_t st) {
-  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
-  const size_t lds = (size_t)4 * 32 * pitch2<CT>() * sizeof(float);
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void *)k_bank_second<G, RT, CT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  k_bank_second<G, RT, CT><<<dim3((unsigned)(slots * ncb)), dim3(256), lds, st>>>(A);
+template <int NW>
+hipError_t launch_first16(const BankArgs &A, int slots, hipStream_t st) {
+  const dim3 grid((unsigned)(A.G * A.P * A.Wk * 2), (unsigned)slots);
+  if (A.xvec)
+    k_bank_first16<NW, true><<<grid, dim3(NW * 64), 0, st>>>(A);
+  else
+    k_bank_first16<NW, false><<<grid, dim3(NW * 64), 0, st>>>(A);
   return hipGetLastError();
 }
 
-template <int RT, int CT>
-hipError_t launch_first_wide(const BankArgs &A, int slots, int ncs, hipStream_t st) {
-  const dim3 grid((unsigned)((slots + 7) / 8 * 8 * A.G * A.P * ncs));
-  constexpr int lds = w1_lds<RT, CT>();
-  const void *f = A.xvec ? (const void *)k_bank_first_wide<RT, CT, true> : (const void *)k_bank_first_wide<RT, CT, false>;
+template <int G, int CT, int NW, int U>
+hipError_t launch_second16(const BankArgs &A, int slots, hipStream_t st) {
+  const dim3 grid((unsigned)((A.b + 16 * CT - 1) / (16 * CT)), (unsigned)slots);
+  k_bank_second16<G, CT, NW, U><<<grid, dim3(NW * 64), 0, st>>>(A);
+  return hipGetLastError();
+}
+
+// The grid of `tiles` tiles in runs for the XCDs, `width` of them to a slot: a
+// run is a slot's tiles, or an eighth of all when there are few slots.
+unsigned xcd_grid(BankArgs &A, int64_t tiles, int width) {
+  A.span = (int)std::max<int64_t>(1, std::min<int64_t>(width, tiles / 16));
+  const int64_t runs = (tiles + A.span - 1) / A.span;
+  return (unsigned)((runs + 7) / 8 * 8 * A.span);
+}
+
+template <int RT, int CT, int NW>
+hipError_t launch_first_wide(BankArgs A, int slots, int ncs, hipStream_t st) {
+  const dim3 grid(xcd_grid(A, (int64_t)slots * A.G * A.P * ncs, A.G * A.P * ncs));
+  constexpr int lds = w1_lds<RT, CT, NW>();
+  const void *f = A.xvec ? (const void *)k_bank_first_wide<RT, CT, NW, true> : (const void *)k_bank_first_wide<RT, CT, NW, false>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
   if (A.xvec)
-    k_bank_first_wide<RT, CT, true><<<grid, dim3(kW1Waves * 64), lds, st>>>(A, slots, ncs);
+    k_bank_first_wide<RT, CT, NW, true><<<grid, dim3(NW * 64), lds, st>>>(A, slots, ncs);
   else
-    k_bank_first_wide<RT, CT, false><<<grid, dim3(kW1Waves * 64), lds, st>>>(A, slots, ncs);
+    k_bank_first_wide<RT, CT, NW, false><<<grid, dim3(NW * 64), lds, st>>>(A, slots, ncs);
   return hipGetLastError();
 }
 
-// Column tiles per workgroup: a segment's tiles in the fewest groups of at
-// most five (160 of 256 registers are sums then), spread evenly.
-template <int RT>
-hipError_t launch_first_wide(const BankArgs &A, int slots, hipStream_t st) {
-  const int ncs = (A.Wk + 4) / 5;
-  switch ((A.Wk + ncs - 1) / ncs) {
-    case 1: return launch_first_wide<RT, 1>(A, slots, ncs, st);
-    case 2: return launch_first_wide<RT, 2>(A, slots, ncs, st);
-    case 3: return launch_first_wide<RT, 3>(A, slots, ncs, st);
-    case 4: return launch_first_wide<RT, 4>(A, slots, ncs, st);
-    default: return launch_first_wide<RT, 5>(A, slots, ncs, st);
+template <int RT, int NW>
+hipError_t launch_first_wide(const BankArgs &A, int slots, int ct, hipStream_t st) {
+  const int ncs = (A.Wk + ct - 1) / ct;
+  switch (ct) {
+    case 1: return launch_first_wide<RT, 1, NW>(A, slots, ncs, st);
+    case 2: return launch_first_wide<RT, 2, NW>(A, slots, ncs, st);
+    case 3: return launch_first_wide<RT, 3, NW>(A, slots, ncs, st);
+    case 4: return launch_first_wide<RT, 4, NW>(A, slots, ncs, st);
+    default: return launch_first_wide<RT, 5, NW>(A, slots, ncs, st);
   }
 }
 
-template <int G, int CT, int D>
-hipError_t launch_second_wide(const BankArgs &A, int slots, hipStream_t st) {
-  const int ncb = (A.b + 128 * CT - 1) / (128 * CT);
-  constexpr int lds = w2_lds<CT, D>();
+// Column tiles per workgroup: a segment's tiles in the fewest groups of at
+// most five (RT = 2: 160 of 256 registers are sums then), spread evenly; fewer
+// tiles a group while that leaves CUs without a workgroup.
+template <int RT>
+hipError_t launch_first_wide(const BankArgs &A, int slots, int cus, hipStream_t st) {
+  int ncs = (A.Wk + 4) / 5;
+  while (ncs < A.Wk && (int64_t)slots * A.G * A.P * ncs < cus) ++ncs;
+  const int ct = (A.Wk + ncs - 1) / ncs;
+  if constexpr (RT == 2)
+    if ((int64_t)slots * A.G * A.P * ncs > cus) return launch_first_wide<RT, 4>(A, slots, ct, st);
+  return launch_first_wide<RT, 8>(A, slots, ct, st);
+}
+
+template <int G, int RT, int CT, int NW, int KW>
+hipError_t launch_second_wide(BankArgs A, int slots, hipStream_t st) {
+  const int ncb = (A.b + NW * 32 * CT - 1) / (NW * 32 * CT);
+  constexpr int lds = w2_lds<RT, CT, NW, KW>();
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void *)k_bank_second_wide<G, CT, D>,
+    const hipError_t e = hipFuncSetAttribute((const void *)k_bank_second_wide<G, RT, CT, NW, KW>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  k_bank_second_wide<G, CT, D><<<dim3((unsigned)((slots + 7) / 8 * 8 * ncb)), dim3(256), lds, st>>>(A, slots);
+  const dim3 grid(xcd_grid(A, (int64_t)slots * ncb, ncb));
+  k_bank_second_wide<G, RT, CT, NW, KW><<<grid, dim3(NW * 64), lds, st>>>(A, slots);
   return hipGetLastError();
 }
 
@@ -932,6 +1084,8 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   lb_status gs = grow(B, A.rows, who, true, st);
   if (gs != LB_OK) return gs;
   A.desc = B->desc;
+  A.one[0] = B->host[A.e0];
+  A.one[1] = B->host[(size_t)(B->G - 1) * B->E + A.e0];
   A.T = B->T;
   A.zero = device_zero(B->first);
   A.E = B->E;
@@ -939,33 +1093,39 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   A.s = (int)Ly.s; A.L = (int)Ly.L; A.P = Ly.P; A.G = B->G; A.R1 = (int)Ly.R1; A.Wk = (int)Ly.Wk;
   A.xvec = A.a % 8 == 0 && A.ldx % 8 == 0 && (uintptr_t)A.x % 16 == 0;
   const int wide = A.f32 ? 4 : 8;
+  A.pair = A.ldy % 2 == 0 && (uintptr_t)A.y % (A.f32 ? 8 : 4) == 0;
   A.yvec = A.ldy % wide == 0 && (uintptr_t)A.y % 16 == 0 &&
            (!A.res || (A.ldr % wide == 0 && (uintptr_t)A.res % 16 == 0));
 
   const int64_t avg = A.offsets ? (A.rows + A.E - 1) / A.E : A.rows;
   const int64_t big_wg = (int64_t)(A.rows / 64) * ((A.b + 511) / 512);
-  const bool big = avg >= 64 && big_wg >= cus;
-  A.tm = big ? 64 : 32;
-  const int64_t slots = A.offsets ? A.rows / A.tm + std::min<int64_t>(A.E, A.rows) : (A.rows + A.tm - 1) / A.tm;
-  const int per = A.tm / 32, ntile = A.G * A.P * A.Wk;
-  const int64_t window = std::min<int64_t>(B->parts / per, (int64_t)0x7fffffff / 64 / std::max(ntile * per, (A.b + 127) / 128));
+  A.lg = avg <= 16 ? 4 : avg >= 64 && big_wg >= cus ? 6 : 5;
+  const int64_t slots = A.offsets ? (A.rows >> A.lg) + std::min<int64_t>(A.E, A.rows)
+                                  : (A.rows + (1 << A.lg) - 1) >> A.lg;
+  const int per = A.lg == 6 ? 2 : 1;  // 32-row parts of T per slot
+  const int64_t tiles = std::max<int64_t>((int64_t)A.G * A.P * A.Wk, (A.b + 127) / 128);
+  const int64_t window = std::min<int64_t>({B->parts / per, (int64_t)0x7fffffff / 1024 / tiles, 65535});
   for (int64_t s0 = 0; s0 < slots; s0 += window) {
     const int ns = (int)std::min<int64_t>(window, slots - s0);
     A.slot0 = (int)s0;
-    const dim3 grid((unsigned)(ns * per * ntile));
-    hipError_t e = hipSuccess;
-    if (big)
-      e = launch_first_wide<2>(A, ns, st);
-    else if (A.xvec)
-      k_bank_first<true><<<grid, dim3(kN1Waves * 64), 0, st>>>(A);
-    else
-      k_bank_first<false><<<grid, dim3(kN1Waves * 64), 0, st>>>(A);
-    if (e == hipSuccess) e = hipGetLastError();
-    if (e == hipSuccess) {
-      if (A.G == 1)
-        e = big ? launch_second_wide<1, SCT, SD1>(A, ns, st) : launch_second<1, 1, 1>(A, ns, st);
-      else
-        e = big ? launch_second_wide<2, 2, SD2>(A, ns, st) : launch_second<2, 1, 1>(A, ns, st);
+    hipError_t e;
+    if (A.lg == 4) {
+      e = A.R1 >= 64 ? launch_first16<8>(A, ns, st) : launch_first16<4>(A, ns, st);
+      // 32 columns a workgroup when all of them start at once, else 64 (8
+      // experts of 4096 -> 11008, gated, a row each: 9.1 against 11.0 us; one
+      // row alone: 5.6 against 5.0 us)
+      const bool many = (int64_t)ns * ((A.b + 31) / 32) > 4 * cus;
+      if (e == hipSuccess)
+        e = A.G == 1 ? (many ? launch_second16<1, 4, 4, 3>(A, ns, st) : launch_second16<1, 2, 4, 3>(A, ns, st))
+                     : (many ? launch_second16<2, 4, 4, 3>(A, ns, st) : launch_second16<2, 2, 4, 3>(A, ns, st));
+    } else if (A.lg == 5) {
+      e = launch_first_wide<1>(A, ns, cus, st);
+      if (e == hipSuccess)
+        e = A.G == 1 ? launch_second_wide<1, 1, 1, 8, 4>(A, ns, st) : launch_second_wide<2, 1, 1, 8, 4>(A, ns, st);
+    } else {
+      e = launch_first_wide<2>(A, ns, cus, st);
+      if (e == hipSuccess)
+        e = A.G == 1 ? launch_second_wide<1, 2, 2, 4, 2>(A, ns, st) : launch_second_wide<2, 2, 2, 4, 2>(A, ns, st);
     }
     if (e != hipSuccess) return set_error(LB_EHIP, std::string(who) + ": " + hipGetErrorString(e));
   }
@@ -1025,11 +1185,11 @@ extern "C" lb_status lb_bank_create(lb_layer *const *layers, lb_layer *const *ga
   }
   DeviceGuard dg(layers[0]->ly.device);
   lb_bank *B = nullptr;
-  std::vector<LayerDesc> desc;
   try {
-    desc.resize((size_t)G * n);
     B = new lb_bank();
+    B->host.resize((size_t)G * n);
   } catch (...) {
+    delete B;
     return set_error(LB_ENOMEM, "lb_bank_create: host allocation");
   }
   B->E = n;
@@ -1045,14 +1205,14 @@ extern "C" lb_status lb_bank_create(lb_layer *const *layers, lb_layer *const *ga
       lb_bank_destroy(B);
       return st;
     }
-    desc[i] = {LB_G(gu32, L->ly.sv1m), LB_G(gu32, L->ly.su2m), LB_G(gu16, L->ly.g), LB_G(gu16, L->ly.l), LB_G(gu16, L->ly.h)};
+    B->host[i] = {LB_G(gu32, L->ly.sv1m), LB_G(gu32, L->ly.su2m), LB_G(gu16, L->ly.g), LB_G(gu16, L->ly.l), LB_G(gu16, L->ly.h)};
   }
-  hipError_t e = hipMalloc(&B->desc, desc.size() * sizeof(LayerDesc));
+  hipError_t e = hipMalloc(&B->desc, B->host.size() * sizeof(LayerDesc));
   if (e != hipSuccess) {
     lb_bank_destroy(B);
     return set_error(LB_ENOMEM, std::string("lb_bank_create: hipMalloc: ") + hipGetErrorString(e));
   }
-  e = hipMemcpy(B->desc, desc.data(), desc.size() * sizeof(LayerDesc), hipMemcpyHostToDevice);
+  e = hipMemcpy(B->desc, B->host.data(), B->host.size() * sizeof(LayerDesc), hipMemcpyHostToDevice);
   if (e == hipSuccess) e = hipDeviceSynchronize();
   if (e != hipSuccess) {
     lb_bank_destroy(B);

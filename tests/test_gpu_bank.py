@@ -288,15 +288,17 @@ def test_grouped_offsets_are_clamped(lbm):
     B.close()
 
 
-def test_grouped_equals_forward_bit_for_bit(lbm):
-    """The same rows through lb_bank_grouped and, expert by expert, lb_bank_forward."""
+def test_grouped_and_forward_agree(lbm):
+    """The same rows through lb_bank_grouped and, expert by expert, lb_bank_forward: both within the tolerance of the
+    float64 result (the calls choose their kernels by their own row counts, so sums may be ordered differently)."""
     torch = lbtest.torch_dev()
-    say("[case] grouped equals forward")
+    say("[case] grouped and forward")
     up, ul = _layers(lbm, 200, 136, 21, True, 8, 31)
     B = lbm.Bank(ul)
     c = np.array([3, 0, 32, 33, 1, 0, 20, 8])
     off = np.concatenate([[0], np.cumsum(c)]).astype(np.int32)
-    x = _dev(lb_synth.activations(int(off[-1]), 200, seed=3))
+    xh = lb_synth.activations(int(off[-1]), 200, seed=3)
+    x = _dev(xh)
     y = torch.empty((int(off[-1]), 136), dtype=torch.float16, device="cuda")
     z = torch.empty_like(y)
     B.grouped(x, _dev(off), y, act="silu")
@@ -305,7 +307,12 @@ def test_grouped_equals_forward_bit_for_bit(lbm):
         if hi > lo:
             B.forward(x[lo:hi], z[lo:hi], expert=e, act="silu")
     torch.cuda.synchronize()
-    assert torch.equal(y, z)
+    for e in range(8):
+        lo, hi = off[e], off[e + 1]
+        if hi > lo:
+            ref, tol = bankref.fused(xh[lo:hi], up[e], act_name="silu")
+            assert_within(y[lo:hi].cpu().numpy(), ref, tol, f"grouped, expert {e}")
+            assert_within(z[lo:hi].cpu().numpy(), ref, tol, f"forward, expert {e}")
     B.close()
 
 
