@@ -85,10 +85,16 @@ struct BankArgs {
   int a, a16, b, b16, s, L, P, G, R1, Wk;
   int lg, slot0;  // rows per slot are 2^lg; first slot of this launch
   int span;       // neighbouring tiles that go to one XCD (many-row kernels)
-  int act, f32, xvec, yvec, pair;  // pair: y rows take stores of two elements
+  int act, f32, xvec;
 };
 
 #define LB_G(T, p) ((T)(uintptr_t)(p))
+
+// 16 and 4 bytes at an element's alignment: global memory takes them as one
+// access (with eight 2-byte ones 1023 rows of 1031 -> 2743 took 23.7 us, not
+// 17.3).
+typedef u32x4 __attribute__((aligned(2), address_space(1))) loose128;
+typedef uint32_t __attribute__((aligned(2), address_space(1))) loose32;
 
 __device__ __forceinline__ float h2f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
 __device__ __forceinline__ uint16_t f2h(float v) { return __half_as_ushort(__float2half_rn(v)); }
@@ -162,12 +168,10 @@ __device__ __forceinline__ LayerDesc layer_of(const BankArgs &A, int side, int e
 // zeros past a.
 template <bool XV>
 __device__ __forceinline__ u32x4 load8(const uint16_t *p) {
-  typedef u32x4 __attribute__((aligned(2))) loose;
-  typedef const loose __attribute__((address_space(1))) *gloose;
   if constexpr (XV)
     return *LB_G(gu128, p);
   else
-    return *LB_G(gloose, p);
+    return *LB_G(const loose128 *, p);
 }
 template <bool XV>
 __device__ __forceinline__ u32x4 load_x(const BankArgs &A, const uint16_t *row, int i) {
@@ -590,41 +594,44 @@ __device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = lds[row * kPitch + c8 * 8 + i];
-    const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
-    if (A.yvec && j + 8 <= A.b) {
+const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
+    if (j + 8 <= A.b) {
       if (A.f32) {
-        if (A.res) {
-          const float4 r0 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[0];
-          const float4 r1 = reinterpret_cast<const float4 *>((const float *)A.res + ro)[1];
-          v[0] += r0.x; v[1] += r0.y; v[2] += r0.z; v[3] += r0.w;
-          v[4] += r1.x; v[5] += r1.y; v[6] += r1.z; v[7] += r1.w;
+        float *y = (float *)A.y + yo;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u32x4 o;
+          if (A.res) {
+            const u32x4 r = *LB_G(const loose128 *, (const float *)A.res + ro + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * h + i] += __uint_as_float(r[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = __float_as_uint(v[4 * h + i]);
+          *LB_G(loose128 *, y + 4 * h) = o;
         }
-        float4 *dst = reinterpret_cast<float4 *>((float *)A.y + yo);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
       } else {
+        u32x4 o;
         if (A.res) {
-          const u32x4 r = *reinterpret_cast<const u32x4 *>((const uint16_t *)A.res + ro);
+          const u32x4 r = *LB_G(const loose128 *, (const uint16_t *)A.res + ro);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             v[2 * i] += h2f((uint16_t)(r[i] & 0xffffu));
             v[2 * i + 1] += h2f((uint16_t)(r[i] >> 16));
           }
         }
-        u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = f2h(v[2 * i]) | ((uint32_t)f2h(v[2 * i + 1]) << 16);
-        *reinterpret_cast<u32x4 *>((uint16_t *)A.y + yo) = o;
+        *LB_G(loose128 *, (uint16_t *)A.y + yo) = o;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (j + i >= A.b) break;
-        if (A.f32) {
+        if (A.f32)
           ((float *)A.y)[yo + i] = v[i] + (A.res ? ((const float *)A.res)[ro + i] : 0.f);
-        } else {
+        else
           ((uint16_t *)A.y)[yo + i] = f2h(v[i] + (A.res ? h2f(((const uint16_t *)A.res)[ro + i]) : 0.f));
-        }
       }
     }
   }
@@ -734,12 +741,8 @@ k_bank_second16(BankArgs A) {
         v[0] += r[0];
         if (two) v[1] += r[1];
       }
-      if (A.pair && two) {
-        *reinterpret_cast<float2 *>(y) = make_float2(v[0], v[1]);
-      } else {
-        y[0] = v[0];
-        if (two) y[1] = v[1];
-      }
+      y[0] = v[0];
+      if (two) y[1] = v[1];
     } else {
       uint16_t *y = (uint16_t *)A.y + yo;
       if (A.res) {
@@ -747,12 +750,10 @@ k_bank_second16(BankArgs A) {
         v[0] += h2f(r[0]);
         if (two) v[1] += h2f(r[1]);
       }
-      if (A.pair && two) {
-        *reinterpret_cast<uint32_t *>(y) = f2h(v[0]) | ((uint32_t)f2h(v[1]) << 16);
-      } else {
+      if (two)
+        *LB_G(loose32 *, y) = f2h(v[0]) | ((uint32_t)f2h(v[1]) << 16);
+      else
         y[0] = f2h(v[0]);
-        if (two) y[1] = f2h(v[1]);
-      }
     }
   }
 }
@@ -784,10 +785,32 @@ k_bank_second_wide(BankArgs A, int slots) {
   const int tile = xcd_tile(A.span), slot = tile / ncb, cb = tile - slot * ncb;
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
   const int j0 = (cb * NW + w) * 32 * CT;
-  int e, row0, n;
-  if (slot >= slots || !find_slot(A, A.slot0 + slot, e, row0, n)) return;
+  if (slot >= slots) return;
 
   const int nch = (A.Wk + KW - 1) / KW;  // chunks of a path
+  // The wave's copies of a chunk, at addresses that only advance: kT KB of T
+  // from piece tu of the chunk on (past a path's last word they read on, T has
+  // room behind it), and its words (the last one again past it); with CT = 1
+  // two words of its 32 columns at once.  T does not depend on the expert, so
+  // its first chunk is on its way before the slot is looked up.
+  const int tu = w * kT;
+  const uint16_t *src[kT];
+#pragma unroll
+  for (int f = 0; f < kT; ++f) {
+    const int u = tu + f, rt = u / (KW * 4), piece = u % (KW * 4);
+    src[f] = A.T + ((size_t)(slot * RT + rt) * G * A.P * A.Wk) * 2048 + piece * 512 + lane * 8;
+  }
+  int fpath = 0, fc = 0, fs = 0;  // the next chunk's path (of all sides), number in it, and place
+  auto issue_t = [&]() {
+#pragma unroll
+    for (int f = 0; f < kT; ++f) dma16(src[f], sm + fs + (tu + f) * 1024);
+  };
+  issue_t();
+  int e, row0, n;
+  if (!find_slot(A, A.slot0 + slot, e, row0, n)) {
+    wait_loads<0>();  // the copies land before the LDS is left
+    return;
+  }
   const LayerDesc D0 = layer_of(A, 0, e), D1 = layer_of(A, G - 1, e);
   float16_t acc[G][RT][CT], low[G];
 #pragma unroll
@@ -811,28 +834,13 @@ k_bank_second_wide(BankArgs A, int slots) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) hv[q][pp][ct] = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + jc[ct]];
 
-  // The wave's copies of a chunk, at addresses that only advance: kT KB of T
-  // from piece tu of the chunk on (past a path's last word they read on, T has
-  // room behind it), and its words (the last one again past it); with CT = 1
-  // two words of its 32 columns at once.
-  const int tu = w * kT;
-  const uint16_t *src[kT];
-#pragma unroll
-  for (int f = 0; f < kT; ++f) {
-    const int u = tu + f, rt = u / (KW * 4), piece = u % (KW * 4);
-    src[f] = A.T + ((size_t)(slot * RT + rt) * G * A.P * A.Wk) * 2048 + piece * 512 + lane * 8;
-  }
   unsigned jw[(CT + 1) / 2];
 #pragma unroll
   for (int c = 0; c < (CT + 1) / 2; ++c) jw[c] = min(j0 + c * 64 + (CT == 1 ? lr : lane), A.b16 - 1);
-  gu32 row = D0.su;             // of the next word
-  int fpath = 0, fc = 0, fs = 0;  // the next chunk's path (of all sides), number in it, and place
-  auto issue = [&]() {
-    unsigned char *dst = sm + fs;
+  gu32 row = D0.su;  // of the next word
+  auto issue_w = [&]() {
     const int left = A.Wk - fc * KW;  // words of the path from here on
-#pragma unroll
-    for (int f = 0; f < kT; ++f) dma16(src[f], dst + (tu + f) * 1024);
-    unsigned char *wdst = dst + KW * RT * 4096 + w * KW * CT * 128;
+    unsigned char *wdst = sm + fs + KW * RT * 4096 + w * KW * CT * 128;
 #pragma unroll
     for (int i = 0; i < KW; i += CT == 1 ? 2 : 1) {
       const gu32 r = row + (size_t)min(i, left - 1) * A.b16;
@@ -853,7 +861,7 @@ k_bank_second_wide(BankArgs A, int slots) {
     }
     fs ^= kChunk;
   };
-  issue();
+  issue_w();
   const int paths = G * A.P;
   int at = 0;
 #pragma unroll
@@ -869,7 +877,10 @@ k_bank_second_wide(BankArgs A, int slots) {
       for (int c = 0; c < nch; ++c) {
         wait_loads<0>();  // the chunk has landed: this wave's part, then everybody's
         lds_barrier();
-        if (fpath < paths) issue();  // the next, into the place that all have left behind
+        if (fpath < paths) {  // the next, into the place that all have left behind
+          issue_t();
+          issue_w();
+        }
         const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at) + lane;
         const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + KW * RT * 4096) + w * KW * CT * 32 + lr;
         at ^= kChunk;
@@ -1092,11 +1103,6 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   A.a = (int)Ly.a; A.a16 = (int)Ly.a16; A.b = (int)Ly.b; A.b16 = (int)Ly.b16;
   A.s = (int)Ly.s; A.L = (int)Ly.L; A.P = Ly.P; A.G = B->G; A.R1 = (int)Ly.R1; A.Wk = (int)Ly.Wk;
   A.xvec = A.a % 8 == 0 && A.ldx % 8 == 0 && (uintptr_t)A.x % 16 == 0;
-  const int wide = A.f32 ? 4 : 8;
-  A.pair = A.ldy % 2 == 0 && (uintptr_t)A.y % (A.f32 ? 8 : 4) == 0;
-  A.yvec = A.ldy % wide == 0 && (uintptr_t)A.y % 16 == 0 &&
-           (!A.res || (A.ldr % wide == 0 && (uintptr_t)A.res % 16 == 0));
-
   const int64_t avg = A.offsets ? (A.rows + A.E - 1) / A.E : A.rows;
   const int64_t big_wg = (int64_t)(A.rows / 64) * ((A.b + 511) / 512);
   A.lg = avg <= 16 ? 4 : avg >= 64 && big_wg >= cus ? 6 : 5;

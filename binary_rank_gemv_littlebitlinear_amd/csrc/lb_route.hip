@@ -10,8 +10,8 @@
 // offsets[e + 1] - 1, in the order of the tokens.
 //
 // Choosing takes a wave per token: each lane holds its experts' keys (the
-// logit's order as an unsigned number, then the lowest index) and the wave
-// takes the largest k times.  Sorting is counting: rows per expert of every
+// logit's order as an unsigned number) and the wave takes the largest, of the
+// lowest expert that has it, k times.  Sorting is counting: rows per expert of every
 // block of tokens, then each block places its own rows behind those of the
 // blocks before it, 64 rows of a wave at a time (lanes with the same expert
 // find one another by ballots over the bits of its number).  Counts are
@@ -44,15 +44,57 @@ struct RouteArgs {
   int *hist;  // [block][E]
 };
 
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 __device__ __forceinline__ float h2f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
 
-// One wave: the choices of token t.
+// Reductions over the wave by DPP moves (a few cycles a step; shuffles through
+// LDS made choosing 6 of 64 experts for 16384 tokens take 21 us instead of
+// 11.8): lane 63 ends up with the result.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+constexpr int kShr1 = 0x111, kShr2 = 0x112, kShr4 = 0x114, kShr8 = 0x118, kBcast15 = 0x142, kBcast31 = 0x143;
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp<kShr1, 0xf>(v));
+  v = max(v, dpp<kShr2, 0xf>(v));
+  v = max(v, dpp<kShr4, 0xf>(v));
+  v = max(v, dpp<kShr8, 0xf>(v));
+  v = max(v, dpp<kBcast15, 0xa>(v));
+  v = max(v, dpp<kBcast31, 0xc>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float f) {
+  auto add = [&](uint32_t o) { f += __uint_as_float(o); };
+  add(dpp<kShr1, 0xf>(__float_as_uint(f)));
+  add(dpp<kShr2, 0xf>(__float_as_uint(f)));
+  add(dpp<kShr4, 0xf>(__float_as_uint(f)));
+  add(dpp<kShr8, 0xf>(__float_as_uint(f)));
+  add(dpp<kBcast15, 0xa>(__float_as_uint(f)));
+  add(dpp<kBcast31, 0xc>(__float_as_uint(f)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
+}
+
+// exp(z - top), 1 for the top itself (also when it is infinite).
+__device__ __forceinline__ float part(float z, float top) { return z == top ? 1.f : expf(z - top); }
+
+// A logit as an unsigned number of the same order, 0 for what cannot be
+// chosen (-inf, NaN); and back.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.f);  // -0 and 0 are equal
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+// The lane's keys of token t: expert i * 64 + lane in key[i].
 template <int NV>
-__device__ __forceinline__ void choose(const RouteArgs &A, int t) {
+__device__ __forceinline__ void load_keys(const RouteArgs &A, int t, uint32_t (&key)[NV]) {
   const int lane = threadIdx.x & 63;
-  float z[NV];
-  uint32_t key[NV];  // order-preserving; 0 for what cannot be chosen
-  float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = i * 64 + lane;
@@ -61,76 +103,80 @@ __device__ __forceinline__ void choose(const RouteArgs &A, int t) {
       const int64_t o = (int64_t)t * A.ld + e;
       v = A.f32 ? ((const float *)A.logits)[o] : h2f(((const uint16_t *)A.logits)[o]);
     }
-    if (v != v) v = -INFINITY;
-    z[i] = v;
-    if (v == 0.f) v = 0.f;  // -0 and 0 are equal
-    const uint32_t u = __float_as_uint(v);
-    key[i] = v == -INFINITY ? 0u : (u & 0x80000000u ? ~u : u | 0x80000000u);
-    top = fmaxf(top, v);
+    key[i] = key_of(v);
   }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  float all = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    z[i] = key[i] ? (z[i] == top ? 1.f : expf(z[i] - top)) : 0.f;
-    all += z[i];
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d);
-  float mine = 0.f, sum = 0.f;
+}
+
+// One wave: the choices of token t from its keys.
+template <int NV>
+__device__ __forceinline__ void choose(const RouteArgs &A, int t, uint32_t (&key)[NV]) {
+  const int lane = threadIdx.x & 63;
+  float mine = 0.f, all = 0.f, top = 0.f;
   int my_id = -1;
   for (int j = 0; j < A.k; ++j) {
-    uint64_t best = 0;
-    float p = 0.f;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint64_t c = key[i] ? ((uint64_t)key[i] << 32) | (uint32_t)(kMaxE - 1 - (i * 64 + lane)) : 0ull;
-      if (c > best) {
-        best = c;
-        p = z[i];
+    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+    const uint32_t win = wave_max(best);
+    if (win == 0u) break;  // nothing left
+    if (j == 0) {
+      top = logit_of(win);
+      if (!A.renorm) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) all += key[i] ? part(logit_of(key[i]), top) : 0.f;
       }
     }
-    uint64_t win = best;
+    // the lowest expert that has it
+    int id = -1;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)win, d);
-      win = o > win ? o : win;
+    for (int i = 0; i < NV; ++i) {
+      const unsigned long long m = __ballot(key[i] == win);
+      if (id < 0 && m) id = i * 64 + __ffsll(m) - 1;
     }
-    const bool found = win != 0;
-    const int id = found ? kMaxE - 1 - (int)(uint32_t)win : -1;
-    p = __shfl(p, id & 63);
-    if (!found) p = 0.f;
-    sum += p;
     if (lane == j) {
-      mine = p;
+      mine = part(logit_of(win), top);
       my_id = id;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (found && i * 64 + lane == id) key[i] = 0u;
+      if (i * 64 + lane == id) key[i] = 0u;
   }
+  const float den = wave_sum(A.renorm ? mine : all);
   if (lane < A.k) {
-    const float den = A.renorm ? sum : all;
     A.ids[(int64_t)t * A.k + lane] = my_id;
     A.weights[(int64_t)t * A.k + lane] = my_id >= 0 ? mine / den : 0.f;
   }
 }
 
-__device__ __forceinline__ void choose_any(const RouteArgs &A, int t) {
+// The wave's tokens: t, t + kWaves, ... below t1, the next one's logits on
+// their way meanwhile.
+template <int NV>
+__device__ __forceinline__ void choose_tokens(const RouteArgs &A, int t, int t1) {
+  if (t >= t1) return;
+  uint32_t key[NV];
+  load_keys<NV>(A, t, key);
+  for (; t < t1; t += kWaves) {
+    uint32_t next[NV];
+    load_keys<NV>(A, min(t + kWaves, t1 - 1), next);
+    choose<NV>(A, t, key);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = next[i];
+  }
+}
+
+__device__ __forceinline__ void choose_all(const RouteArgs &A, int t, int t1) {
   if (A.E <= 64)
-    choose<1>(A, t);
+    choose_tokens<1>(A, t, t1);
   else if (A.E <= 256)
-    choose<4>(A, t);
+    choose_tokens<4>(A, t, t1);
   else
-    choose<16>(A, t);
+    choose_tokens<16>(A, t, t1);
 }
 
 // The lanes whose id equals this lane's (id >= 0), by ballots over its bits.
-__device__ __forceinline__ unsigned long long same_id(int id) {
+__device__ __forceinline__ unsigned long long same_id(int id, int bits) {
   unsigned long long m = __ballot(id >= 0);
-#pragma unroll
-  for (int b = 0; b < 10; ++b) {
+  for (int b = 0; b < bits; ++b) {
     const unsigned long long v = __ballot((id >> b) & 1);
     m &= (id >> b) & 1 ? v : ~v;
   }
@@ -141,7 +187,8 @@ __device__ __forceinline__ unsigned long long same_id(int id) {
 // expert e in earlier blocks; total[e]: in all blocks; both in LDS and both
 // given unless `alone` (then counted here).
 __device__ void place(const RouteArgs &A, int t0, int t1, int *cnt, int *start, int *total, bool alone, bool first) {
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, w = wave_id(), lane = tid & 63;
+  const int bits = 32 - __clz(A.E - 1 | 1);
   const int64_t n0 = (int64_t)t0 * A.k;
   const int N = (t1 - t0) * A.k;
   const int per = ((N + kWaves - 1) / kWaves + 63) & ~63;
@@ -150,7 +197,7 @@ __device__ void place(const RouteArgs &A, int t0, int t1, int *cnt, int *start, 
   __syncthreads();
   for (int i = lo; i < hi; i += 64) {
     const int id = i + lane < hi ? A.ids[n0 + i + lane] : -1;
-    const unsigned long long m = same_id(id);
+    const unsigned long long m = same_id(id, bits);
     if (id >= 0 && (m & ((1ull << lane) - 1)) == 0) cnt[w * A.E + id] += __popcll(m);
   }
   __syncthreads();
@@ -198,11 +245,11 @@ __device__ void place(const RouteArgs &A, int t0, int t1, int *cnt, int *start, 
     const int64_t at = n0 + i + lane;
     const bool in = i + lane < hi;
     const int id = in ? A.ids[at] : -1;
-    const unsigned long long m = same_id(id), less = m & ((1ull << lane) - 1);
+    const unsigned long long m = same_id(id, bits), less = m & ((1ull << lane) - 1);
     int r = -1;
     if (id >= 0) {
       r = cnt[w * A.E + id] + __popcll(less);
-      A.token[r] = (int)(at / A.k);
+      A.token[r] = (int)((unsigned)at / (unsigned)A.k);  // at < 2^30
     }
     if (in) A.row[at] = r;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -219,7 +266,7 @@ __device__ void place(const RouteArgs &A, int t0, int t1, int *cnt, int *start, 
 
 __global__ void __launch_bounds__(kThreads) k_route_one(RouteArgs A) {
   extern __shared__ int sh[];  // cnt [16][E], start [E], total [E]
-  for (int t = threadIdx.x >> 6; t < A.T; t += kWaves) choose_any(A, t);
+  choose_all(A, wave_id(), A.T);
   __threadfence_block();
   __syncthreads();
   place(A, 0, A.T, sh, sh + kWaves * A.E, sh + (kWaves + 1) * A.E, true, true);
@@ -229,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) k_route_choose(RouteArgs A) {
   extern __shared__ int sh[];  // [E]
   const int t0 = blockIdx.x * A.tb, t1 = min(A.T, t0 + A.tb);
   for (int e = threadIdx.x; e < A.E; e += kThreads) sh[e] = 0;
-  for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kWaves) choose_any(A, t);
+  choose_all(A, t0 + wave_id(), t1);
   __threadfence_block();
   __syncthreads();
   const int64_t n0 = (int64_t)t0 * A.k;
@@ -250,10 +297,15 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs A) {
   const int ng = max(1, kThreads / A.E), e0 = threadIdx.x % A.E, gq = threadIdx.x / A.E;
   if (gq < ng) {
     int before = 0, all = 0;
-    for (int q = gq; q < nb; q += ng) {
-      const int v = A.hist[(int64_t)q * A.E + e0];
-      all += v;
-      if (q < b) before += v;
+    for (int q0 = gq; q0 < nb; q0 += 8 * ng) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = q0 + u * ng < nb ? A.hist[(int64_t)(q0 + u * ng) * A.E + e0] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        all += v[u];
+        if (q0 + u * ng < b) before += v[u];
+      }
     }
     atomicAdd(&start[e0], before);
     atomicAdd(&total[e0], all);
@@ -265,8 +317,10 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs A) {
 
 // ------------------------------------------------------------- combining
 // out[t] = residual[t] + sum_j weights[t, j] y[row[t, j]] in the order of j,
-// fp32, rounded once.  Bound by reading y and writing out.  A thread takes V
-// neighbouring columns (16 bytes of y) of one token.
+// fp32, rounded once.  Bound by reading y and writing out (8192 tokens of 2
+// rows of 4096 and a residual: 269 MB in 50 us, 5.3 TB/s, what a large copy
+// reaches).  A thread takes 8 neighbouring columns (16 bytes of y) of one
+// token.
 struct CombineArgs {
   const uint16_t *y;
   const int *row;
@@ -277,64 +331,69 @@ struct CombineArgs {
   int y_rows, T, k, f32, nb;  // nb: workgroups per token
 };
 
-template <int V>
+// 16 bytes at an element's alignment (global memory takes them as one access).
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 __attribute__((aligned(2), address_space(1))) loose128;
+#define LB_LOOSE(p) ((loose128 *)(uintptr_t)(p))
+
+__device__ __forceinline__ void add8(float (&acc)[8], u32x4 q, float w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(w, h2f((uint16_t)(q[i] & 0xffffu)), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, h2f((uint16_t)(q[i] >> 16)), acc[2 * i + 1]);
+  }
+}
+
 __global__ void __launch_bounds__(256) k_route_combine(CombineArgs A) {
-  const int t = blockIdx.x / A.nb, c = ((blockIdx.x - t * A.nb) * 256 + threadIdx.x) * V;
+  const int t = blockIdx.x / A.nb, c = ((blockIdx.x - t * A.nb) * 256 + threadIdx.x) * 8;
   if (c >= A.width) return;
-  float acc[V];
+  const int64_t ro = (int64_t)t * A.ldr + c, oo = (int64_t)t * A.ldo + c;
+  const int *row = A.row + (int64_t)t * A.k;
+  const float *weights = A.weights + (int64_t)t * A.k;
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int j = 0; j < A.k; ++j) {
-    const int r = A.row[(int64_t)t * A.k + j];
-    if (r < 0 || r >= A.y_rows) continue;
-    const float w = A.weights[(int64_t)t * A.k + j];
-    const uint16_t *src = A.y + (int64_t)r * A.ldy + c;
-    if constexpr (V == 8) {
-      const uint4 q = *reinterpret_cast<const uint4 *>(src);
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  if (c + 8 <= A.width) {
+    for (int j = 0; j < A.k; ++j) {
+      const int r = row[j];
+      if (r < 0 || r >= A.y_rows) continue;
+      add8(acc, *LB_LOOSE(A.y + (int64_t)r * A.ldy + c), weights[j]);
+    }
+    if (A.f32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(w, h2f((uint16_t)(u[i] & 0xffffu)), acc[2 * i]);
-        acc[2 * i + 1] = fmaf(w, h2f((uint16_t)(u[i] >> 16)), acc[2 * i + 1]);
+      for (int h = 0; h < 2; ++h) {
+        u32x4 o;
+        if (A.res) {
+          const u32x4 r = *LB_LOOSE((const float *)A.res + ro + 4 * h);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[4 * h + i] += __uint_as_float(r[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __float_as_uint(acc[4 * h + i]);
+        *LB_LOOSE((float *)A.out + oo + 4 * h) = o;
       }
     } else {
-      acc[0] = fmaf(w, h2f(*src), acc[0]);
+      if (A.res) add8(acc, *LB_LOOSE((const uint16_t *)A.res + ro), 1.f);
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = __half_as_ushort(__float2half_rn(acc[2 * i])) |
+               ((uint32_t)__half_as_ushort(__float2half_rn(acc[2 * i + 1])) << 16);
+      *LB_LOOSE((uint16_t *)A.out + oo) = o;
     }
+    return;
   }
-  const int64_t ro = (int64_t)t * A.ldr + c, oo = (int64_t)t * A.ldo + c;
-  if constexpr (V == 8) {
-    if (A.f32) {
-      if (A.res) {
-        const float4 *r = reinterpret_cast<const float4 *>((const float *)A.res + ro);
-        const float4 r0 = r[0], r1 = r[1];
-        acc[0] += r0.x; acc[1] += r0.y; acc[2] += r0.z; acc[3] += r0.w;
-        acc[4] += r1.x; acc[5] += r1.y; acc[6] += r1.z; acc[7] += r1.w;
-      }
-      float4 *o = reinterpret_cast<float4 *>((float *)A.out + oo);
-      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      return;
+  for (int i = 0; c + i < A.width; ++i) {  // the row's last, incomplete piece
+    float v = 0.f;
+    for (int j = 0; j < A.k; ++j) {
+      const int r = row[j];
+      if (r >= 0 && r < A.y_rows) v = fmaf(weights[j], h2f(A.y[(int64_t)r * A.ldy + c + i]), v);
     }
-    if (A.res) {
-      const uint4 q = *reinterpret_cast<const uint4 *>((const uint16_t *)A.res + ro);
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] += h2f((uint16_t)(u[i] & 0xffffu));
-        acc[2 * i + 1] += h2f((uint16_t)(u[i] >> 16));
-      }
-    }
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = __half_as_ushort(__float2half_rn(acc[2 * i])) |
-             ((uint32_t)__half_as_ushort(__float2half_rn(acc[2 * i + 1])) << 16);
-    *reinterpret_cast<uint4 *>((uint16_t *)A.out + oo) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else if (A.f32) {
-    ((float *)A.out)[oo] = acc[0] + (A.res ? ((const float *)A.res)[ro] : 0.f);
-  } else {
-    ((uint16_t *)A.out)[oo] =
-        __half_as_ushort(__float2half_rn(acc[0] + (A.res ? h2f(((const uint16_t *)A.res)[ro]) : 0.f)));
+    if (A.f32)
+      ((float *)A.out)[oo + i] = v + (A.res ? ((const float *)A.res)[ro + i] : 0.f);
+    else
+      ((uint16_t *)A.out)[oo + i] =
+          __half_as_ushort(__float2half_rn(v + (A.res ? h2f(((const uint16_t *)A.res)[ro + i]) : 0.f)));
   }
 }
 
@@ -444,11 +503,7 @@ extern "C" lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy
   A.ldy = ldy; A.ldr = ldr; A.ldo = ldo; A.width = width;
   A.y_rows = (int)y_rows; A.k = k;
   A.f32 = out_type == LB_F32;
-  const int wide = A.f32 ? 4 : 8;
-  const bool vec = width % 8 == 0 && ldy % 8 == 0 && (uintptr_t)y % 16 == 0 && ldo % wide == 0 &&
-                   (uintptr_t)out % 16 == 0 && (!residual || (ldr % wide == 0 && (uintptr_t)residual % 16 == 0));
-  const int per = vec ? 2048 : 256;
-  A.nb = (int)((width + per - 1) / per);
+  A.nb = (int)((width + 2047) / 2048);
   // windows of tokens keep the grid below 2^31 threads
   const int64_t window = std::max<int64_t>(1, (int64_t)0x7fffffff / 256 / A.nb);
   for (int64_t t0 = 0; t0 < tokens; t0 += window) {
@@ -459,10 +514,7 @@ extern "C" lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy
     W.weights += t0 * k;
     W.out = (char *)out + (size_t)t0 * ldo * os;
     if (residual) W.res = (const char *)residual + (size_t)t0 * ldr * os;
-    if (vec)
-      k_route_combine<8><<<dim3((unsigned)(n * A.nb)), dim3(256), 0, (hipStream_t)stream>>>(W);
-    else
-      k_route_combine<1><<<dim3((unsigned)(n * A.nb)), dim3(256), 0, (hipStream_t)stream>>>(W);
+    k_route_combine<<<dim3((unsigned)(n * A.nb)), dim3(256), 0, (hipStream_t)stream>>>(W);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_route_combine: ") + hipGetErrorString(e));
   }
