@@ -558,8 +558,9 @@ constexpr int pitch2() { return 32 * CT + 4; }
 
 // The epilogue of one 32-row tile (rows 32 rt .. of the slot) and 32 CT columns
 // from j0 on: up and gate hold the wave's accumulators (gate unused unless
-// G = 2), lds 32 x (32 CT + 4) floats of the wave's own.
-template <int G, int CT>
+// G = 2; already activated with READY), lds 32 x (32 CT + 4) floats of the
+// wave's own.
+template <int G, int CT, bool READY = false>
 __device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n, int rt, int j0,
                                        const float16_t (&up)[CT], const float16_t (&gate)[CT], float *lds) {
   constexpr int kPitch = pitch2<CT>();
@@ -569,15 +570,17 @@ __device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n
   for (int ct = 0; ct < CT; ++ct) {
     const int j = j0 + ct * 32 + lr;
     bu[ct] = A.bias[0] && j < A.b ? h2f(A.bias[0][(size_t)e * A.b + j]) : 0.f;
-    bg[ct] = G == 2 && A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
+    bg[ct] = G == 2 && !READY && A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
   }
-  with_act(A.act, [&](auto act) {
+  with_act(READY ? LB_ACT_NONE : A.act, [&](auto act) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float v = up[ct][i] + bu[ct];
-        if constexpr (G == 2)
+        if constexpr (READY)
+          v = gate[ct][i] * v;
+        else if constexpr (G == 2)
           v = activate<decltype(act)::value>(gate[ct][i] + bg[ct]) * v;
         else
           v = activate<decltype(act)::value>(v);
@@ -758,52 +761,187 @@ k_bank_second16(BankArgs A) {
   }
 }
 
-// More rows: a workgroup of NW waves, 32 RT rows of one slot, every wave 32 CT
-// columns of all G sides.  T and the sign words are copied into LDS in chunks
-// of KW 32-column words of a path, the next chunk during the products of one:
-// T once for the workgroup, a wave's words by itself.  (Three or four chunks
-// on their way changed nothing.)  With two waves on a SIMD a wave
-// issues an instruction every four or five cycles at best, so what bounds this is
-// the instructions a product needs: per 16 columns and column tile 4 shifts
-// and 8 sign flips (4 when hi and lo have sums of their own), shared by RT row
-// tiles, and everything that is not per product is kept out of the loop.  An operand read serves CT expanded sign operands, one of those two
-// row tiles.
-template <int RT, int CT, int NW, int KW>
-constexpr int w2_chunk() { return KW * (RT * 4096 + NW * CT * 128); }
-template <int RT, int CT, int NW, int KW>
-constexpr int w2_lds() { return std::max(2 * w2_chunk<RT, CT, NW, KW>(), NW * 32 * pitch2<(CT > 1 ? 2 : 1)>() * 4); }
+// Between the two: a workgroup of 8 waves, 32 rows of one slot x 256 columns.
+// Four waves take one half of the words of K, four the other: with gates the
+// layer's and the gate's, without the first and the last.  So twice the waves
+// share what a row tile of 32 offers, and each expands half the signs.  Every
+// wave has 64 columns, hi and lo sums apart.  T and words go through two LDS
+// buffers, chunks of two words of each half.  At the end the second half's
+// sums (activated, with gates) pass to the first through LDS.
+constexpr int kMidT = 16384, kMidChunk = kMidT + 4096;              // T, words
+constexpr int kMidLds = 32768 + 4 * 32 * pitch2<1>() * 4;           // the sums handed over, the epilogue's rows
+static_assert(2 * kMidChunk <= kMidLds, "the chunks fit too");
 
-template <int G, int RT, int CT, int NW, int KW>
-__global__ void __launch_bounds__(NW * 64, G * RT * CT == 4 ? 4 : 2)
-k_bank_second_wide(BankArgs A, int slots) {
-  constexpr int kT = RT * KW * 4 / NW;  // T copies of a wave per chunk
-  constexpr int kChunk = w2_chunk<RT, CT, NW, KW>(), kEp = CT > 1 ? 2 : 1;
-  constexpr bool kApart = RT * CT == 1;  // hi and lo products in sums of their own: lo needs no 2^-11 h
-  static_assert(kT * NW == RT * KW * 4 && (CT == 1 ? KW % 2 == 0 : CT % 2 == 0), "the copies below");
-  extern __shared__ __align__(16) unsigned char sm[];
-  const int ncb = (A.b + NW * 32 * CT - 1) / (NW * 32 * CT);
+template <int G>
+__global__ void __launch_bounds__(512)
+k_bank_second_mid(BankArgs A, int slots) {
+  __shared__ __align__(16) unsigned char sm[kMidLds];
+  const int ncb = (A.b + 255) >> 8;
   const int tile = xcd_tile(A.span), slot = tile / ncb, cb = tile - slot * ncb;
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  const int j0 = (cb * NW + w) * 32 * CT;
+  const int half = w >> 2, j0 = cb * 256 + (w & 3) * 64;
   if (slot >= slots) return;
 
-  const int nch = (A.Wk + KW - 1) / KW;  // chunks of a path
-  // The wave's copies of a chunk, at addresses that only advance: kT KB of T
-  // from piece tu of the chunk on (past a path's last word they read on, T has
-  // room behind it), and its words (the last one again past it); with CT = 1
-  // two words of its 32 columns at once.  T does not depend on the expert, so
-  // its first chunk is on its way before the slot is looked up.
-  const int tu = w * kT;
-  const uint16_t *src[kT];
+  const int nit = A.P * A.Wk;
+  const int first = G == 2 ? nit : (nit + 1) >> 1;         // words of the first half; the longer one
+  const int count = half ? G * nit - first : first;        // of this wave's
+  const int word0 = G == 1 && half ? first : 0, side = G == 2 ? half : 0;  // its first word, within its side
+  const int nch = (first + 1) >> 1;
+  // the wave's copies of a chunk: 2 KB of its half's T (words past the last
+  // read on, T has room behind it), and two words of its 64 columns
+  const uint16_t *src = A.T + ((size_t)slot * G * nit + (half ? first : 0)) * 2048 + (w & 3) * 1024 + lane * 8;
+  int at = 0;
+  auto issue_t = [&]() {
 #pragma unroll
-  for (int f = 0; f < kT; ++f) {
-    const int u = tu + f, rt = u / (KW * 4), piece = u % (KW * 4);
-    src[f] = A.T + ((size_t)(slot * RT + rt) * G * A.P * A.Wk) * 2048 + piece * 512 + lane * 8;
+    for (int f = 0; f < 2; ++f) dma16(src + f * 512, sm + at + (w * 2 + f) * 1024);
+    src += 4096;
+  };
+  issue_t();
+  int e, row0, n;
+  if (!find_slot(A, A.slot0 + slot, e, row0, n)) {
+    wait_loads<0>();  // the copies land before the LDS is left
+    return;
   }
+  const LayerDesc D = layer_of(A, side, e);
+  const unsigned jw = min(j0 + lane, A.b16 - 1);
+  auto issue_w = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dma4((const void *)(D.su + (size_t)min(word0 + min(2 * c + i, max(count - 1, 0)), nit - 1) * A.b16 + jw),
+           sm + at + kMidT + (w * 2 + i) * 256);
+  };
+  issue_w(0);
+  uint32_t hh[2][2];  // [path][column tile], two copies per register
+#pragma unroll
+  for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+      const uint16_t h = D.h[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
+      hh[pp][ct] = h | ((uint32_t)h << 16);
+    }
+  float16_t acc[2], low[2];
+#pragma unroll
+  for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[ct][i] = low[ct][i] = 0.f;
+
+  for (int c = 0; c < nch; ++c) {
+    wait_loads<0>();  // the chunk has landed: this wave's part, then everybody's
+    lds_barrier();
+    const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at + half * 8192) + lane;
+    const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + kMidT + w * 512) + lr;
+    at ^= kMidChunk;
+    if (c + 1 < nch) {  // into the place that all have left behind
+      issue_t();
+      issue_w(c + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int it = 2 * c + i;
+      if (it >= count) break;
+      const int pp = word0 + it >= A.Wk;
+      const int left = A.s - 32 * (word0 + it - pp * A.Wk);
+      u32x4 t[2][2];  // [half of the word][plane]
+#pragma unroll
+      for (int f = 0; f < 4; ++f) t[f >> 1][f & 1] = tl[i * 256 + f * 64];
+      uint32_t wd[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) wd[ct] = wl[i * 64 + ct * 32] << (4 * lh);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        if (st == 1 && left <= 16) break;  // padding
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+          const half8_t b = flip(splat(pp ? hh[1][ct] : hh[0][ct]), wd[ct] << (8 * st));
+          acc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st][0]), b, acc[ct], 0, 0, 0);
+          low[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st][1]), b, low[ct], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int ct = 0; ct < 2; ++ct) acc[ct] += low[ct] * 0x1p-11f;
+  __syncthreads();
+  float4_t *over = reinterpret_cast<float4_t *>(sm) + (w & 3) * 512 + lane;  // [column tile][registers / 4][lane]
+  if (half) {
+    if constexpr (G == 2) {
+      float bg[2];
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) {
+        const int j = j0 + ct * 32 + lr;
+        bg[ct] = A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
+      }
+      with_act(A.act, [&](auto act) {
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[ct][i] = activate<decltype(act)::value>(acc[ct][i] + bg[ct]);
+      });
+    }
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        over[(ct * 4 + q) * 64] = float4_t{acc[ct][4 * q], acc[ct][4 * q + 1], acc[ct][4 * q + 2], acc[ct][4 * q + 3]};
+  }
+  __syncthreads();
+  if (half) return;
+  float *rows = reinterpret_cast<float *>(sm + 32768) + w * 32 * pitch2<1>();
+#pragma unroll
+  for (int ct = 0; ct < 2; ++ct) {
+    if (j0 + ct * 32 >= A.b) break;
+    float16_t up[1] = {acc[ct]}, other[1];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4_t v = over[(ct * 4 + q) * 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) other[0][4 * q + i] = v[i];
+    }
+    if constexpr (G == 2) {
+      finish<2, 1, true>(A, e, row0, n, 0, j0 + ct * 32, up, other, rows);
+    } else {
+      up[0] += other[0];
+      finish<1, 1>(A, e, row0, n, 0, j0 + ct * 32, up, other, rows);
+    }
+  }
+}
+
+// Many rows: a workgroup of 4 waves, 64 rows of one slot, every wave 64 columns
+// of all G sides.  T and the sign words are copied into LDS in chunks of two
+// 32-column words of a path, the next chunk during the products of one: T once
+// for the workgroup, a wave's words by itself.  (Three or four chunks on their
+// way, or longer ones, changed nothing.)  With two waves on a SIMD (G = 2; four
+// with G = 1) a wave issues an instruction every four or five cycles at best, so
+// besides the products (hi and lo: 104e9 flops for 4096 gated rows of 4096 ->
+// 11008 at s = 133, 47 us of the 122 at the clock it runs at) what counts is
+// instructions: per 16 columns and column tile 4 shifts and 8 sign flips, shared
+// by two row tiles, and everything that is not per product is out of the loop.
+// Without its epilogue the kernel takes 98 us, without products 59.
+constexpr int kW2T = 16384, kW2Chunk = kW2T + 2048;                              // T, words
+constexpr int kW2Lds = 2 * kW2Chunk;
+static_assert(kW2Lds >= 4 * 32 * pitch2<2>() * 4, "the epilogue's rows fit");
+
+template <int G>
+__global__ void __launch_bounds__(256, G == 1 ? 4 : 2)
+k_bank_second_wide(BankArgs A, int slots) {
+  __shared__ __align__(16) unsigned char sm[kW2Lds];
+  const int ncb = (A.b + 255) >> 8;
+  const int tile = xcd_tile(A.span), slot = tile / ncb, cb = tile - slot * ncb;
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  const int j0 = (cb * 4 + w) * 64;
+  if (slot >= slots) return;
+
+  const int nch = (A.Wk + 1) >> 1;  // chunks of a path
+  // The wave's copies of a chunk, at addresses that only advance: one word of T
+  // of one row tile (past a path's last word it reads on, T has room behind
+  // it), and two words of its own columns (the last one again past it).  T does
+  // not depend on the expert, so its first chunk is on its way before the slot
+  // is looked up.
+  const uint16_t *src = A.T + ((size_t)(slot * 2 + (w >> 1)) * G * A.P * A.Wk + (w & 1)) * 2048 + lane * 8;
   int fpath = 0, fc = 0, fs = 0;  // the next chunk's path (of all sides), number in it, and place
   auto issue_t = [&]() {
 #pragma unroll
-    for (int f = 0; f < kT; ++f) dma16(src[f], sm + fs + (tu + f) * 1024);
+    for (int f = 0; f < 4; ++f) dma16(src + f * 512, sm + fs + (w * 4 + f) * 1024);
   };
   issue_t();
   int e, row0, n;
@@ -812,64 +950,49 @@ k_bank_second_wide(BankArgs A, int slots) {
     return;
   }
   const LayerDesc D0 = layer_of(A, 0, e), D1 = layer_of(A, G - 1, e);
-  float16_t acc[G][RT][CT], low[G];
+  const unsigned jw = min(j0 + lane, A.b16 - 1);
+  gu32 row = D0.su;  // of the next word
+  auto issue_w = [&]() {
+    const int left = A.Wk - fc * 2;  // words of the path from here on
 #pragma unroll
-  for (int q = 0; q < G; ++q)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      low[q][i] = 0.f;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) acc[q][rt][ct][i] = 0.f;
+    for (int i = 0; i < 2; ++i)
+      dma4((const void *)(row + (size_t)min(i, left - 1) * A.b16 + jw), sm + fs + kW2T + (w * 2 + i) * 256);
+    const int step = min(2, left);
+    row += (size_t)step * A.b16;
+    src += step * 2048;
+    if (++fc == nch) {
+      fc = 0;
+      if (++fpath == A.P) row = D1.su;
     }
-  int jc[CT];
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) jc[ct] = min(j0 + ct * 32 + lr, A.b16 - 1);
-  uint16_t hv[G][2][CT];
+    fs ^= kW2Chunk;
+  };
+  issue_w();
+  uint16_t hv[G][2][2];
 #pragma unroll
   for (int q = 0; q < G; ++q)
 #pragma unroll
     for (int pp = 0; pp < 2; ++pp)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) hv[q][pp][ct] = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + jc[ct]];
+      for (int ct = 0; ct < 2; ++ct)
+        hv[q][pp][ct] = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
+  float16_t acc[G][2][2];
+#pragma unroll
+  for (int q = 0; q < G; ++q)
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[q][rt][ct][i] = 0.f;
 
-  unsigned jw[(CT + 1) / 2];
-#pragma unroll
-  for (int c = 0; c < (CT + 1) / 2; ++c) jw[c] = min(j0 + c * 64 + (CT == 1 ? lr : lane), A.b16 - 1);
-  gu32 row = D0.su;  // of the next word
-  auto issue_w = [&]() {
-    const int left = A.Wk - fc * KW;  // words of the path from here on
-    unsigned char *wdst = sm + fs + KW * RT * 4096 + w * KW * CT * 128;
-#pragma unroll
-    for (int i = 0; i < KW; i += CT == 1 ? 2 : 1) {
-      const gu32 r = row + (size_t)min(i, left - 1) * A.b16;
-      if constexpr (CT == 1) {
-        dma4((const void *)(r + (lh && i + 1 < left ? A.b16 : 0) + jw[0]), wdst + i * 128);
-      } else {
-#pragma unroll
-        for (int c = 0; c < CT / 2; ++c) dma4((const void *)(r + jw[c]), wdst + i * CT * 128 + c * 256);
-      }
-    }
-    const int step = min(KW, left);
-    row += (size_t)step * A.b16;
-#pragma unroll
-    for (int f = 0; f < kT; ++f) src[f] += step * 2048;
-    if (++fc == nch) {
-      fc = 0;
-      if (++fpath == A.P) row = D1.su;
-    }
-    fs ^= kChunk;
-  };
-  issue_w();
   const int paths = G * A.P;
   int at = 0;
 #pragma unroll
   for (int q = 0; q < G; ++q)
     for (int pp = 0; pp < A.P; ++pp) {
-      uint32_t hh[CT], hl[CT];  // the path's h (and 2^-11 h): two copies per register
+      uint32_t hh[2], hl[2];  // the path's h and 2^-11 h: two copies per register
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
+      for (int ct = 0; ct < 2; ++ct) {
         const uint16_t h = pp ? hv[q][1][ct] : hv[q][0][ct], hs = f2h(h2f(h) * 0x1p-11f);
         hh[ct] = h | ((uint32_t)h << 16);
         hl[ct] = hs | ((uint32_t)hs << 16);
@@ -882,65 +1005,45 @@ k_bank_second_wide(BankArgs A, int slots) {
           issue_w();
         }
         const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at) + lane;
-        const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + KW * RT * 4096) + w * KW * CT * 32 + lr;
-        at ^= kChunk;
-        const int steps = (A.s - 32 * KW * c + 15) >> 4;  // blocks of 16 columns that are not padding
-        u32x4 t[2][RT][2];                                // [half][row tile][plane]
-        uint32_t wd[CT];
+        const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + kW2T + w * 512) + lr;
+        at ^= kW2Chunk;
+        const int steps = (A.s - 64 * c + 15) >> 4;  // blocks of 16 columns that are not padding
+        u32x4 t[2][2][2];                            // [half][row tile][plane]
+        uint32_t wd[2];
         auto read = [&](int st) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+          for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              t[st & 1][rt][k] = tl[(rt * KW + (st >> 1)) * 256 + ((st & 1) * 2 + k) * 64];
-        };
-        auto multiply = [&](int st) {
-          if ((st & 1) == 0) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) wd[ct] = wl[(st >> 1) * CT * 32 + ct * 32] << (4 * lh);
-          }
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            const uint32_t sh = wd[ct] << (8 * (st & 1));
-            const half8_t bh = flip(splat(hh[ct]), sh), bl = kApart ? bh : flip(splat(hl[ct]), sh);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) {
-                float16_t &a = kApart && k ? low[q] : acc[q][rt][ct];
-                a = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][k]), k ? bl : bh, a, 0, 0, 0);
-              }
-          }
+            for (int k = 0; k < 2; ++k) t[st & 1][rt][k] = tl[(rt * 2 + (st >> 1)) * 256 + ((st & 1) * 2 + k) * 64];
         };
         read(0);
 #pragma unroll
-        for (int st = 0; st < 2 * KW; ++st) {
+        for (int st = 0; st < 4; ++st) {
           if (st >= steps) break;
-          if (st + 1 < 2 * KW) read(st + 1);
-          multiply(st);
+          if (st < 3) read(st + 1);
+          if ((st & 1) == 0) {
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) wd[ct] = wl[(st >> 1) * 64 + ct * 32] << (4 * lh);
+          }
+#pragma unroll
+          for (int ct = 0; ct < 2; ++ct) {
+            const uint32_t sh = wd[ct] << (8 * (st & 1));
+            const half8_t bh = flip(splat(hh[ct]), sh), bl = flip(splat(hl[ct]), sh);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int rt = 0; rt < 2; ++rt)
+                acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][k]), k ? bl : bh,
+                                                                        acc[q][rt][ct], 0, 0, 0);
+          }
         }
       }
     }
-  if constexpr (kApart) {
-#pragma unroll
-    for (int q = 0; q < G; ++q) acc[q][0][0] += low[q] * 0x1p-11f;
-  }
   __syncthreads();
-  float *lds = reinterpret_cast<float *>(sm) + w * 32 * pitch2<kEp>();
+  float *lds = reinterpret_cast<float *>(sm) + w * 32 * pitch2<2>();
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (rt * 32 >= n) break;
-#pragma unroll
-    for (int cp = 0; cp < CT; cp += kEp) {
-      float16_t up[kEp], gate[kEp];
-#pragma unroll
-      for (int i = 0; i < kEp; ++i) {
-        up[i] = acc[0][rt][cp + i];
-        gate[i] = acc[G - 1][rt][cp + i];
-      }
-      if (j0 + cp * 32 < A.b) finish<G, kEp>(A, e, row0, n, rt, j0 + cp * 32, up, gate, lds);
-    }
-  }
+  for (int rt = 0; rt < 2; ++rt)
+    if (rt * 32 < n && j0 < A.b) finish<G, 2>(A, e, row0, n, rt, j0, acc[0][rt], acc[G - 1][rt], lds);
 }
 
 // ------------------------------------------------------------------ host
@@ -1075,17 +1178,19 @@ hipError_t launch_first_wide(const BankArgs &A, int slots, int cus, hipStream_t 
   return launch_first_wide<RT, 8>(A, slots, ct, st);
 }
 
-template <int G, int RT, int CT, int NW, int KW>
-hipError_t launch_second_wide(BankArgs A, int slots, hipStream_t st) {
-  const int ncb = (A.b + NW * 32 * CT - 1) / (NW * 32 * CT);
-  constexpr int lds = w2_lds<RT, CT, NW, KW>();
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void *)k_bank_second_wide<G, RT, CT, NW, KW>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
-  }
+template <int G>
+hipError_t launch_second_mid(BankArgs A, int slots, hipStream_t st) {
+  const int ncb = (A.b + 255) / 256;
   const dim3 grid(xcd_grid(A, (int64_t)slots * ncb, ncb));
-  k_bank_second_wide<G, RT, CT, NW, KW><<<grid, dim3(NW * 64), lds, st>>>(A, slots);
+  k_bank_second_mid<G><<<grid, dim3(512), 0, st>>>(A, slots);
+  return hipGetLastError();
+}
+
+template <int G>
+hipError_t launch_second_wide(BankArgs A, int slots, hipStream_t st) {
+  const int ncb = (A.b + 255) / 256;
+  const dim3 grid(xcd_grid(A, (int64_t)slots * ncb, ncb));
+  k_bank_second_wide<G><<<grid, dim3(256), 0, st>>>(A, slots);
   return hipGetLastError();
 }
 
@@ -1127,11 +1232,11 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
     } else if (A.lg == 5) {
       e = launch_first_wide<1>(A, ns, cus, st);
       if (e == hipSuccess)
-        e = A.G == 1 ? launch_second_wide<1, 1, 1, 8, 4>(A, ns, st) : launch_second_wide<2, 1, 1, 8, 4>(A, ns, st);
+        e = A.G == 1 ? launch_second_mid<1>(A, ns, st) : launch_second_mid<2>(A, ns, st);
     } else {
       e = launch_first_wide<2>(A, ns, cus, st);
       if (e == hipSuccess)
-        e = A.G == 1 ? launch_second_wide<1, 2, 2, 4, 2>(A, ns, st) : launch_second_wide<2, 2, 2, 4, 2>(A, ns, st);
+        e = A.G == 1 ? launch_second_wide<1>(A, ns, st) : launch_second_wide<2>(A, ns, st);
     }
     if (e != hipSuccess) return set_error(LB_EHIP, std::string(who) + ": " + hipGetErrorString(e));
   }
