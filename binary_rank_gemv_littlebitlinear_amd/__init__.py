@@ -72,6 +72,7 @@ def load_library(path: str = LIB_PATH):
         "lb_stack_timeline": ([vp, vp, i64, P(i64)], i32),
         "lb_stack_destroy": ([vp], i32),
         "lb_bank_create": ([vp, vp, i32, P(vp)], i32),
+        "lb_bank_shape": ([vp, P(i32), P(i32), P(i64), P(i64), P(i32)], i32),
         "lb_bank_reserve": ([vp, i64], i32),
         "lb_bank_forward": ([vp, i32, vp, i64, vp, i64, i32, i64, i32, vp, vp, vp, i64, vp], i32),
         "lb_bank_grouped": ([vp, vp, i64, i64, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, i64, vp], i32),
@@ -99,7 +100,7 @@ EXPORTED = ("lb_create", "lb_pack_signs", "lb_set_scales", "lb_forward", "lb_for
             "lb_stack_trace_elems", "lb_stack_reserve", "lb_stack_set_mode", "lb_stack_check",
             "lb_stack_test_wait_failure", "lb_stack_test_delay",
             "lb_stack_timeline", "lb_stack_destroy",
-            "lb_bank_create", "lb_bank_reserve", "lb_bank_forward", "lb_bank_grouped", "lb_bank_destroy",
+            "lb_bank_create", "lb_bank_shape", "lb_bank_reserve", "lb_bank_forward", "lb_bank_grouped", "lb_bank_destroy",
             "lb_route_ws_bytes", "lb_route", "lb_route_combine", "lb_status_str", "lb_last_error", "lb_version")
 
 
@@ -327,6 +328,13 @@ def lb_bank_create(layers, gates=None) -> int:
     return out.value
 
 
+def lb_bank_shape(bank: int):
+    """(layers, gated, a, b, device) of a bank."""
+    n, g, d, a, b = C.c_int(), C.c_int(), C.c_int(), C.c_int64(), C.c_int64()
+    _check(load_library().lb_bank_shape(bank, C.byref(n), C.byref(g), C.byref(a), C.byref(b), C.byref(d)))
+    return n.value, bool(g.value), a.value, b.value, d.value
+
+
 def lb_bank_reserve(bank: int, rows: int):
     _check(load_library().lb_bank_reserve(bank, int(rows)))
 
@@ -339,12 +347,12 @@ def _say(t) -> str:
 # device numbers (-1: not on a GPU) and leave the wording of errors to the failing case.
 def _rows(name, t, width, dtypes, dev):
     """(rows, row stride) of a 2-d tensor of `width` columns with unit column stride on GPU `dev`."""
-    shape, st = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != width or t.dtype not in dtypes or t.get_device() != dev or (
-            st[1] != 1 and width > 1):
-        raise ValueError(f"{name} must be 2-d with {width} unit-stride columns, of {dtypes}, on GPU {dev}, not {_say(t)}")
-    # a single row's stride is never used; torch leaves it arbitrary
-    return (shape[0], st[0]) if shape[0] > 1 else (shape[0], width)
+    if t.dim() == 2:
+        (rows, cols), (ld, unit) = t.shape, t.stride()
+        if cols == width and (unit == 1 or width == 1) and t.dtype in dtypes and t.get_device() == dev:
+            # a single row's stride is never used; torch leaves it arbitrary
+            return rows, ld if rows > 1 else width
+    raise ValueError(f"{name} must be 2-d with {width} unit-stride columns, of {dtypes}, on GPU {dev}, not {_say(t)}")
 
 
 def _flat(name, t, shape, dtype, dev):
@@ -363,7 +371,7 @@ def _stream_of(stream, dev):
 def _on_device(dev, fn, *args):
     """Calls the library with GPU `dev` current (for calls that have no object to take the device from)."""
     import torch
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         return _check(fn(*args))
     with torch.cuda.device(dev):
         _check(fn(*args))
@@ -383,9 +391,7 @@ def _types():
 def _epilogue(bank, y, act, bias, gate_bias, residual):
     """The arguments that lb_bank_forward and lb_bank_grouped share: GPU, rows, then in the C order."""
     _types()
-    dev, b, n = y.get_device(), bank.b, bank.n
-    if dev < 0:
-        raise ValueError("y must be a device tensor")
+    dev, b, n = bank.device, bank.b, bank.n
     rows, ldy = _rows("y", y, b, _f16_f32, dev)
     dtype = y.dtype
     if act is None:
@@ -415,7 +421,7 @@ def lb_bank_forward(bank, x, y, expert: int = 0, act=None, bias=None, gate_bias=
     xr, ldx = _rows("x", x, bank.a, _only_f16, dev)
     if xr != rows:
         raise ValueError("x and y must have the same number of rows")
-    _check(_lib.lb_bank_forward(bank.handle, expert, x.data_ptr(), ldx, py, ldy, yt, rows, act, pb, pg, pr, ldr,
+    _check(_lib.lb_bank_forward(bank.handle, int(expert), x.data_ptr(), ldx, py, ldy, yt, rows, act, pb, pg, pr, ldr,
                                 _stream_of(stream, dev)))
 
 
@@ -567,9 +573,9 @@ class Bank:
         self.gates = list(gates) if gates is not None else None
         if not self.layers:
             raise ValueError("a bank needs at least one layer")
-        self.n, self.a, self.b = len(self.layers), self.layers[0].a, self.layers[0].b
         self.handle = lb_bank_create([L.handle for L in self.layers],
                                      [L.handle for L in self.gates] if self.gates is not None else None)
+        self.n, _, self.a, self.b, self.device = lb_bank_shape(self.handle)
 
     def reserve(self, rows: int):
         lb_bank_reserve(self.handle, rows)

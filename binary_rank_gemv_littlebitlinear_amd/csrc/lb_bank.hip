@@ -1343,6 +1343,16 @@ extern "C" lb_status lb_bank_destroy(lb_bank *B) {
   return LB_OK;
 }
 
+extern "C" lb_status lb_bank_shape(const lb_bank *B, int *n, int *gated, int64_t *a, int64_t *b, int *device) {
+  if (!B) return set_error(LB_EINVAL, "lb_bank_shape: NULL bank");
+  if (n) *n = B->E;
+  if (gated) *gated = B->G == 2;
+  if (a) *a = B->a;
+  if (b) *b = B->b;
+  if (device) *device = B->device;
+  return LB_OK;
+}
+
 extern "C" lb_status lb_bank_reserve(lb_bank *B, int64_t rows) {
   if (!B) return set_error(LB_EINVAL, "lb_bank_reserve: NULL bank");
   if (rows < 0 || rows > kMaxRows) return set_error(LB_EINVAL, "lb_bank_reserve: rows must be in [0, 2^30]");

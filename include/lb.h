@@ -451,6 +451,10 @@ lb_status lb_bank_grouped(lb_bank *B, const void *x, int64_t x_rows, int64_t ldx
                           int act, const void *bias, const void *gate_bias, const void *residual,
                           int64_t ldr, void *stream);
 
+/* Layers of the bank, whether it has gates, widths, and the device that all
+ * pointers and streams of its calls belong to.  Any pointer may be NULL. */
+lb_status lb_bank_shape(const lb_bank *B, int *n, int *gated, int64_t *a, int64_t *b, int *device);
+
 lb_status lb_bank_destroy(lb_bank *B);
 
 /* ------------------------------------------------------------- routing */
@@ -469,7 +473,7 @@ lb_status lb_bank_destroy(lb_bank *B);
  *             an expert's rows are in the order of the tokens.  -1 behind
  *             the last row
  *   row       tokens x k: the row of every choice
- * ws is device scratch of at least lb_route_ws_bytes bytes (none for 64
+ * No array may overlap another.  ws is device scratch of at least lb_route_ws_bytes bytes (none for 64
  * tokens or fewer), not shared with calls that may run at the same time.  Only
  * launches kernels; with no tokens it writes offsets alone. */
 lb_status lb_route_ws_bytes(int64_t tokens, int experts, int k, uint64_t *bytes);

@@ -31,6 +31,7 @@ def test_null_handles(lbm, lib):
     assert lib.lb_bank_reserve(None, 1) == lbm.LB_EINVAL
     assert lib.lb_bank_forward(None, 0, 16, 1, 64, 1, 0, 1, 0, None, None, None, 0, None) == lbm.LB_EINVAL
     assert lib.lb_bank_grouped(None, 16, 1, 1, None, 64, 1, 128, 1, 0, 0, None, None, None, 0, None) == lbm.LB_EINVAL
+    assert lib.lb_bank_shape(None, None, None, None, None, None) == lbm.LB_EINVAL
     assert lib.lb_bank_destroy(None) == lbm.LB_OK
     with pytest.raises(ValueError):
         lbm.Bank([])

@@ -116,11 +116,12 @@ def test_small_and_large_values(lbm):
 
 @pytest.mark.parametrize("off,ldx,ldy,ldr", [(0, 1008, 608, 616), (1, 1003, 601, 603), (0, 1001, 600, 600), (8, 1016, 616, 600)])
 @pytest.mark.parametrize("out", [np.float16, np.float32])
-def test_strides_and_alignment(lbm, off, ldx, ldy, ldr, out):
+@pytest.mark.parametrize("M", [9, 45, 8200])
+def test_strides_and_alignment(lbm, off, ldx, ldy, ldr, out, M):
     """Row strides, and x, y and residual that begin inside an allocation; what lies between y's rows stays."""
     torch = lbtest.torch_dev()
-    say(f"[case] bank strides off={off} ldx={ldx} ldy={ldy} ldr={ldr}")
-    a, b, M = 1000, 600, 45
+    say(f"[case] bank strides off={off} ldx={ldx} ldy={ldy} ldr={ldr} M={M}")
+    a, b = 1000, 600
     up, ul = _layers(lbm, a, b, 40, True, 1, 11)
     B = lbm.Bank(ul)
     rng = np.random.default_rng(3)
@@ -161,23 +162,24 @@ def test_residual_in_place(lbm):
     B.close()
 
 
-def test_rows_are_independent(lbm):
-    """NaN and infinity in one row of x stay in that row's output."""
+@pytest.mark.parametrize("M", [12, 40, 8200])
+def test_rows_are_independent(lbm, M):
+    """NaN and infinity in one row of x stay in that row's output (each launch shape)."""
     torch = lbtest.torch_dev()
-    say("[case] bank NaN rows")
-    a, b, M = 1000, 600, 40
+    say(f"[case] bank NaN rows M={M}")
+    a, b = 1000, 600
     up, ul = _layers(lbm, a, b, 40, True, 1, 11)
     B = lbm.Bank(ul)
     x = lb_synth.activations(M, a, seed=8)
     clean = torch.empty((M, b), dtype=torch.float16, device="cuda")
     B.forward(_dev(x), clean)
-    x[3, 5], x[37, 999] = np.nan, np.inf
+    x[3, 5], x[M - 3, 999] = np.nan, np.inf
     y = torch.empty_like(clean)
     B.forward(_dev(x), y)
     torch.cuda.synchronize()
-    keep = [i for i in range(M) if i not in (3, 37)]
+    keep = [i for i in range(M) if i not in (3, M - 3)]
     assert torch.equal(y[keep], clean[keep])
-    assert torch.isnan(y[3]).all() and not torch.isfinite(y[37]).any()
+    assert torch.isnan(y[3]).all() and not torch.isfinite(y[M - 3]).any()
     B.close()
 
 
@@ -252,20 +254,72 @@ def test_grouped_odd(lbm):
     _grouped(lbm, 259, 131, 63, False, 5, c, act="gelu", bias=True, residual=True, gather=True)
 
 
-def test_grouped_index_out_of_range_reads_zeros(lbm):
+@pytest.mark.parametrize("b,rows", [(136, 6), (136, 70), (8200, 1100)])
+def test_grouped_index_out_of_range_reads_zeros(lbm, b, rows):
+    """In each launch shape; the rows around the bad ones keep their values."""
     torch = lbtest.torch_dev()
-    say("[case] grouped bad index")
-    up, ul = _layers(lbm, 200, 136, 21, True, 2, 31)
+    say(f"[case] grouped bad index rows={rows}")
+    up, ul = _layers(lbm, 200, b, 21, True, 2, 31)
     B = lbm.Bank(ul)
     x = lb_synth.activations(4, 200, seed=1)
-    index = np.array([0, -1, 3, 4, 2 ** 31 - 1, -2 ** 31], np.int32)
-    y = torch.full((6, 136), 9.0, dtype=torch.float16, device="cuda")
-    B.grouped(_dev(x), _dev(np.array([0, 3, 6], np.int32)), y, index=_dev(index))
+    index = np.arange(rows, dtype=np.int32) % 4
+    bad = [1, rows // 2 - 1, rows // 2, rows - 1]
+    index[bad] = [-1, 4, 2 ** 31 - 1, -2 ** 31]
+    half = rows // 2
+    y = torch.full((rows, b), 9.0, dtype=torch.float16, device="cuda")
+    B.grouped(_dev(x), _dev(np.array([0, half, rows], np.int32)), y, index=_dev(index))
     torch.cuda.synchronize()
     got = y.cpu().numpy()
-    assert (got[[1, 3, 4, 5]] == 0).all()
-    ref, tol = bankref.fused(x[[0, 3]], up[0])
-    assert_within(got[[0, 2]], ref, tol, "good rows")
+    assert (got[bad] == 0).all()
+    for e, lo, hi in ((0, 0, half), (1, half, rows)):
+        good = np.array([i for i in range(lo, hi) if i not in bad])
+        ref, tol = bankref.fused(x, up[e])
+        assert_within(got[good], ref[index[good]], tol[index[good]], f"good rows of expert {e}")
+    B.close()
+
+
+@pytest.mark.parametrize("rows", [300, 40000])
+def test_grouped_many_experts(lbm, rows):
+    """1024 experts (three layers over and over), some without rows, one with a third of them."""
+    torch = lbtest.torch_dev()
+    say(f"[case] 1024 experts rows={rows}")
+    up, ul = _layers(lbm, 40, 24, 9, False, 3, 91)
+    n = 1024
+    rng = np.random.default_rng(rows)
+    c = rng.multinomial(rows - rows // 3, np.ones(n) / n)
+    c[700] += rows // 3
+    off = np.concatenate([[0], np.cumsum(c)]).astype(np.int32)
+    x = lb_synth.activations(rows, 40, seed=2)
+    B = lbm.Bank([ul[e % 3] for e in range(n)])
+    y = torch.empty((rows, 24), dtype=torch.float32, device="cuda")
+    B.grouped(_dev(x), _dev(off), y)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy()
+    expert = np.repeat(np.arange(n), c)
+    for k in range(3):
+        mine = expert % 3 == k
+        ref, tol = bankref.fused(x[mine], up[k], out=np.float32)
+        assert_within(got[mine], ref, tol, f"layer {k}")
+    B.close()
+
+
+def test_grouped_strided_x_with_rows_to_spare(lbm):
+    """x as a column slice, with more rows than the call has; a bank of one layer."""
+    torch = lbtest.torch_dev()
+    say("[case] grouped strided x")
+    up, ul = _layers(lbm, 200, 136, 21, True, 1, 31)
+    B = lbm.Bank(ul)
+    base = torch.full((50, 230), float("nan"), dtype=torch.float16, device="cuda")
+    xh = lb_synth.activations(50, 200, seed=4)
+    x = base[:, 17:217]
+    x.copy_(_dev(xh))
+    y = torch.full((33, 136), 9.0, dtype=torch.float16, device="cuda")
+    B.grouped(x, _dev(np.array([2, 31], np.int32)), y)
+    torch.cuda.synchronize()
+    got = y.cpu().numpy()
+    ref, tol = bankref.fused(xh[2:31], up[0])
+    assert_within(got[2:31], ref, tol, "strided x")
+    assert (got[:2] == 9).all() and (got[31:] == 9).all()
     B.close()
 
 
@@ -475,6 +529,11 @@ def test_refusals(lbm):
                 lambda: B.grouped(x, off.long(), y), lambda: B.grouped(x, off, y, index=off)):
         with pytest.raises(ValueError):
             bad()
+    assert lbm.lb_bank_shape(B.handle) == (2, False, 200, 136, torch.cuda.current_device())
+    B.device += 1  # tensors of another GPU than the bank's
+    with pytest.raises(ValueError):
+        B.forward(x, y)
+    B.device -= 1
     lib, p = lbm.load_library(), y.data_ptr()
     base = dict(e=0, x=x.data_ptr(), ldx=200, y=p, ldy=136, yt=0, M=4, act=0, bias=None, gb=None, res=None, ldr=0)
     for bad in (dict(e=2), dict(e=-1), dict(x=None), dict(y=None), dict(ldx=199), dict(ldy=135), dict(yt=2), dict(M=-1),
