@@ -22,11 +22,11 @@
 // the end, whatever the batch size.  With w as one fp16 number the error of
 // an fp16 y is 1.4 times that of its own rounding (1.75 times when gated).
 //
-// Rows are cut into slots of tm rows (32 or 64) of one expert.  Without
-// offsets slot i is rows [i tm, (i + 1) tm); with offsets every wave finds
-// its slot from the experts' row counts, so the host never waits for them:
-// the grid is sized for the most slots that `rows` rows can make,
-// rows / tm + min(experts, rows), and workgroups past the last slot leave.
+// Rows are cut into slots of n rows (16, 32 or 64, see run) of one expert.
+// Without offsets slot i is rows [i n, (i + 1) n); with offsets every wave
+// finds its slot from the experts' row counts, so the host never waits for
+// them: the grid is sized for the most slots that `rows` rows can make,
+// rows / n + min(experts, rows), and workgroups past the last slot leave.
 //
 // Latent workspace T, per 32-row part of a slot (ps), segment and block of 16
 // columns: [hi, lo][column half 2][32 rows][8 fp16], so that an operand load
@@ -34,7 +34,7 @@
 //   T[(((ps nseg + seg) 2 Wk + k16) 2 + plane) 512 + (c8 32 + row) 8 + c].
 // Columns past s are zero.
 //
-// Instruction: v_mfma_f32_32x32x16_f16.  Operand lanes: A[i][k] in lane
+// Instruction (32- and 64-row slots): v_mfma_f32_32x32x16_f16.  Operand lanes: A[i][k] in lane
 // i + 32 (k / 8), element k % 8; B[k][j] in lane j + 32 (k / 8), element
 // k % 8; D[i][j] in lane j + 32 ((i / 4) % 2), register 4 (i / 8) + i % 4.
 #include <hip/hip_fp16.h>
@@ -117,7 +117,7 @@ __device__ __forceinline__ u32x4 splat(uint32_t v) {
   return o;
 }
 
-// Slot `slot` of the call: its expert, first row and row count (1..tm).
+// Slot `slot` of the call: its expert, first row and row count.
 // Uniform over the wave; false past the last slot.  Offsets are clamped to
 // [0, rows], so no row outside the call is touched whatever they hold.
 __device__ __forceinline__ bool find_slot(const BankArgs &A, int slot, int &e, int &row0, int &n) {
@@ -229,21 +229,29 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Waits for the wave's LDS reads.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // ------------------------------------------------------- first product
-// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 16 latent
-// columns over the whole input dimension, wave w on the blocks of 32 inputs w,
-// w + NW, ...; the waves' sums are added in wave order through LDS.  Bound by
-// latency and by what one CU can issue, hence the small tile (a 32 x 32 one
-// took 6.5 us for one row of a 4096-wide layer, two thirds of it on the four
-// waves a SIMD that wanted to expand signs at once), operands of kF1U blocks requested
-// together, and g (the same for all columns) straight into the wave's LDS.
+// Few rows (slots of 16): a workgroup of 8 waves computes 16 rows x 16 latent
+// columns over the whole input dimension, wave w on the blocks of 32 inputs
+// 2 w, 2 w + 1, 2 w + 16, ... (pairs: whole 128-byte lines of x; single blocks
+// took 7.2 us, not 4.3, for 16 rows of 1024); the waves' sums are added in wave
+// order through LDS.  Bound by latency and by what one CU can issue, hence the
+// small tile (a 32 x 32 one took 6.5 us for one row of a 4096-wide layer, two
+// thirds of it on the four waves a SIMD that wanted to expand signs at once),
+// operands of kF1U blocks requested together, and g (the same for all columns)
+// straight into the wave's LDS.  One row of 4096: 5.1 us, 16 rows 7.8; 11008:
+// 7.4 and 14.5.  4 waves take 5.8 and 8.2, 11.2 and 15.0, no less for 1024; 16
+// waves 6.1 and 11.2, 8.8 and 18.8.
 // v_mfma_f32_16x16x32_f16: A[i][k] in lane i + 16 (k / 8), B[k][j] in lane
 // j + 16 (k / 8), D[i][j] in lane j + 16 (i / 4), register i % 4.
-constexpr int kF1U = 16;
+constexpr int kF1U = 16, kF1Waves = 8;
 
-template <int NW, bool XV>
-__global__ void __launch_bounds__(NW * 64)
+template <bool XV>
+__global__ void __launch_bounds__(kF1Waves * 64)
 k_bank_first16(BankArgs A) {
+  constexpr int NW = kF1Waves;
   __shared__ __align__(16) float red[NW * 256];
   const int tile = blockIdx.x, slot = blockIdx.y, W2 = 2 * A.Wk;
   int seg = 0;
@@ -276,22 +284,25 @@ k_bank_first16(BankArgs A) {
   const int full = A.a >> 5;                                            // whole blocks
   unsigned char *gl = reinterpret_cast<unsigned char *>(red + w * 256);  // the wave's own part of red
   const u32x4 *gs = reinterpret_cast<const u32x4 *>(gl);
-  for (int c0 = w; c0 < full; c0 += NW * kF1U) {
+  auto block = [](int c0, int u) { return c0 + (u >> 1) * 2 * NW + (u & 1); };
+  for (int c0 = 2 * w; c0 < full; c0 += NW * kF1U) {
     uint32_t wd[kF1U];
     u32x4 xv[kF1U];
-    dma16((const void *)(g + min(c0 + (lane >> 2) * NW, full - 1) * 32 + (lane & 3) * 8), gl);
+    dma16((const void *)(g + min(block(c0, lane >> 2), full - 1) * 32 + (lane & 3) * 8), gl);
 #pragma unroll
     for (int u = 0; u < kF1U; ++u) {
-      const int c = min(c0 + u * NW, full - 1);  // past the end: read, not used
+      if (u % 4 == 0 && block(c0, u) >= full) break;
+      const int c = min(block(c0, u), full - 1);  // past the end: read, not used
       wd[u] = (bw + (size_t)c * A.L)[col];
       xv[u] = load8<XV>(xr + c * 32 + o * 8);
     }
     wait_loads<0>();
 #pragma unroll
     for (int u = 0; u < kF1U; ++u) {
-      if (c0 + u * NW >= full) break;
+      if (block(c0, u) >= full) break;
       acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(xv[u]), flip(gs[4 * u + o], wd[u] << (4 * o)), acc, 0, 0, 0);
     }
+    wait_lds();  // g has been read before the next round's is copied over it
   }
   if (full < A.R1 && w == NW - 1) {  // the last block is not whole
     const int i = full * 32 + o * 8;
@@ -323,9 +334,9 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Many rows: a workgroup of 8 waves computes 32 RT rows x 32 CT columns of one
+// Many rows: a workgroup of NW waves computes 32 RT rows x 32 CT columns of one
 // segment over the whole input dimension, wave w on the blocks of 32 inputs
-// 2 w, 2 w + 1, 2 w + 16, ... (pairs: whole 128-byte lines of x).  A wave
+// 2 w, 2 w + 1, 2 w + 2 NW, ... (pairs: whole 128-byte lines of x).  A wave
 // shares its operands with no other, so it stages them itself, without
 // barriers: x rows, the block's g and its columns' sign words are copied into
 // a ring of kW1Ring blocks in the wave's own LDS, all but one in flight (piece
@@ -333,7 +344,10 @@ __device__ __forceinline__ void lds_barrier() {
 // twice).  One expanded sign operand serves RT products.  The waves' sums are
 // added in wave order through LDS, 32 columns at a time.  The workgroups of
 // one slot lie side by side (xcd_tile), so its x rows come from an L2 after
-// the first.
+// the first.  A round of workgroups over 4096 inputs takes 9.5, 11.4, 15 and
+// 20 us with RT = 1 and CT = 1, 2, 3 and 5 (start and sums included), 22 and
+// 33 with RT = 2 and CT = 3 and 5: at 5 a wave's products are 60% of its time,
+// the rest is sign flips and LDS reads, and the start and end of the launch.
 constexpr int kW1Ring = 4;
 template <int RT, int CT>
 constexpr int w1_block() { return RT * 2048 + (CT + 1) / 2 * 256 + 64; }  // x, words, g
@@ -463,6 +477,9 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
     if (next) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) wd[ct] = wn[ct] << (4 * lh);
+      // The words were requested last and LDS answers in order: the block read
+      // in this round has been read before the next round copies over it.
+      asm volatile("" : "+v"(wd[CT - 1])::"memory");
     }
   };
   int i = 0;
@@ -597,7 +614,7 @@ __device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = lds[row * kPitch + c8 * 8 + i];
-const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
+    const int64_t yo = (int64_t)(row0 + rr) * A.ldy + j, ro = (int64_t)(row0 + rr) * A.ldr + j;
     if (j + 8 <= A.b) {
       if (A.f32) {
         float *y = (float *)A.y + yo;
@@ -719,10 +736,10 @@ k_bank_second16(BankArgs A) {
     const int at = ((c >> 4) * 4 + (row & 3)) * 64 + (c & 15) + 16 * (row >> 2);
     const bool two = j + 1 < A.b;
     float v[2], g[2];
-  #pragma unroll
+#pragma unroll
     for (int i = 0; i < 2; ++i) {
       v[i] = g[i] = 0.f;
-  #pragma unroll
+#pragma unroll
       for (int q = 0; q < NW; ++q) {
         v[i] += red[q * G * CT * 256 + at + i];
         if constexpr (G == 2) g[i] += red[(q * G + 1) * CT * 256 + at + i];
@@ -732,7 +749,7 @@ k_bank_second16(BankArgs A) {
       if (G == 2 && A.bias[1]) g[i] += h2f(A.bias[1][(size_t)e * A.b + ji]);
     }
     with_act(A.act, [&](auto act) {
-  #pragma unroll
+#pragma unroll
       for (int i = 0; i < 2; ++i)
         v[i] = G == 2 ? activate<decltype(act)::value>(g[i]) * v[i] : activate<decltype(act)::value>(v[i]);
     });
@@ -1072,20 +1089,39 @@ size_t part_bytes(const lb_bank *B) {
   return (size_t)B->G * Ly.P * Ly.Wk * 2048 * 2;
 }
 
+int cu_count(const lb_bank *B) {
+  const int n = device_info(B->first).cu_count;
+  return n > 0 ? n : 256;
+}
+
+// Up to this many rows a call takes slots of 16: while the first product's
+// 16 x 16 tiles, all slots full, are a few hundred.  16- against 32-row slots,
+// both kernels, 4096 -> 11008 gated at s = 133 (20 words): 32 rows 13.7 against
+// 17.6 us, 64 rows 16.0 against 18.0, 96 rows 20.1 against 18.0; at s = 431 (56
+// words) 32 rows 17.3 against 24.4, 64 rows 27 against 25.5; 4096 -> 4096 at
+// s = 86 (6 words) 256 rows 14.3 against 16.5, 512 rows 23.4 against 18.2.
+// Grouped rows leave slots part empty: 8 layers 8 rows 17.8 against 23, 48 rows
+// 23.9 against 24.1, 64 rows 26.9 against 24.5; 64 layers 1024 -> 1407 (8
+// words) 96 rows 15.6 against 17.8, 180 rows 19.9 against 18.3.
+int64_t few_rows(const lb_bank *B, bool grouped) {
+  const Layer &Ly = B->first->ly;
+  return (grouped ? 4 : 7) * (int64_t)cu_count(B) / (B->G * Ly.P * Ly.Wk);
+}
+
 // The most 32-row parts of T that a call of up to `rows` rows makes, at any
 // slot size (16-row slots take a part each), within the budget (at least one
 // 64-row slot).
 int64_t parts_for(const lb_bank *B, int64_t rows) {
-  const int64_t few = std::min<int64_t>(rows, 16 * (int64_t)B->E);  // 16-row slots are for no more rows
-  const int64_t most = std::max((rows / 64 + 1 + std::min<int64_t>(B->E, rows)) * 2, few / 16 + 1 + std::min<int64_t>(B->E, few));
+  const int64_t few = std::min(rows, few_rows(B, false)), e = std::min<int64_t>(B->E, rows);
+  const int64_t most = std::max((rows / 64 + 1 + e) * 2, few / 16 + 1 + e);
   const int64_t cap = std::max<int64_t>(2, (int64_t)(kTBudget / part_bytes(B)) / 2 * 2);
   return std::min(most, cap);
 }
 
 lb_status grow(lb_bank *B, int64_t rows, const char *who, bool in_call, hipStream_t st) {
-  const std::string pre = std::string(who) + ": ";
   const int64_t need = parts_for(B, rows);
   if (need <= B->parts) return LB_OK;
+  const std::string pre = std::string(who) + ": ";
   if (in_call) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     const hipError_t e = hipStreamIsCapturing(st, &cs);
@@ -1112,13 +1148,12 @@ lb_status grow(lb_bank *B, int64_t rows, const char *who, bool in_call, hipStrea
   return LB_OK;
 }
 
-template <int NW>
 hipError_t launch_first16(const BankArgs &A, int slots, hipStream_t st) {
   const dim3 grid((unsigned)(A.G * A.P * A.Wk * 2), (unsigned)slots);
   if (A.xvec)
-    k_bank_first16<NW, true><<<grid, dim3(NW * 64), 0, st>>>(A);
+    k_bank_first16<true><<<grid, dim3(kF1Waves * 64), 0, st>>>(A);
   else
-    k_bank_first16<NW, false><<<grid, dim3(NW * 64), 0, st>>>(A);
+    k_bank_first16<false><<<grid, dim3(kF1Waves * 64), 0, st>>>(A);
   return hipGetLastError();
 }
 
@@ -1165,14 +1200,38 @@ hipError_t launch_first_wide(const BankArgs &A, int slots, int ct, hipStream_t s
   }
 }
 
-// Column tiles per workgroup: a segment's tiles in the fewest groups of at
-// most five (RT = 2: 160 of 256 registers are sums then), spread evenly; fewer
-// tiles a group while that leaves CUs without a workgroup.
+// The first product of 32- and 64-row slots: column tiles per workgroup (at most
+// five: with RT = 2 160 of 256 registers are sums then), and what a launch
+// costs, in workgroups' times of a column tile.  A CU runs one workgroup at a
+// time, so what counts first is how often all CUs are filled, then the tiles a
+// workgroup has: the fewest rounds, then the fewest tiles.  4096 -> 11008,
+// gated, s = 133: 256 rows 9.4 us with one tile, 17 with five; 768 rows 14.0
+// with three (one round), 17.7 with two, 17.9 with five; 2048 rows 21 with five
+// (one round), 30 with two or three.  A tile alone costs as much as 1.5.
+struct FirstPlan {
+  int ct;
+  int64_t cost;
+};
+FirstPlan first_plan(const BankArgs &A, int64_t slots, int rt, int cus) {
+  FirstPlan best = {1, 0};
+  int64_t fewest = INT64_MAX;
+  for (int c = 1; c <= 5 && c <= A.Wk; ++c) {
+    const int64_t wgs = slots * A.G * A.P * ((A.Wk + c - 1) / c), rounds = (wgs + cus - 1) / cus;
+    if (rounds < fewest) {
+      fewest = rounds;
+      best = {c, rounds * rt * std::max(3, 2 * c)};
+    }
+  }
+  return best;
+}
+
+// With more than a round of 64-row workgroups they have 4 waves, so that two
+// run on a CU and one's end overlaps the other's products (8192 rows of 4096,
+// gated: 54 us against 63 with 8 waves; 270 workgroups of 8192 expert rows of
+// 11008: 113 against 122; one round of 4096 rows: 36 against 33).
 template <int RT>
 hipError_t launch_first_wide(const BankArgs &A, int slots, int cus, hipStream_t st) {
-  int ncs = (A.Wk + 4) / 5;
-  while (ncs < A.Wk && (int64_t)slots * A.G * A.P * ncs < cus) ++ncs;
-  const int ct = (A.Wk + ncs - 1) / ncs;
+  const int ct = first_plan(A, slots, RT, cus).ct, ncs = (A.Wk + ct - 1) / ct;
   if constexpr (RT == 2)
     if ((int64_t)slots * A.G * A.P * ncs > cus) return launch_first_wide<RT, 4>(A, slots, ct, st);
   return launch_first_wide<RT, 8>(A, slots, ct, st);
@@ -1196,7 +1255,7 @@ hipError_t launch_second_wide(BankArgs A, int slots, hipStream_t st) {
 
 lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   const Layer &Ly = B->first->ly;
-  const int cus = device_info(B->first).cu_count > 0 ? device_info(B->first).cu_count : 256;
+  const int cus = cu_count(B);
   lb_status gs = grow(B, A.rows, who, true, st);
   if (gs != LB_OK) return gs;
   A.desc = B->desc;
@@ -1210,18 +1269,33 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   A.xvec = A.a % 8 == 0 && A.ldx % 8 == 0 && (uintptr_t)A.x % 16 == 0;
   const int64_t avg = A.offsets ? (A.rows + A.E - 1) / A.E : A.rows;
   const int64_t big_wg = (int64_t)(A.rows / 64) * ((A.b + 511) / 512);
-  A.lg = avg <= 16 ? 4 : avg >= 64 && big_wg >= cus ? 6 : 5;
+  // Slots of 64 share an expanded sign operand between two row tiles, but make
+  // half the workgroups, and the second product's have half the waves.  64-
+  // against 32-row slots, both kernels: 4096 -> 11008 gated 1024 rows (352
+  // workgroups of 64 x 512) 55.7 against 51.1 us, 2048 rows (704) 93 against 84,
+  // 3000 rows (1012) 137 against 135, 4096 rows (1408) 164 against 177; 4096 ->
+  // 4096 4096 rows (512) 63 against 57, 8192 rows (1024) 106 against 108, 16384
+  // rows 186 against 210.  Below that they win where 32-row slots cost the
+  // first product a round more: 8 layers 11008 -> 4096, 4096 rows (512) 90
+  // against 110 us; not 4096 rows of one layer (100 against 89).
+  const auto plan = [&](int lg) {
+    const int64_t n = A.offsets ? (A.rows >> lg) + std::min<int64_t>(A.E, A.rows) : (A.rows + (1 << lg) - 1) >> lg;
+    return first_plan(A, n, 1 << (lg - 5), cus).cost;
+  };
+  A.lg = A.rows <= few_rows(B, A.offsets != nullptr) ? 4
+         : avg >= 64 && (big_wg >= 4 * cus || (big_wg >= 2 * cus && plan(6) <= plan(5))) ? 6 : 5;
   const int64_t slots = A.offsets ? (A.rows >> A.lg) + std::min<int64_t>(A.E, A.rows)
                                   : (A.rows + (1 << A.lg) - 1) >> A.lg;
   const int per = A.lg == 6 ? 2 : 1;  // 32-row parts of T per slot
   const int64_t tiles = std::max<int64_t>((int64_t)A.G * A.P * A.Wk, (A.b + 127) / 128);
-  const int64_t window = std::min<int64_t>({B->parts / per, (int64_t)0x7fffffff / 1024 / tiles, 65535});
+  const int64_t window =
+      std::max<int64_t>(1, std::min<int64_t>({B->parts / per, (int64_t)0x7fffffff / 1024 / tiles, 65535}));
   for (int64_t s0 = 0; s0 < slots; s0 += window) {
     const int ns = (int)std::min<int64_t>(window, slots - s0);
     A.slot0 = (int)s0;
     hipError_t e;
     if (A.lg == 4) {
-      e = A.R1 >= 64 ? launch_first16<8>(A, ns, st) : launch_first16<4>(A, ns, st);
+      e = launch_first16(A, ns, st);
       // 32 columns a workgroup when all of them start at once, else 64 (8
       // experts of 4096 -> 11008, gated, a row each: 9.1 against 11.0 us; one
       // row alone: 5.6 against 5.0 us)
@@ -1248,33 +1322,33 @@ size_t extent(int64_t rows, int64_t ld, int64_t n, int size) { return (size_t)((
 
 // The checks both calls share.
 lb_status check(const lb_bank *B, const BankArgs &A, int64_t rows, int64_t x_rows, int y_type, const char *who) {
-  const std::string pre = std::string(who) + ": ";
-  if (y_type != LB_F16 && y_type != LB_F32) return set_error(LB_EINVAL, pre + "y_type must be LB_F16 or LB_F32");
-  if (A.act < LB_ACT_NONE || A.act > LB_ACT_SILU) return set_error(LB_EINVAL, pre + "unknown activation");
+  const auto refuse = [who](const char *why) { return set_error(LB_EINVAL, std::string(who) + ": " + why); };
+  if (y_type != LB_F16 && y_type != LB_F32) return refuse("y_type must be LB_F16 or LB_F32");
+  if (A.act < LB_ACT_NONE || A.act > LB_ACT_SILU) return refuse("unknown activation");
   if (rows < 0 || x_rows < 0 || rows > kMaxRows || x_rows > kMaxRows)
-    return set_error(LB_EINVAL, pre + "row counts must be in [0, 2^30]");
+    return refuse("row counts must be in [0, 2^30]");
   if (rows == 0) return LB_OK;
-  if (!A.x || !A.y) return set_error(LB_EINVAL, pre + "NULL x or y");
-  if (x_rows == 0) return set_error(LB_EINVAL, pre + "x has no rows");
-  if (A.bias[1] && B->G == 1) return set_error(LB_EINVAL, pre + "a gate bias needs a bank with gates");
+  if (!A.x || !A.y) return refuse("NULL x or y");
+  if (x_rows == 0) return refuse("x has no rows");
+  if (A.bias[1] && B->G == 1) return refuse("a gate bias needs a bank with gates");
   if (A.ldx < B->a || A.ldy < B->b || (A.res && A.ldr < B->b))
-    return set_error(LB_EINVAL, pre + "a row stride is smaller than the row");
+    return refuse("a row stride is smaller than the row");
   if (A.ldx > ((int64_t)1 << 31) || A.ldy > ((int64_t)1 << 31) || A.ldr > ((int64_t)1 << 31))
-    return set_error(LB_EINVAL, pre + "a row stride exceeds 2^31");
+    return refuse("a row stride exceeds 2^31");
   const int ys = y_type == LB_F32 ? 4 : 2;
   if (((uintptr_t)A.x | (uintptr_t)A.bias[0] | (uintptr_t)A.bias[1]) % 2 || ((uintptr_t)A.y | (uintptr_t)A.res) % ys ||
       ((uintptr_t)A.index | (uintptr_t)A.offsets) % 4)
-    return set_error(LB_EINVAL, pre + "misaligned pointer");
+    return refuse("misaligned pointer");
   const size_t yn = extent(rows, A.ldy, B->b, ys);
-  if (overlaps(A.x, extent(x_rows, A.ldx, B->a, 2), A.y, yn)) return set_error(LB_EINVAL, pre + "x and y overlap");
+  if (overlaps(A.x, extent(x_rows, A.ldx, B->a, 2), A.y, yn)) return refuse("x and y overlap");
   if (A.res && !(A.res == A.y && A.ldr == A.ldy) && overlaps(A.res, extent(rows, A.ldr, B->b, ys), A.y, yn))
-    return set_error(LB_EINVAL, pre + "residual and y overlap (they may be the same rows)");
+    return refuse("residual and y overlap (they may be the same rows)");
   for (const uint16_t *bias : A.bias)
     if (bias && overlaps(bias, (size_t)B->E * B->b * 2, A.y, yn))
-      return set_error(LB_EINVAL, pre + "a bias and y overlap");
+      return refuse("a bias and y overlap");
   if ((A.index && overlaps(A.index, (size_t)rows * 4, A.y, yn)) ||
       (A.offsets && overlaps(A.offsets, (size_t)(B->E + 1) * 4, A.y, yn)))
-    return set_error(LB_EINVAL, pre + "index or offsets and y overlap");
+    return refuse("index or offsets and y overlap");
   return LB_OK;
 }
 

@@ -473,7 +473,8 @@ lb_status lb_bank_destroy(lb_bank *B);
  *             an expert's rows are in the order of the tokens.  -1 behind
  *             the last row
  *   row       tokens x k: the row of every choice
- * No array may overlap another.  ws is device scratch of at least lb_route_ws_bytes bytes (none for 64
+ * No array may overlap another.  ws is device scratch of at least
+ * lb_route_ws_bytes bytes (which never shrink as tokens grow; none for 32
  * tokens or fewer), not shared with calls that may run at the same time.  Only
  * launches kernels; with no tokens it writes offsets alone. */
 lb_status lb_route_ws_bytes(int64_t tokens, int experts, int k, uint64_t *bytes);

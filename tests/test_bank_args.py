@@ -49,7 +49,9 @@ def _route(lib, **kw):
                                  dict(logits=None), dict(ids=None), dict(weights=None), dict(offsets=None),
                                  dict(token=None), dict(row=None), dict(logits=(1 << 20) + 2), dict(row=(6 << 20) + 1),
                                  dict(tokens=65), dict(tokens=65, ws=7 << 20, ws_bytes=63),
-                                 dict(tokens=65, ws=None, ws_bytes=64)])
+                                 dict(tokens=65, ws=None, ws_bytes=64), dict(ld=(1 << 31) + 1), dict(ids=3 << 20),
+                                 dict(row=(4 << 20) + 4), dict(logits=(5 << 20) + 16),
+                                 dict(tokens=65, ws=6 << 20, ws_bytes=1 << 12)])
 def test_route_refusals(lbm, lib, bad):
     assert _route(lib, **bad) == lbm.LB_EINVAL
     assert lib.lb_last_error().startswith(b"lb_route")
@@ -57,9 +59,12 @@ def test_route_refusals(lbm, lib, bad):
 
 def test_route_workspace_sizes(lbm):
     assert lbm.lb_route_ws_bytes(0, 8, 2) == 0
-    assert lbm.lb_route_ws_bytes(64, 8, 2) == 0
-    assert lbm.lb_route_ws_bytes(65, 8, 2) == 2 * 8 * 4
+    assert lbm.lb_route_ws_bytes(32, 8, 2) == 0
+    assert lbm.lb_route_ws_bytes(33, 8, 2) == 3 * 8 * 4
+    assert lbm.lb_route_ws_bytes(4097, 8, 2) == 256 * 8 * 4
     assert lbm.lb_route_ws_bytes(1 << 20, 1024, 64) == 256 * 1024 * 4
+    sizes = [lbm.lb_route_ws_bytes(t, 8, 2) for t in range(0, 9000, 7)]
+    assert sizes == sorted(sizes), "enough for some tokens is enough for fewer"
     for bad in ((-1, 8, 2), (4, 0, 1), (4, 8, 0), (4, 8, 9), (1 << 30, 8, 2)):
         with pytest.raises(lbm.LBError):
             lbm.lb_route_ws_bytes(*bad)

@@ -79,9 +79,40 @@ def test_epilogues(lbm, act, gated, out):
 @pytest.mark.parametrize("M,b,gated", [(1024, 4000, False), (1500, 8200, False), (1100, 4100, True), (16400, 40, False),
                                        (16390, 72, True)])
 def test_many_rows(lbm, M, b, gated):
-    """Enough rows for every launch shape."""
+    """Many rows, wide and narrow, each of them checked."""
     say(f"[case] bank forward M={M} b={b} gated={gated}")
     _forward(lbm, 128, b, 45, True, M, gated=gated, act="gelu" if not gated else "silu", bias=True, residual=True)
+
+
+# the rank makes one to five column tiles per workgroup of the first product
+FEW_ROWS = [(1000, 1000, 20, False), (448, 1500, 20, True), (1792, 72, 20, False), (224, 72, 60, True)]
+MIDDLE = [(2112, 40, s, False) for s in (80, 190, 277, 384, 480)] + [(1100, 300, 20, True), (2112, 72, 45, True)]
+MANY_NARROW = [(4200, 8200, s, True) for s in (20, 64, 95, 127, 160)]
+MANY_WIDE = [(2112, 16400, s, False) for s in (20, 256, 640, 860, 1100)]
+
+
+@pytest.mark.parametrize("a", [128, 131])
+@pytest.mark.parametrize("M,b,s,gated", FEW_ROWS + MIDDLE + MANY_NARROW + MANY_WIDE)
+def test_launch_shapes(lbm, a, M, b, s, gated):
+    """Every kernel with every number of column tiles, aligned x rows and others; a sample of the rows is checked,
+    the first and last of a slot among them."""
+    torch = lbtest.torch_dev()
+    say(f"[case] bank launch shapes a={a} M={M} b={b} s={s} gated={gated}")
+    rng = np.random.default_rng(9)
+    up, ul = _layers(lbm, a, b, s, gated, 1, 11)
+    gate, gl = _layers(lbm, a, b, s, gated, 1, 12) if gated else (None, None)
+    x = lb_synth.activations(M, a, seed=9)
+    bv, _, rv = _extras(rng, 1, b, M, True, False, True, np.float32)
+    B = lbm.Bank(ul, gl)
+    y = torch.full((M, b), float("nan"), device="cuda")
+    B.forward(_dev(x), y, act="silu", bias=_dev(bv), residual=_dev(rv))
+    torch.cuda.synchronize()
+    assert torch.isfinite(y).all()
+    rows = np.unique(np.concatenate([[0, 15, 16, 31, 32, 63, 64, M // 64 * 64 - 1, M - 1], rng.integers(0, M, 60)]))
+    ref, tol = bankref.fused(x[rows], up[0], gate[0] if gated else None, "silu", bv[0], None, rv[rows], np.float32)
+    assert_within(y[torch.from_numpy(rows).cuda()].cpu().numpy(), ref, tol, f"a={a} M={M} b={b} s={s} gated={gated}")
+    B.close()
+    _cache.clear()
 
 
 @pytest.mark.parametrize("a,M", [(4096, 1), (11008, 3), (28672, 1), (8192, 130)])
@@ -116,7 +147,7 @@ def test_small_and_large_values(lbm):
 
 @pytest.mark.parametrize("off,ldx,ldy,ldr", [(0, 1008, 608, 616), (1, 1003, 601, 603), (0, 1001, 600, 600), (8, 1016, 616, 600)])
 @pytest.mark.parametrize("out", [np.float16, np.float32])
-@pytest.mark.parametrize("M", [9, 45, 8200])
+@pytest.mark.parametrize("M", [9, 45, 8200, 33000])
 def test_strides_and_alignment(lbm, off, ldx, ldy, ldr, out, M):
     """Row strides, and x, y and residual that begin inside an allocation; what lies between y's rows stays."""
     torch = lbtest.torch_dev()
@@ -162,7 +193,7 @@ def test_residual_in_place(lbm):
     B.close()
 
 
-@pytest.mark.parametrize("M", [12, 40, 8200])
+@pytest.mark.parametrize("M", [12, 300, 8200, 33000])
 def test_rows_are_independent(lbm, M):
     """NaN and infinity in one row of x stay in that row's output (each launch shape)."""
     torch = lbtest.torch_dev()
@@ -248,13 +279,21 @@ def test_grouped_large(lbm, gated):
     _grouped(lbm, 128, 8200, 45, True, 9, c, gated=gated, act="gelu_tanh", bias=True, gather=True)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_many_rows(lbm, gated):
+    """64-row slots: runs of none, one, a slot less a row, a slot, a slot and a row, and long ones."""
+    say(f"[case] grouped many rows gated={gated}")
+    c = np.array([0, 1, 63, 64, 65, 700, 0, 1151, 131])
+    _grouped(lbm, 128, 16400, 45, False, 9, c, gated=gated, act="silu", bias=True, gather=True, before=3, behind=7)
+
+
 def test_grouped_odd(lbm):
     say("[case] grouped odd sizes")
     c = _counts("ragged", 5, np.random.default_rng(6))
     _grouped(lbm, 259, 131, 63, False, 5, c, act="gelu", bias=True, residual=True, gather=True)
 
 
-@pytest.mark.parametrize("b,rows", [(136, 6), (136, 70), (8200, 1100)])
+@pytest.mark.parametrize("b,rows", [(136, 6), (136, 1100), (8200, 1100), (16400, 2200)])
 def test_grouped_index_out_of_range_reads_zeros(lbm, b, rows):
     """In each launch shape; the rows around the bad ones keep their values."""
     torch = lbtest.torch_dev()
