@@ -573,31 +573,32 @@ __device__ __forceinline__ void with_act(int act, F &&f) {
 template <int CT>
 constexpr int pitch2() { return 32 * CT + 4; }
 
-// The epilogue of one 32-row tile (rows 32 rt .. of the slot) and 32 CT columns
-// from j0 on: up and gate hold the wave's accumulators (gate unused unless
-// G = 2; already activated with READY), lds 32 x (32 CT + 4) floats of the
-// wave's own.
-template <int G, int CT, bool READY = false>
-__device__ __forceinline__ void finish(const BankArgs &A, int e, int row0, int n, int rt, int j0,
-                                       const float16_t (&up)[CT], const float16_t (&gate)[CT], float *lds) {
-  constexpr int kPitch = pitch2<CT>();
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  float bu[CT], bg[CT];
+// The biases of the lane's columns j0 + 32 ct + lane % 32.
+template <int CT>
+__device__ __forceinline__ void load_bias(const BankArgs &A, int side, int e, int j0, float (&v)[CT]) {
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    const int j = j0 + ct * 32 + lr;
-    bu[ct] = A.bias[0] && j < A.b ? h2f(A.bias[0][(size_t)e * A.b + j]) : 0.f;
-    bg[ct] = G == 2 && !READY && A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
+    const int j = j0 + ct * 32 + (threadIdx.x & 31);
+    v[ct] = A.bias[side] && j < A.b ? h2f(A.bias[side][(size_t)e * A.b + j]) : 0.f;
   }
-  with_act(READY ? LB_ACT_NONE : A.act, [&](auto act) {
+}
+
+// The epilogue of one 32-row tile (rows 32 rt .. of the slot) and 32 CT columns
+// from j0 on: up and gate hold the wave's accumulators (gate unused unless
+// G = 2), lds 32 x (32 CT + 4) floats of the wave's own.
+template <int G, int CT>
+__device__ __forceinline__ void finish(const BankArgs &A, int row0, int n, int rt, int j0, const float16_t (&up)[CT],
+                                       const float16_t (&gate)[CT], const float (&bu)[CT], const float (&bg)[CT],
+                                       float *lds) {
+  constexpr int kPitch = pitch2<CT>();
+  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
+  with_act(A.act, [&](auto act) {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float v = up[ct][i] + bu[ct];
-        if constexpr (READY)
-          v = gate[ct][i] * v;
-        else if constexpr (G == 2)
+        if constexpr (G == 2)
           v = activate<decltype(act)::value>(gate[ct][i] + bg[ct]) * v;
         else
           v = activate<decltype(act)::value>(v);
@@ -783,14 +784,21 @@ k_bank_second16(BankArgs A) {
 // layer's and the gate's, without the first and the last.  So twice the waves
 // share what a row tile of 32 offers, and each expands half the signs.  Every
 // wave has 64 columns, hi and lo sums apart.  T and words go through two LDS
-// buffers, chunks of two words of each half.  At the end the second half's
-// sums (activated, with gates) pass to the first through LDS.
-constexpr int kMidT = 16384, kMidChunk = kMidT + 4096;              // T, words
-constexpr int kMidLds = 32768 + 4 * 32 * pitch2<1>() * 4;           // the sums handed over, the epilogue's rows
+// buffers, a word of each half at a time, and from there into two sets of
+// registers.  At the end the waves of the two halves exchange sums through LDS,
+// each for one of their two column tiles, and finish the other.  128 gated rows
+// 4096 -> 11008 at s = 431 take 18.1 us: 10.1e9 flops of hi and lo products, 9
+// us at a large library product's rate on all CUs, here on the 172 of 256 that
+// have a workgroup.  128 columns a workgroup fill more CUs and expand no more
+// signs, but read T twice as often: 18.5 us, 512 rows 24.6 against 21.2.  More
+// chunks on their way (rings of 4 and 6: 18.5, 18.8) or two words a chunk, which
+// leaves a workgroup a CU (64 layers, 1542 rows: 19.2 against 15.6), are slower.
+constexpr int kMidT = 8192, kMidChunk = kMidT + 2048;  // T, words
+constexpr int kMidLds = 32768 + 8 * 32 * pitch2<1>() * 4;  // the sums exchanged, the epilogue's rows
 static_assert(2 * kMidChunk <= kMidLds, "the chunks fit too");
 
 template <int G>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 4)
 k_bank_second_mid(BankArgs A, int slots) {
   __shared__ __align__(16) unsigned char sm[kMidLds];
   const int ncb = (A.b + 255) >> 8;
@@ -803,17 +811,14 @@ k_bank_second_mid(BankArgs A, int slots) {
   const int first = G == 2 ? nit : (nit + 1) >> 1;         // words of the first half; the longer one
   const int count = half ? G * nit - first : first;        // of this wave's
   const int word0 = G == 1 && half ? first : 0, side = G == 2 ? half : 0;  // its first word, within its side
-  const int nch = (first + 1) >> 1;
-  // the wave's copies of a chunk: 2 KB of its half's T (words past the last
-  // read on, T has room behind it), and two words of its 64 columns
-  const uint16_t *src = A.T + ((size_t)slot * G * nit + (half ? first : 0)) * 2048 + (w & 3) * 1024 + lane * 8;
-  int at = 0;
-  auto issue_t = [&]() {
-#pragma unroll
-    for (int f = 0; f < 2; ++f) dma16(src + f * 512, sm + at + (w * 2 + f) * 1024);
-    src += 4096;
+  // the wave's copies of a chunk: 1 KB of its half's T (words past the last
+  // read on, T has room behind it), and a word of its columns
+  const uint16_t *src = A.T + ((size_t)slot * G * nit + (half ? first : 0)) * 2048 + (w & 3) * 512 + lane * 8;
+  auto issue_t = [&](int at) {
+    dma16(src, sm + at + w * 1024);
+    src += 2048;
   };
-  issue_t();
+  issue_t(0);
   int e, row0, n;
   if (!find_slot(A, A.slot0 + slot, e, row0, n)) {
     wait_loads<0>();  // the copies land before the LDS is left
@@ -821,13 +826,15 @@ k_bank_second_mid(BankArgs A, int slots) {
   }
   const LayerDesc D = layer_of(A, side, e);
   const unsigned jw = min(j0 + lane, A.b16 - 1);
-  auto issue_w = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      dma4((const void *)(D.su + (size_t)min(word0 + min(2 * c + i, max(count - 1, 0)), nit - 1) * A.b16 + jw),
-           sm + at + kMidT + (w * 2 + i) * 256);
+  auto issue_w = [&](int c, int at) {
+    dma4((const void *)(D.su + (size_t)min(word0 + min(c, max(count - 1, 0)), nit - 1) * A.b16 + jw),
+         sm + at + kMidT + w * 256);
   };
-  issue_w(0);
+  issue_w(0, 0);
+  if (first > 1) {
+    issue_t(kMidChunk);
+    issue_w(1, kMidChunk);
+  }
   uint32_t hh[2][2];  // [path][column tile], two copies per register
 #pragma unroll
   for (int pp = 0; pp < 2; ++pp)
@@ -836,90 +843,98 @@ k_bank_second_mid(BankArgs A, int slots) {
       const uint16_t h = D.h[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
       hh[pp][ct] = h | ((uint32_t)h << 16);
     }
+  const int jm = j0 + half * 32;  // of its two column tiles the wave finishes this one
+  float bu[1], bg[1];
+  load_bias<1>(A, 0, e, jm, bu);
+  load_bias<1>(A, G - 1, e, jm, bg);
   float16_t acc[2], low[2];
 #pragma unroll
   for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[ct][i] = low[ct][i] = 0.f;
 
-  for (int c = 0; c < nch; ++c) {
-    wait_loads<0>();  // the chunk has landed: this wave's part, then everybody's
-    lds_barrier();
-    const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at + half * 8192) + lane;
-    const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + kMidT + w * 512) + lr;
-    at ^= kMidChunk;
-    if (c + 1 < nch) {  // into the place that all have left behind
-      issue_t();
-      issue_w(c + 1);
-    }
+  // chunk c is read from LDS during the products of the one before it
+  struct Operands {
+    u32x4 t[2][2];  // [half of the word][plane]
+    uint32_t wd[2];
+  };
+  auto read = [&](Operands &o, int at) {
+    const u32x4 *tl = reinterpret_cast<const u32x4 *>(sm + at + half * 4096) + lane;
+    const uint32_t *wl = reinterpret_cast<const uint32_t *>(sm + at + kMidT + w * 256) + lr;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int it = 2 * c + i;
-      if (it >= count) break;
-      const int pp = word0 + it >= A.Wk;
-      const int left = A.s - 32 * (word0 + it - pp * A.Wk);
-      u32x4 t[2][2];  // [half of the word][plane]
+    for (int f = 0; f < 4; ++f) o.t[f >> 1][f & 1] = tl[f * 64];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) t[f >> 1][f & 1] = tl[i * 256 + f * 64];
-      uint32_t wd[2];
+    for (int ct = 0; ct < 2; ++ct) o.wd[ct] = wl[ct * 32];
+  };
+  auto multiply = [&](const Operands &o, int c) {
+    if (c >= count) return;
+    const int pp = word0 + c >= A.Wk;
+    const int left = A.s - 32 * (word0 + c - pp * A.Wk);
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) wd[ct] = wl[i * 64 + ct * 32] << (4 * lh);
+    for (int st = 0; st < 2; ++st) {
+      if (st == 1 && left <= 16) break;  // padding
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        if (st == 1 && left <= 16) break;  // padding
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-          const half8_t b = flip(splat(pp ? hh[1][ct] : hh[0][ct]), wd[ct] << (8 * st));
-          acc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st][0]), b, acc[ct], 0, 0, 0);
-          low[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st][1]), b, low[ct], 0, 0, 0);
-        }
+      for (int ct = 0; ct < 2; ++ct) {
+        const half8_t b = flip(splat(pp ? hh[1][ct] : hh[0][ct]), o.wd[ct] << (4 * lh + 8 * st));
+        acc[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(o.t[st][0]), b, acc[ct], 0, 0, 0);
+        low[ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(o.t[st][1]), b, low[ct], 0, 0, 0);
       }
     }
+  };
+  Operands even, odd;
+  if (first > 1)  // the chunk has landed: this wave's part, then everybody's
+    wait_loads<2>();
+  else
+    wait_loads<0>();
+  lds_barrier();
+  read(even, 0);
+  auto step = [&](int c, const Operands &now, Operands &next, int at) {  // chunk c, which lay at `at`
+    if (c + 1 < first) {
+      wait_loads<0>();
+      lds_barrier();  // and everybody has read chunk c
+      if (c + 2 < first) {
+        issue_t(at);
+        issue_w(c + 2, at);
+      }
+      read(next, kMidChunk - at);
+    }
+    multiply(now, c);
+  };
+  for (int c = 0; c < first; c += 2) {
+    step(c, even, odd, 0);
+    if (c + 1 < first) step(c + 1, odd, even, kMidChunk);
   }
 #pragma unroll
   for (int ct = 0; ct < 2; ++ct) acc[ct] += low[ct] * 0x1p-11f;
   __syncthreads();
-  float4_t *over = reinterpret_cast<float4_t *>(sm) + (w & 3) * 512 + lane;  // [column tile][registers / 4][lane]
-  if (half) {
-    if constexpr (G == 2) {
-      float bg[2];
+  // a column tile's sums go to the wave of the other half that finishes it
+  float4_t *over = reinterpret_cast<float4_t *>(sm) + lane;  // [wave][registers / 4][lane]
 #pragma unroll
-      for (int ct = 0; ct < 2; ++ct) {
-        const int j = j0 + ct * 32 + lr;
-        bg[ct] = A.bias[1] && j < A.b ? h2f(A.bias[1][(size_t)e * A.b + j]) : 0.f;
-      }
-      with_act(A.act, [&](auto act) {
+  for (int q = 0; q < 4; ++q) {
+    float4_t v;
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[ct][i] = activate<decltype(act)::value>(acc[ct][i] + bg[ct]);
-      });
-    }
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        over[(ct * 4 + q) * 64] = float4_t{acc[ct][4 * q], acc[ct][4 * q + 1], acc[ct][4 * q + 2], acc[ct][4 * q + 3]};
+    for (int i = 0; i < 4; ++i) v[i] = half ? acc[0][4 * q + i] : acc[1][4 * q + i];
+    over[(w * 4 + q) * 64] = v;
   }
   __syncthreads();
-  if (half) return;
+  if (jm >= A.b) return;
+  float16_t own[1], other[1];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) own[0][i] = half ? acc[1][i] : acc[0][i];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4_t v = over[((w ^ 4) * 4 + q) * 64];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) other[0][4 * q + i] = v[i];
+  }
   float *rows = reinterpret_cast<float *>(sm + 32768) + w * 32 * pitch2<1>();
-#pragma unroll
-  for (int ct = 0; ct < 2; ++ct) {
-    if (j0 + ct * 32 >= A.b) break;
-    float16_t up[1] = {acc[ct]}, other[1];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4_t v = over[(ct * 4 + q) * 64];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) other[0][4 * q + i] = v[i];
-    }
-    if constexpr (G == 2) {
-      finish<2, 1, true>(A, e, row0, n, 0, j0 + ct * 32, up, other, rows);
-    } else {
-      up[0] += other[0];
-      finish<1, 1>(A, e, row0, n, 0, j0 + ct * 32, up, other, rows);
-    }
+  if constexpr (G == 1) {
+    own[0] += other[0];
+    finish<1, 1>(A, row0, n, 0, jm, own, other, bu, bg, rows);
+  } else if (half) {
+    finish<2, 1>(A, row0, n, 0, jm, other, own, bu, bg, rows);
+  } else {
+    finish<2, 1>(A, row0, n, 0, jm, own, other, bu, bg, rows);
   }
 }
 
@@ -1058,9 +1073,12 @@ k_bank_second_wide(BankArgs A, int slots) {
     }
   __syncthreads();
   float *lds = reinterpret_cast<float *>(sm) + w * 32 * pitch2<2>();
+  float bu[2], bg[2];
+  load_bias<2>(A, 0, e, j0, bu);
+  load_bias<2>(A, G - 1, e, j0, bg);
 #pragma unroll
   for (int rt = 0; rt < 2; ++rt)
-    if (rt * 32 < n && j0 < A.b) finish<G, 2>(A, e, row0, n, rt, j0, acc[0][rt], acc[G - 1][rt], lds);
+    if (rt * 32 < n && j0 < A.b) finish<G, 2>(A, row0, n, rt, j0, acc[0][rt], acc[G - 1][rt], bu, bg, lds);
 }
 
 // ------------------------------------------------------------------ host
