@@ -660,10 +660,13 @@ __device__ __forceinline__ void finish(const BankArgs &A, int row0, int n, int r
   __builtin_amdgcn_wave_barrier();
 }
 
-// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 32 columns
-// of all G sides, the waves interleaved over the (side, path, 32-column word)
-// parts of K, so that everything is requested at once; their sums are added in
-// wave order through LDS, where a thread finishes two neighbouring columns.
+// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 16 CT
+// columns of all G sides, the waves interleaved over the (side, path, 32-column
+// word) parts of K, U of them requested at once; their sums are added in wave
+// order through LDS, where a thread finishes two neighbouring columns.  Bound by
+// latency: 4.0 us for one row of 4096 -> 4096 at s = 86 (all of K requested at
+// once), 5.0 us for one gated row 4096 -> 11008 at s = 133; 8.8 us for 8 layers
+// of it, a row each (9.2 MB).
 template <int G, int CT, int NW, int U>
 __global__ void __launch_bounds__(NW * 64)
 k_bank_second16(BankArgs A) {
@@ -942,13 +945,16 @@ k_bank_second_mid(BankArgs A, int slots) {
 // of all G sides.  T and the sign words are copied into LDS in chunks of two
 // 32-column words of a path, the next chunk during the products of one: T once
 // for the workgroup, a wave's words by itself.  (Three or four chunks on their
-// way, or longer ones, changed nothing.)  With two waves on a SIMD (G = 2; four
-// with G = 1) a wave issues an instruction every four or five cycles at best, so
-// besides the products (hi and lo: 104e9 flops for 4096 gated rows of 4096 ->
-// 11008 at s = 133, 47 us of the 122 at the clock it runs at) what counts is
-// instructions: per 16 columns and column tile 4 shifts and 8 sign flips, shared
-// by two row tiles, and everything that is not per product is out of the loop.
-// Without its epilogue the kernel takes 98 us, without products 59.
+// way, longer ones, a chunk's first operands read before the last products of
+// the one before it, or 8 waves and 512 columns changed nothing or cost up to
+// 8%.)  With two waves on a SIMD (G = 2; four with G = 1) a wave issues an
+// instruction every four or five cycles at best, so besides the products (hi and
+// lo: 104e9 flops for 4096 gated rows of 4096 -> 11008 at s = 133, 47 us of the
+// 122 at the clock it runs at) what counts is instructions: per 16 columns and
+// column tile 4 shifts and 8 sign flips, shared by two row tiles, and everything
+// that is not per product is out of the loop.  Without its epilogue the kernel
+// takes 98 us, without products 59.  8192 rows of 11008 -> 4096 in 8 layers
+// (G = 1) take 51 us.
 constexpr int kW2T = 16384, kW2Chunk = kW2T + 2048;                              // T, words
 constexpr int kW2Lds = 2 * kW2Chunk;
 static_assert(kW2Lds >= 4 * 32 * pitch2<2>() * 4, "the epilogue's rows fit");
