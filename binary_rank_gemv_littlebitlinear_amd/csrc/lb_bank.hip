@@ -233,25 +233,27 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // ------------------------------------------------------- first product
-// Few rows (slots of 16): a workgroup of 8 waves computes 16 rows x 16 latent
+// Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 16 latent
 // columns over the whole input dimension, wave w on the blocks of 32 inputs
-// 2 w, 2 w + 1, 2 w + 16, ... (pairs: whole 128-byte lines of x; single blocks
+// 2 w, 2 w + 1, 2 w + 2 NW, ... (pairs: whole 128-byte lines of x; single blocks
 // took 7.2 us, not 4.3, for 16 rows of 1024); the waves' sums are added in wave
 // order through LDS.  Bound by latency and by what one CU can issue, hence the
 // small tile (a 32 x 32 one took 6.5 us for one row of a 4096-wide layer, two
 // thirds of it on the four waves a SIMD that wanted to expand signs at once),
 // operands of kF1U blocks requested together, and g (the same for all columns)
 // straight into the wave's LDS.  One row of 4096: 5.1 us, 16 rows 7.8; 11008:
-// 7.4 and 14.5.  4 waves take 5.8 and 8.2, 11.2 and 15.0, no less for 1024; 16
-// waves 6.1 and 11.2, 8.8 and 18.8.
+// 7.4 and 14.5.  4 waves take 5.8 and 8.2, 11.2 and 15.0; 16 waves 6.1 and 11.2,
+// 8.8 and 18.8.  Up to 2048 inputs, all blocks of which 4 waves request at once,
+// 4 do: 64 layers of 1024 inputs, 60 gated rows (some 800 workgroups) 5.9 us
+// against 8.0 with 8, and one slot as fast (1024 inputs 3.8 against 3.7, 16 rows
+// of 2048 5.7 against 5.4).
 // v_mfma_f32_16x16x32_f16: A[i][k] in lane i + 16 (k / 8), B[k][j] in lane
 // j + 16 (k / 8), D[i][j] in lane j + 16 (i / 4), register i % 4.
-constexpr int kF1U = 16, kF1Waves = 8;
+constexpr int kF1U = 16;
 
-template <bool XV>
-__global__ void __launch_bounds__(kF1Waves * 64)
+template <int NW, bool XV>
+__global__ void __launch_bounds__(NW * 64)
 k_bank_first16(BankArgs A) {
-  constexpr int NW = kF1Waves;
   __shared__ __align__(16) float red[NW * 256];
   const int tile = blockIdx.x, slot = blockIdx.y, W2 = 2 * A.Wk;
   int seg = 0;
@@ -1172,12 +1174,13 @@ lb_status grow(lb_bank *B, int64_t rows, const char *who, bool in_call, hipStrea
   return LB_OK;
 }
 
+template <int NW>
 hipError_t launch_first16(const BankArgs &A, int slots, hipStream_t st) {
   const dim3 grid((unsigned)(A.G * A.P * A.Wk * 2), (unsigned)slots);
   if (A.xvec)
-    k_bank_first16<true><<<grid, dim3(kF1Waves * 64), 0, st>>>(A);
+    k_bank_first16<NW, true><<<grid, dim3(NW * 64), 0, st>>>(A);
   else
-    k_bank_first16<false><<<grid, dim3(kF1Waves * 64), 0, st>>>(A);
+    k_bank_first16<NW, false><<<grid, dim3(NW * 64), 0, st>>>(A);
   return hipGetLastError();
 }
 
@@ -1319,7 +1322,7 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
     A.slot0 = (int)s0;
     hipError_t e;
     if (A.lg == 4) {
-      e = launch_first16(A, ns, st);
+      e = A.R1 > 4 * kF1U ? launch_first16<8>(A, ns, st) : launch_first16<4>(A, ns, st);
       // 32 columns a workgroup when all of them start at once, else 64 (8
       // experts of 4096 -> 11008, gated, a row each: 9.1 against 11.0 us; one
       // row alone: 5.6 against 5.0 us)

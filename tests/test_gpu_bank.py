@@ -115,7 +115,7 @@ def test_launch_shapes(lbm, a, M, b, s, gated):
     _cache.clear()
 
 
-@pytest.mark.parametrize("a,M", [(4096, 1), (11008, 3), (28672, 1), (8192, 130)])
+@pytest.mark.parametrize("a,M", [(2049, 5), (2743, 16), (4096, 1), (11008, 3), (28672, 1), (8192, 130)])
 def test_wide_inputs(lbm, a, M):
     say(f"[case] bank forward a={a} M={M}")
     _forward(lbm, a, 96, 86, True, M, out=np.float32)
