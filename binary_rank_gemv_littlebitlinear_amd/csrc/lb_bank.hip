@@ -16,11 +16,15 @@
 //
 // Rounding: the operands +-g and +-h are exact in fp16 (a stored scale with
 // its sign bit flipped), x is fp16, the accumulators are fp32.  w is kept as
-// two fp16 numbers, hi = fp16(w) and lo = fp16(2^11 (w - hi)), multiplied
-// by +-h and +-2^-11 h: the pair carries 22 bits of w for every |w| < 65504
-// down to 2^-14 (an absolute 2^-36 below), so y is rounded once, at
-// the end, whatever the batch size.  With w as one fp16 number the error of
-// an fp16 y is 1.4 times that of its own rounding (1.75 times when gated).
+// two fp16 numbers, hi = fp16(w) and lo = fp16(2^11 (w - hi)): the pair
+// carries 22 bits of w for every |w| < 65504 down to 2^-14 (an absolute
+// 2^-36 below), so y is rounded once, at the end, whatever the batch size.
+// Both are multiplied by the same +-h; the lo sums are kept apart and joined
+// to the hi sums times 2^-11 in fp32.  (2^-11 h as an operand would lose a
+// bit for every halving of |h| below 2^-3, where it is no longer normal;
+// k_bank_second_wide without gates uses one, and scales h first.)  With w as
+// one fp16 number the error of an fp16 y is 1.4 times that of its own
+// rounding (1.75 times when gated).
 //
 // Rows are cut into slots of n rows (16, 32 or 64, see run) of one expert.
 // Without offsets slot i is rows [i n, (i + 1) n); with offsets every wave
@@ -665,7 +669,9 @@ __device__ __forceinline__ void finish(const BankArgs &A, int row0, int n, int r
 // Few rows (slots of 16): a workgroup of NW waves computes 16 rows x 16 CT
 // columns of all G sides, the waves interleaved over the (side, path, 32-column
 // word) parts of K, U of them requested at once; their sums are added in wave
-// order through LDS, where a thread finishes two neighbouring columns.  Bound by
+// order through LDS, where a thread finishes two neighbouring columns.  A wave's
+// parts of the layer come before those of the gate, so it holds the hi and lo
+// sums of one side only.  Bound by
 // latency: 4.0 us for one row of 4096 -> 4096 at s = 86 (all of K requested at
 // once), 5.0 us for one gated row 4096 -> 11008 at s = 133; 8.8 us for 8 layers
 // of it, a row each (9.2 MB).
@@ -681,13 +687,24 @@ k_bank_second16(BankArgs A) {
 
   const int nit = A.P * A.Wk, items = G * nit;
   unsigned jc[CT];
-  float4_t acc[G][CT];
+  float4_t acc[CT], low[CT];  // hi and lo sums of the side in hand
+  const auto clear = [&]() {
 #pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    jc[c] = min(j0 + 16 * c + lr, A.b16 - 1);
+    for (int c = 0; c < CT; ++c) acc[c] = low[c] = float4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
 #pragma unroll
-    for (int q = 0; q < G; ++q) acc[q][c] = float4_t{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int c = 0; c < CT; ++c) jc[c] = min(j0 + 16 * c + lr, A.b16 - 1);
+  int side = 0;
+  const auto next_side = [&]() {  // the side's sums to LDS
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(((w * G + side) * CT + ct) * 4 + i) * 64 + lane] = fmaf(low[ct][i], 0x1p-11f, acc[ct][i]);
+    clear();
+    ++side;
+  };
   // the lane's 8 latent columns of a word: block o / 2, half o % 2
   const uint16_t *tp = A.T + (size_t)slot * items * 2048 + (o >> 1) * 1024 + ((o & 1) * 32 + lr) * 8;
   for (int x0 = w; x0 < items; x0 += U * NW) {
@@ -712,29 +729,16 @@ k_bank_second16(BankArgs A) {
     for (int u = 0; u < U; ++u) {
       const int x = x0 + u * NW;
       if (x >= items) break;
-      auto mma = [&](float4_t (&c)[CT]) {
+      if (G == 2 && side == 0 && x >= nit) next_side();
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const uint16_t hs = f2h(h2f(hv[u][ct]) * 0x1p-11f);
-          const uint32_t wl = wd[u][ct] << (4 * o);
-          c[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              as_h8(t[u][0]), flip(splat(hv[u][ct] | ((uint32_t)hv[u][ct] << 16)), wl), c[ct], 0, 0, 0);
-          c[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              as_h8(t[u][1]), flip(splat(hs | ((uint32_t)hs << 16)), wl), c[ct], 0, 0, 0);
-        }
-      };
-      if (G == 1 || x < nit)
-        mma(acc[0]);
-      else
-        mma(acc[G - 1]);
+      for (int ct = 0; ct < CT; ++ct) {
+        const half8_t b = flip(splat(hv[u][ct] | ((uint32_t)hv[u][ct] << 16)), wd[u][ct] << (4 * o));
+        acc[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(t[u][0]), b, acc[ct], 0, 0, 0);
+        low[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(t[u][1]), b, low[ct], 0, 0, 0);
+      }
     }
   }
-#pragma unroll
-  for (int q = 0; q < G; ++q)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[(((w * G + q) * CT + ct) * 4 + i) * 64 + lane] = acc[q][ct][i];
+  while (side < G) next_side();  // a wave may have no part of a side
   __syncthreads();
   for (int id = threadIdx.x; id < n * 8 * CT; id += NW * 64) {
     const int row = id / (8 * CT), c = id % (8 * CT) * 2, j = j0 + c;
@@ -943,6 +947,17 @@ k_bank_second_mid(BankArgs A, int slots) {
   }
 }
 
+// The power of two (its exponent) that brings a column's h into [2^14, 2^15), so
+// that 2^-11 h is exact too: that of the larger of two paths (h0 | h1 << 16), or,
+// where a column of the wave has them further apart than 2^16, each path's own.
+__device__ __forceinline__ int lift(uint32_t h01, int path) {
+  const auto by = [](float h) { return h > 0.f && h < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(h) : 0; };
+  const float h0 = fabsf(h2f((uint16_t)h01)), h1 = fabsf(h2f((uint16_t)(h01 >> 16)));
+  const float top = fmaxf(h0, h1), low = fminf(h0, h1);
+  if (__any(low > 0.f && low < top * 0x1p-16f)) return by(path ? h1 : h0);
+  return by(top);
+}
+
 // Many rows: a workgroup of 4 waves, 64 rows of one slot, every wave 64 columns
 // of all G sides.  T and the sign words are copied into LDS in chunks of two
 // 32-column words of a path, the next chunk during the products of one: T once
@@ -953,10 +968,14 @@ k_bank_second_mid(BankArgs A, int slots) {
 // instruction every four or five cycles at best, so besides the products (hi and
 // lo: 104e9 flops for 4096 gated rows of 4096 -> 11008 at s = 133, 47 us of the
 // 122 at the clock it runs at) what counts is instructions: per 16 columns and
-// column tile 4 shifts and 8 sign flips, shared by two row tiles, and everything
-// that is not per product is out of the loop.  Without its epilogue the kernel
+// column tile 4 shifts and 4 sign flips (8 with G = 1), shared by two row tiles,
+// and everything that is not per product is out of the loop.  Without its epilogue the kernel
 // takes 98 us, without products 59.  8192 rows of 11008 -> 4096 in 8 layers
-// (G = 1) take 51 us.
+// (G = 1) take 52 us.
+// With gates the lo sums of the side in hand have registers of their own (240 of
+// 256).  Without, that would leave two waves on a SIMD instead of four (58 us),
+// so one sum takes hi h and lo 2^-11 h, both scaled by the column's `lift`, which
+// is divided out at the end: powers of two, exact throughout.
 constexpr int kW2T = 16384, kW2Chunk = kW2T + 2048;                              // T, words
 constexpr int kW2Lds = 2 * kW2Chunk;
 static_assert(kW2Lds >= 4 * 32 * pitch2<2>() * 4, "the epilogue's rows fit");
@@ -1007,14 +1026,14 @@ k_bank_second_wide(BankArgs A, int slots) {
     fs ^= kW2Chunk;
   };
   issue_w();
-  uint16_t hv[G][2][2];
+  uint32_t hv[G][2];  // of the column tiles' two paths (one path: twice the same)
 #pragma unroll
   for (int q = 0; q < G; ++q)
 #pragma unroll
-    for (int pp = 0; pp < 2; ++pp)
-#pragma unroll
-      for (int ct = 0; ct < 2; ++ct)
-        hv[q][pp][ct] = (q ? D1.h : D0.h)[(size_t)(pp < A.P ? pp : 0) * A.b16 + min(j0 + ct * 32 + lr, A.b16 - 1)];
+    for (int ct = 0; ct < 2; ++ct) {
+      const gu16 h = (q ? D1.h : D0.h) + min(j0 + ct * 32 + lr, A.b16 - 1);
+      hv[q][ct] = h[0] | ((uint32_t)h[(size_t)(A.P - 1) * A.b16] << 16);
+    }
   float16_t acc[G][2][2];
 #pragma unroll
   for (int q = 0; q < G; ++q)
@@ -1028,14 +1047,34 @@ k_bank_second_wide(BankArgs A, int slots) {
   const int paths = G * A.P;
   int at = 0;
 #pragma unroll
-  for (int q = 0; q < G; ++q)
+  for (int q = 0; q < G; ++q) {
+    float16_t low[2][2];  // lo sums, with gates
+    if constexpr (G == 2) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) low[rt][ct][i] = 0.f;
+    }
     for (int pp = 0; pp < A.P; ++pp) {
-      uint32_t hh[2], hl[2];  // the path's h and 2^-11 h: two copies per register
+      uint32_t hh[2], hl[2];  // the path's h and, without gates, 2^-11 h: two copies per register
 #pragma unroll
       for (int ct = 0; ct < 2; ++ct) {
-        const uint16_t h = pp ? hv[q][1][ct] : hv[q][0][ct], hs = f2h(h2f(h) * 0x1p-11f);
+        uint16_t h = (uint16_t)(pp ? hv[q][ct] >> 16 : hv[q][ct]);
+        if constexpr (G == 1) {
+          const int by = lift(hv[q][ct], pp);
+          const float hf = ldexpf(h2f(h), by);
+          const uint16_t hs = f2h(hf * 0x1p-11f);
+          h = f2h(hf);
+          hl[ct] = hs | ((uint32_t)hs << 16);
+          const int was = lift(hv[q][ct], 0);
+          if (pp && __any(by != was)) {
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) acc[q][rt][ct] *= ldexpf(1.f, by - was);
+          }
+        }
         hh[ct] = h | ((uint32_t)h << 16);
-        hl[ct] = hs | ((uint32_t)hs << 16);
       }
       for (int c = 0; c < nch; ++c) {
         wait_loads<0>();  // the chunk has landed: this wave's part, then everybody's
@@ -1068,17 +1107,31 @@ k_bank_second_wide(BankArgs A, int slots) {
 #pragma unroll
           for (int ct = 0; ct < 2; ++ct) {
             const uint32_t sh = wd[ct] << (8 * (st & 1));
-            const half8_t bh = flip(splat(hh[ct]), sh), bl = flip(splat(hl[ct]), sh);
+            const half8_t bh = flip(splat(hh[ct]), sh), bl = G == 1 ? flip(splat(hl[ct]), sh) : bh;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int rt = 0; rt < 2; ++rt)
-                acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][k]), k ? bl : bh,
-                                                                        acc[q][rt][ct], 0, 0, 0);
+            for (int rt = 0; rt < 2; ++rt) {
+              acc[q][rt][ct] = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][0]), bh, acc[q][rt][ct], 0, 0, 0);
+              float16_t &lo = G == 1 ? acc[q][rt][ct] : low[rt][ct];
+              lo = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(t[st & 1][rt][1]), bl, lo, 0, 0, 0);
+            }
           }
         }
       }
     }
+    if constexpr (G == 2) {
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) acc[q][rt][ct] += low[rt][ct] * 0x1p-11f;
+    } else {
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) {
+        const float f = ldexpf(1.f, -lift(hv[q][ct], A.P - 1));
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) acc[q][rt][ct] *= f;
+      }
+    }
+  }
   __syncthreads();
   float *lds = reinterpret_cast<float *>(sm) + w * 32 * pitch2<2>();
   float bu[2], bg[2];
