@@ -1397,9 +1397,6 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   return LB_OK;
 }
 
-// Bytes from the first to the last element of `rows` rows of `n` elements.
-size_t extent(int64_t rows, int64_t ld, int64_t n, int size) { return (size_t)((rows - 1) * ld + n) * size; }
-
 // The checks both calls share.
 lb_status check(const lb_bank *B, const BankArgs &A, int64_t rows, int64_t x_rows, int y_type, const char *who) {
   const auto refuse = [who](const char *why) { return set_error(LB_EINVAL, std::string(who) + ": " + why); };
@@ -1419,15 +1416,17 @@ lb_status check(const lb_bank *B, const BankArgs &A, int64_t rows, int64_t x_row
   if (((uintptr_t)A.x | (uintptr_t)A.bias[0] | (uintptr_t)A.bias[1]) % 2 || ((uintptr_t)A.y | (uintptr_t)A.res) % ys ||
       ((uintptr_t)A.index | (uintptr_t)A.offsets) % 4)
     return refuse("misaligned pointer");
-  const size_t yn = extent(rows, A.ldy, B->b, ys);
-  if (overlaps(A.x, extent(x_rows, A.ldx, B->a, 2), A.y, yn)) return refuse("x and y overlap");
-  if (A.res && !(A.res == A.y && A.ldr == A.ldy) && overlaps(A.res, extent(rows, A.ldr, B->b, ys), A.y, yn))
+  const auto strided = [](const void *p, int64_t r, int64_t ld, int64_t n, int size) {
+    return Rows{p, r, (size_t)ld * size, (size_t)n * size};
+  };
+  const auto flat = [](const void *p, int64_t n, int size) { return Rows{p, 1, 0, (size_t)n * size}; };
+  const Rows y = strided(A.y, rows, A.ldy, B->b, ys);
+  if (meet(strided(A.x, x_rows, A.ldx, B->a, 2), y)) return refuse("x and y overlap");
+  if (A.res && !(A.res == A.y && A.ldr == A.ldy) && meet(strided(A.res, rows, A.ldr, B->b, ys), y))
     return refuse("residual and y overlap (they may be the same rows)");
   for (const uint16_t *bias : A.bias)
-    if (bias && overlaps(bias, (size_t)B->E * B->b * 2, A.y, yn))
-      return refuse("a bias and y overlap");
-  if ((A.index && overlaps(A.index, (size_t)rows * 4, A.y, yn)) ||
-      (A.offsets && overlaps(A.offsets, (size_t)(B->E + 1) * 4, A.y, yn)))
+    if (bias && meet(flat(bias, B->E * B->b, 2), y)) return refuse("a bias and y overlap");
+  if ((A.index && meet(flat(A.index, rows, 4), y)) || (A.offsets && meet(flat(A.offsets, B->E + 1, 4), y)))
     return refuse("index or offsets and y overlap");
   return LB_OK;
 }

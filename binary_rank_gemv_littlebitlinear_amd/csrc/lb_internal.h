@@ -30,6 +30,7 @@
 #include <vector>
 
 #include "../../include/lb.h"
+#include "lb_rows.h"
 
 namespace lbi {
 
@@ -53,12 +54,6 @@ struct DeviceGuard {
     if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
   }
 };
-
-// Whether the np bytes at p and the nq bytes at q share any.
-inline bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
-  const char *a = (const char *)p, *b = (const char *)q;
-  return a < b + nq && b < a + np;
-}
 
 struct Layer {
   int64_t a = 0, b = 0, s = 0;

@@ -445,15 +445,14 @@ extern "C" lb_status lb_route(const void *logits, int logits_type, int64_t ld, i
     return set_error(LB_EINVAL, "lb_route: misaligned pointer");
   const int ls = logits_type == LB_F32 ? 4 : 2;
   const size_t n = (size_t)tokens * k * 4;
-  const struct {
-    const void *p;
-    size_t bytes;
-  } arrays[] = {{logits, tokens ? (size_t)((tokens - 1) * ld + experts) * ls : 0}, {offsets, (size_t)(experts + 1) * 4},
-                {ids, n}, {weights, n}, {token, n}, {row, n}, {ws, (size_t)need}};
-  for (const auto &u : arrays)
-    for (const auto *v = &u + 1; v != std::end(arrays); ++v)
-      if (u.bytes && v->bytes && overlaps(u.p, u.bytes, v->p, v->bytes))
-        return set_error(LB_EINVAL, "lb_route: two arrays overlap");
+  const int64_t any = tokens > 0;
+  const Rows arrays[] = {{logits, tokens, (size_t)ld * ls, (size_t)experts * ls},
+                         {offsets, 1, 0, (size_t)(experts + 1) * 4},
+                         {ids, any, 0, n}, {weights, any, 0, n}, {token, any, 0, n}, {row, any, 0, n},
+                         {ws, need > 0, 0, (size_t)need}};
+  for (const Rows &u : arrays)
+    for (const Rows *v = &u + 1; v != std::end(arrays); ++v)
+      if (meet(u, *v)) return set_error(LB_EINVAL, "lb_route: two arrays overlap");
   RouteArgs A = {};
   A.logits = logits;
   A.ld = ld;
@@ -505,12 +504,13 @@ extern "C" lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy
   const int os = out_type == LB_F32 ? 4 : 2;
   if ((uintptr_t)y % 2 || ((uintptr_t)row | (uintptr_t)weights) % 4 || ((uintptr_t)out | (uintptr_t)residual) % os)
     return set_error(LB_EINVAL, "lb_route_combine: misaligned pointer");
-  const size_t on = (size_t)((tokens - 1) * ldo + width) * os;
-  if ((y_rows && overlaps(y, (size_t)((y_rows - 1) * ldy + width) * 2, out, on)) ||
-      overlaps(row, (size_t)tokens * k * 4, out, on) || overlaps(weights, (size_t)tokens * k * 4, out, on))
+  const Rows o = {out, tokens, (size_t)ldo * os, (size_t)width * os};
+  const size_t choices = (size_t)tokens * k * 4;
+  if (meet({y, y_rows, (size_t)ldy * 2, (size_t)width * 2}, o) || meet({row, 1, 0, choices}, o) ||
+      meet({weights, 1, 0, choices}, o))
     return set_error(LB_EINVAL, "lb_route_combine: an input and out overlap");
   if (residual && !(residual == out && ldr == ldo) &&
-      overlaps(residual, (size_t)((tokens - 1) * ldr + width) * os, out, on))
+      meet({residual, tokens, (size_t)ldr * os, (size_t)width * os}, o))
     return set_error(LB_EINVAL, "lb_route_combine: residual and out overlap (they may be the same rows)");
   CombineArgs A = {};
   A.y = (const uint16_t *)y;

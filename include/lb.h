@@ -430,8 +430,10 @@ lb_status lb_bank_reserve(lb_bank *B, int64_t rows);
  *             be y itself with the same stride (y is then added to)
  * Pointers need the alignment of their elements only; rows whose pointers,
  * strides and widths are multiples of 16 bytes are read and written in
- * 16-byte pieces (faster).  y must not overlap the other arrays.  M = 0 is
- * a no-op; M <= 2^30. */
+ * 16-byte pieces (faster).  y must not overlap the other arrays: either
+ * their spans, first to last element, are apart, or they are column blocks of
+ * one buffer, with the same row stride in bytes and no column in common.
+ * M = 0 is a no-op; M <= 2^30. */
 lb_status lb_bank_forward(lb_bank *B, int expert, const void *x, int64_t ldx, void *y, int64_t ldy,
                           int y_type, int64_t M, int act, const void *bias, const void *gate_bias,
                           const void *residual, int64_t ldr, void *stream);
@@ -487,7 +489,8 @@ lb_status lb_route(const void *logits, int logits_type, int64_t ld, int64_t toke
  * width; row and weights are tokens x k (k <= 64); residual (or NULL) and
  * out are of out_type; ldy, ldr and ldo are row strides.  Rows outside
  * [0, y_rows) add nothing.  residual may be out itself with the same
- * stride; out must not overlap the other arrays. */
+ * stride; out must not overlap the other arrays (column blocks of one buffer
+ * with the same row stride in bytes do not). */
 lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy, const int32_t *row,
                            const float *weights, int64_t tokens, int k, int64_t width,
                            const void *residual, int64_t ldr, void *out, int64_t ldo, int out_type,
