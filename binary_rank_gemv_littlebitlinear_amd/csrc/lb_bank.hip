@@ -536,7 +536,10 @@ k_bank_first_wide(BankArgs A, int slots, int ncs) {
 // ------------------------------------------------------ second product
 // Activations in fp32 on the hardware's exp2 and reciprocal (a step of error
 // each): v / (1 + exp(-c)) takes six instructions, where expf and a division
-// take some forty, and a wave has 64 of them against 288 matrix products.
+// take some forty, and a wave has 64 of them against 288 matrix products.  The
+// rounding of exp's argument u adds a few times |u| 2^-24 of the result, so far
+// into a tail the relative error grows (SiLU at -10: up to 2e-6); the absolute
+// one does not.
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ float rcp_hw(float v) { return __builtin_amdgcn_rcpf(v); }
 constexpr float kLog2e = 1.4426950408889634f;
@@ -546,13 +549,20 @@ __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == LB_ACT_RELU) {
     return v > 0.f || v != v ? v : 0.f;
   } else if constexpr (ACT == LB_ACT_GELU) {
-    // v/2 erfc(-v / sqrt 2), erfc by Abramowitz and Stegun 7.1.26 (within 1.5e-7)
-    const float z = fabsf(v) * 0.70710678118654752f;
-    const float t = rcp_hw(fmaf(0.3275911f, z, 1.f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f) * t * exp2_hw(-kLog2e * z * z);  // erfc(z)
+    // v/2 erfc(-v / sqrt 2).  For z = |v| / sqrt 2, exp(z^2) erfc(z) = t P(t) with
+    // t = 1 / (1 + 0.21 |v|) and P a least-maximum fit of degree 8 to 0 <= z <= 10
+    // (2^-25.8 of the value), so the tail is as exact as the rest.  (A fit of
+    // small absolute error, 1.5e-7, was off by 5e-4 of gelu(-4), a whole half
+    // step of fp16.)
+    const float t = rcp_hw(fmaf(0.21f, fabsf(v), 1.f));
+    float q = fmaf(-0.14310356f, t, 0.56614528f);
+    q = fmaf(q, t, -0.65833091f);
+    q = fmaf(q, t, 0.69624549f);
+    q = fmaf(q, t, -0.18602241f);
+    q = fmaf(q, t, 0.24893199f);
+    q = fmaf(q, t, 0.1386041f);
+    q = fmaf(q, t, 0.17010479f);
+    q = fmaf(q, t, 0.16742524f) * t * exp2_hw(-0.5f * kLog2e * (v * v));  // erfc(z)
     return 0.5f * v * (v > 0.f ? 2.f - q : q);
   } else if constexpr (ACT == LB_ACT_GELU_TANH) {
     // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)): no cancellation for negative u
