@@ -975,13 +975,14 @@ __device__ __forceinline__ int lift(uint32_t h01, int path) {
 // way, longer ones, a chunk's first operands read before the last products of
 // the one before it, or 8 waves and 512 columns changed nothing or cost up to
 // 8%.)  With two waves on a SIMD (G = 2; four with G = 1) a wave issues an
-// instruction every four or five cycles at best, so besides the products (hi and
-// lo: 104e9 flops for 4096 gated rows of 4096 -> 11008 at s = 133, 47 us of the
-// 122 at the clock it runs at) what counts is instructions: per 16 columns and
-// column tile 4 shifts and 4 sign flips (8 with G = 1), shared by two row tiles,
-// and everything that is not per product is out of the loop.  Without its epilogue the kernel
-// takes 98 us, without products 59.  8192 rows of 11008 -> 4096 in 8 layers
-// (G = 1) take 52 us.
+// instruction every four or five cycles at best, so besides the products what
+// counts is instructions: per 16 columns and column tile 4 shifts and 4 sign
+// flips (8 with G = 1), shared by two row tiles, and everything that is not per
+// product is out of the loop.  4096 gated rows of 4096 -> 11008 at s = 133 take
+// 119 to 132 us, as the clock allows: hi and lo products are 104e9 flops, 47 us
+// of it.  (Without its epilogue the kernel took 98 us of 122, without products
+// 59, when one sum held hi and lo.)  8192 rows of 11008 -> 4096 in 8 layers
+// (G = 1) take 49 to 52 us.
 // With gates the lo sums of the side in hand have registers of their own (240 of
 // 256).  Without, that would leave two waves on a SIMD instead of four (58 us),
 // so one sum takes hi h and lo 2^-11 h, both scaled by the column's `lift`, which
@@ -1186,12 +1187,12 @@ int cu_count(const lb_bank *B) {
 // Up to this many rows a call takes slots of 16: while the first product's
 // 16 x 16 tiles, all slots full, are a few hundred.  16- against 32-row slots,
 // both kernels, 4096 -> 11008 gated at s = 133 (20 words): 32 rows 13.7 against
-// 17.6 us, 64 rows 16.0 against 18.0, 96 rows 20.1 against 18.0; at s = 431 (56
-// words) 32 rows 17.3 against 24.4, 64 rows 27 against 25.5; 4096 -> 4096 at
-// s = 86 (6 words) 256 rows 14.3 against 16.5, 512 rows 23.4 against 18.2.
-// Grouped rows leave slots part empty: 8 layers 8 rows 17.8 against 23, 48 rows
-// 23.9 against 24.1, 64 rows 26.9 against 24.5; 64 layers 1024 -> 1407 (8
-// words) 96 rows 15.6 against 17.8, 180 rows 19.9 against 18.3.
+// 17.6 us, 64 rows 16.5 against 17.8, 96 rows 20.5 against 18.0; at s = 431 (56
+// words) 32 rows 17.6 against 24.5, 64 rows 26.8 against 25.4; 4096 -> 4096 at
+// s = 86 (6 words) 256 rows 14.2 against 15.7, 512 rows 23.2 against 17.3.
+// Grouped rows leave slots part empty: 8 layers 8 rows 18.3 against 22.7, 48 rows
+// 25.0 against 24.2, 64 rows 26.5 against 24.1; 64 layers 1024 -> 1407 (8
+// words) 96 rows 16.2 against 17.0, 180 rows 18.9 against 17.6.
 int64_t few_rows(const lb_bank *B, bool grouped) {
   const Layer &Ly = B->first->ly;
   return (grouped ? 4 : 7) * (int64_t)cu_count(B) / (B->G * Ly.P * Ly.Wk);
@@ -1292,12 +1293,16 @@ hipError_t launch_first_wide(const BankArgs &A, int slots, int ct, hipStream_t s
 
 // The first product of 32- and 64-row slots: column tiles per workgroup (at most
 // five: with RT = 2 160 of 256 registers are sums then), and what a launch
-// costs, in workgroups' times of a column tile.  A CU runs one workgroup at a
-// time, so what counts first is how often all CUs are filled, then the tiles a
-// workgroup has: the fewest rounds, then the fewest tiles.  4096 -> 11008,
-// gated, s = 133: 256 rows 9.4 us with one tile, 17 with five; 768 rows 14.0
-// with three (one round), 17.7 with two, 17.9 with five; 2048 rows 21 with five
-// (one round), 30 with two or three.  A tile alone costs as much as 1.5.
+// costs, in workgroups' times of a column tile.  What counts first is how often
+// all CUs are filled, then the tiles a workgroup has: the fewest rounds, then
+// the fewest tiles.  A round is a workgroup a CU, which is what LDS leaves room
+// for with three tiles or more (with 8 waves); two of one or two tiles fit (74 KB
+// of LDS at RT = 1), but then share the CU's time: 288 workgroups of two tiles
+// take 17.7 us where 256 take 11.4.  4096 -> 11008, gated, s = 133: 256 rows 9.4
+// us with one tile, 17 with five; 768 rows 14.0 with three (one round), 17.7 with
+// two, 17.9 with five; 2048 rows 21 with five (one round), 30 with two or three.
+// A tile alone costs as much as 1.5.  Of grouped calls `slots` is the most that
+// their rows can make.
 struct FirstPlan {
   int ct;
   int64_t cost;
@@ -1358,22 +1363,23 @@ lb_status run(lb_bank *B, BankArgs A, const char *who, hipStream_t st) {
   A.s = (int)Ly.s; A.L = (int)Ly.L; A.P = Ly.P; A.G = B->G; A.R1 = (int)Ly.R1; A.Wk = (int)Ly.Wk;
   A.xvec = A.a % 8 == 0 && A.ldx % 8 == 0 && (uintptr_t)A.x % 16 == 0;
   const int64_t avg = A.offsets ? (A.rows + A.E - 1) / A.E : A.rows;
-  const int64_t big_wg = (int64_t)(A.rows / 64) * ((A.b + 511) / 512);
+  // pieces of 64 rows and 512 columns of y: two workgroups of the second product
+  const int64_t pieces = (int64_t)(A.rows / 64) * ((A.b + 511) / 512);
   // Slots of 64 share an expanded sign operand between two row tiles, but make
   // half the workgroups, and the second product's have half the waves.  64-
-  // against 32-row slots, both kernels: 4096 -> 11008 gated 1024 rows (352
-  // workgroups of 64 x 512) 55.7 against 51.1 us, 2048 rows (704) 93 against 84,
-  // 3000 rows (1012) 137 against 135, 4096 rows (1408) 164 against 177; 4096 ->
-  // 4096 4096 rows (512) 63 against 57, 8192 rows (1024) 106 against 108, 16384
-  // rows 186 against 210.  Below that they win where 32-row slots cost the
-  // first product a round more: 8 layers 11008 -> 4096, 4096 rows (512) 90
-  // against 110 us; not 4096 rows of one layer (100 against 89).
+  // against 32-row slots, both kernels: 4096 -> 11008 gated 1024 rows (352 pieces)
+  // 56 against 51 us, 2048 rows (704) 101 against 96, 3000 rows (1012) 137 against
+  // 149, 4096 rows (1408) 168 against 185; 4096 -> 4096 4096 rows (512) 64 against
+  // 57, 8192 rows (1024) 106 against 113, 16384 rows 193 against 218.  Below four a
+  // CU they win where 32-row slots cost the first product a round more: 8 layers
+  // 11008 -> 4096, 4096 rows (512) 90 against 114 us; not 4096 rows of one layer
+  // (102 against 91).
   const auto plan = [&](int lg) {
     const int64_t n = A.offsets ? (A.rows >> lg) + std::min<int64_t>(A.E, A.rows) : (A.rows + (1 << lg) - 1) >> lg;
     return first_plan(A, n, 1 << (lg - 5), cus).cost;
   };
   A.lg = A.rows <= few_rows(B, A.offsets != nullptr) ? 4
-         : avg >= 64 && (big_wg >= 4 * cus || (big_wg >= 2 * cus && plan(6) <= plan(5))) ? 6 : 5;
+         : avg >= 64 && (pieces >= 4 * cus || (pieces >= 2 * cus && plan(6) <= plan(5))) ? 6 : 5;
   const int64_t slots = A.offsets ? (A.rows >> A.lg) + std::min<int64_t>(A.E, A.rows)
                                   : (A.rows + (1 << A.lg) - 1) >> A.lg;
   const int per = A.lg == 6 ? 2 : 1;  // 32-row parts of T per slot
