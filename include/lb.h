@@ -384,9 +384,11 @@ lb_status lb_stack_destroy(lb_stack *S);
  *
  * for one of its layers (lb_bank_forward) or for rows sorted by layer, each
  * run of rows with its own (lb_bank_grouped: the experts of a mixture).
- * Accumulation is fp32 and the latent vector keeps 22 bits, at every row
- * count; y is rounded once.  (|l_k t_k| must stay below 65504, fp16's
- * largest number, or y is not finite.)
+ * Accumulation is fp32 and the latent vector w = l t keeps 22 bits, at every
+ * row count and size of h; y is rounded once.  That holds for |w_k| from
+ * 2^-14 up; smaller ones are off by at most 2^-36.  Beyond 65504, fp16's
+ * largest number, y is not finite (lb_forward, which keeps w in fp32 below 64
+ * rows, has no such limit there).
  *
  * Layers stay owned by the caller and must outlive the bank; their signs
  * and scales must be set before lb_bank_create, which builds their
