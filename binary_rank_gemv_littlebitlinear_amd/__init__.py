@@ -80,6 +80,17 @@ def load_library(path: str = LIB_PATH):
         "lb_route_ws_bytes": ([i64, i32, i32, P(u64)], i32),
         "lb_route": ([vp, i32, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, u64, vp], i32),
         "lb_route_combine": ([vp, i64, i64, vp, vp, i64, i32, i64, vp, i64, vp, i64, i32, vp], i32),
+        "lb_norm": ([i32, vp, i32, i64, i32, vp, vp, vp, i64, vp, i64, C.c_float, i32, vp, vp, C.c_float, vp, i64, vp,
+                     i64, i64, i64, vp], i32),
+        "lb_cache_create": ([i64, i32, i32, i32, P(vp)], i32),
+        "lb_cache_shape": ([vp, P(i64), P(i32), P(i32), P(i32), P(i32)], i32),
+        "lb_cache_append": ([vp, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, i32, vp, vp, vp, i64, i32, i32,
+                             i64, vp], i32),
+        "lb_cache_read": ([vp, vp, i64, vp, i64, vp, vp, vp, i64, i32, i32, i64, vp], i32),
+        "lb_cache_reserve": ([vp, i64, i32, i64, i64], i32),
+        "lb_cache_attend": ([vp, vp, i64, i32, vp, i64, vp, vp, vp, i64, i32, i32, i64, i64, C.c_float, i32, i32, vp],
+                            i32),
+        "lb_cache_destroy": ([vp], i32),
         "lb_status_str": ([i32], C.c_char_p),
         "lb_last_error": ([], C.c_char_p),
         "lb_version": ([], i32),
@@ -101,7 +112,9 @@ EXPORTED = ("lb_create", "lb_pack_signs", "lb_set_scales", "lb_forward", "lb_for
             "lb_stack_test_wait_failure", "lb_stack_test_delay",
             "lb_stack_timeline", "lb_stack_destroy",
             "lb_bank_create", "lb_bank_shape", "lb_bank_reserve", "lb_bank_forward", "lb_bank_grouped", "lb_bank_destroy",
-            "lb_route_ws_bytes", "lb_route", "lb_route_combine", "lb_status_str", "lb_last_error", "lb_version")
+            "lb_route_ws_bytes", "lb_route", "lb_route_combine",
+            "lb_norm", "lb_cache_create", "lb_cache_shape", "lb_cache_append", "lb_cache_read", "lb_cache_reserve",
+            "lb_cache_attend", "lb_cache_destroy", "lb_status_str", "lb_last_error", "lb_version")
 
 
 def _status_name(st: int) -> str:
@@ -485,6 +498,158 @@ def lb_route_combine(y, row, weights, out, residual=None, stream=None):
                LB_F32 if dtype is _f32 else LB_F16, _stream_of(stream, dev))
 
 
+NORMS = {"rms": 0, "layer": 1}
+
+
+def lb_norm(r, x=None, y=None, out=None, kind="rms", weight=None, bias=None, post=False, post_weight=None,
+            post_bias=None, gate=None, scale=1.0, eps=1e-5, stream=None):
+    """out = scale * r + gate * (norm of) y, x = its norm (see include/lb.h).
+
+    r and y may be None, not both; gate has one row or a row for each of r's."""
+    _types()
+    lead = y if r is None else r
+    if lead is None:
+        raise ValueError("lb_norm needs r or y")
+    dev = lead.get_device()
+    if lead.dim() != 2 or dev < 0:
+        raise ValueError("r and y must be 2-d device tensors")
+    try:
+        k = NORMS[kind]
+    except KeyError:
+        raise ValueError(f"kind must be one of {sorted(NORMS)}, not {kind!r}") from None
+    rows, width = lead.shape
+    like = out if r is None else r
+    rtype = _f16 if like is None else like.dtype
+    if rtype is not _f16 and rtype is not _f32:
+        raise ValueError(f"the residual must be {_f16} or {_f32}, not {rtype}")
+
+    def of(name, t, dtypes):
+        if t is None:
+            return None, 0
+        n, ld = _rows(name, t, width, dtypes, dev)
+        if n != rows:
+            raise ValueError(f"{name} must have {rows} rows, not {n}")
+        return t.data_ptr(), ld
+
+    def vec(name, t):
+        return None if t is None else _flat(name, t, (width,), _f16, dev)
+
+    py, ldy = of("y", y, _f16_f32)
+    pr, ldr = of("r", r, _f16_f32)
+    po, ldo = of("out", out, (rtype,))
+    px, ldx = of("x", x, _only_f16)
+    pg, ldg = None, 0
+    if gate is not None:
+        n, ldg = _rows("gate", gate, width, _only_f16, dev)
+        if n != rows and n != 1:
+            raise ValueError(f"gate must have 1 or {rows} rows, not {n}")
+        pg = gate.data_ptr()
+        if n == 1:
+            ldg = 0
+    _on_device(dev, load_library().lb_norm, k, py, LB_F32 if y is not None and y.dtype is _f32 else LB_F16, ldy,
+               1 if post else 0, vec("post_weight", post_weight), vec("post_bias", post_bias), pg, ldg, pr, ldr, scale,
+               LB_F32 if rtype is _f32 else LB_F16, vec("weight", weight), vec("bias", bias), eps, po, ldo, px, ldx, rows,
+               width, _stream_of(stream, dev))
+
+
+def lb_cache_create(pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    out = C.c_void_p()
+    _check(load_library().lb_cache_create(int(pages), int(page_tokens), int(kv_heads), int(head_dim), C.byref(out)))
+    return out.value
+
+
+def lb_cache_shape(cache: int):
+    """(pages, page_tokens, kv_heads, head_dim, device) of a cache."""
+    n, p, k, d, dev = C.c_int64(), C.c_int(), C.c_int(), C.c_int(), C.c_int()
+    _check(load_library().lb_cache_shape(cache, C.byref(n), C.byref(p), C.byref(k), C.byref(d), C.byref(dev)))
+    return n.value, p.value, k.value, d.value, dev.value
+
+
+def lb_cache_reserve(cache: int, rows: int, heads: int, sequences: int, max_length: int):
+    _check(load_library().lb_cache_reserve(cache, int(rows), int(heads), int(sequences), int(max_length)))
+
+
+def _sequences(rows, lengths, table, start, dev):
+    """start, lengths, table, its row stride, columns, sequences, rows: the C order."""
+    _types()
+    if table.dim() != 2 or table.dtype is not _i32 or table.get_device() != dev:
+        raise ValueError(f"table must be a 2-d {_i32} tensor on GPU {dev}, not {_say(table)}")
+    (n, columns), (ld, unit) = table.shape, table.stride()
+    if unit != 1 and columns > 1:
+        raise ValueError(f"table must have unit-stride columns, not {_say(table)}")
+    if start is None and rows != n:
+        raise ValueError(f"without start there is a row for each sequence: {n}, not {rows}")
+    return (None if start is None else _flat("start", start, (n + 1,), _i32, dev), _flat("lengths", lengths, (n,), _i32, dev),
+            table.data_ptr(), ld if n > 1 else columns, columns, n, rows)
+
+
+def _heads(name, t, dim, dev):
+    """(pointer, row stride, rows, heads) of a 2-d tensor with `dim` columns for each head."""
+    if t.dim() != 2 or t.shape[1] % dim or not t.shape[1]:
+        raise ValueError(f"{name} must be 2-d with {dim} columns for each head, not {_say(t)}")
+    rows, ld = _rows(name, t, t.shape[1], _only_f16, dev)
+    return t.data_ptr(), ld, rows, t.shape[1] // dim
+
+
+def lb_cache_append(cache, k, v, lengths, table, start=None, q=None, q_out=None, rope=None, interleaved=False,
+                    stream=None):
+    """``Cache`` owner and tensors: the rows of k and v into the pages of their sequences (see include/lb.h)."""
+    _types()
+    dev, width = cache.device, cache.kv_heads * cache.head_dim
+    rows, ldk = _rows("k", k, width, _only_f16, dev)
+    vr, ldv = _rows("v", v, width, _only_f16, dev)
+    if vr != rows:
+        raise ValueError("k and v must have the same number of rows")
+    pq = po = pr = None
+    ldq = ldo = heads = positions = rot = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        pq, ldq, qr, heads = _heads("q", q, cache.head_dim, dev)
+        po, ldo, wr, oh = _heads("q_out", q_out, cache.head_dim, dev)
+        if qr != rows or wr != rows or oh != heads:
+            raise ValueError("q and q_out must have k's rows and the same heads")
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope must be 2-d: positions x rot")
+        positions, rot = rope.shape
+        pr = _flat("rope", rope, (positions, rot), _f32, dev)
+    _check(_lib.lb_cache_append(cache.handle, k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, po, ldo, heads, pr, positions,
+                                rot, 1 if interleaved else 0, *_sequences(rows, lengths, table, start, dev),
+                                _stream_of(stream, dev)))
+
+
+def lb_cache_read(cache, k, v, lengths, table, start=None, stream=None):
+    """``Cache`` owner and tensors: k and v receive the values of the sequences' last tokens (see include/lb.h)."""
+    _types()
+    dev, width = cache.device, cache.kv_heads * cache.head_dim
+    rows, ldk = _rows("k", k, width, _only_f16, dev)
+    vr, ldv = _rows("v", v, width, _only_f16, dev)
+    if vr != rows:
+        raise ValueError("k and v must have the same number of rows")
+    _check(_lib.lb_cache_read(cache.handle, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                              *_sequences(rows, lengths, table, start, dev), _stream_of(stream, dev)))
+
+
+def lb_cache_attend(cache, q, out, lengths, table, start=None, max_length=None, scale=None, causal=True, window=0,
+                    stream=None):
+    """``Cache`` owner and tensors: out = attention of q over the cache (see include/lb.h); scale defaults to
+    1 / sqrt(head_dim)."""
+    _types()
+    dev = cache.device
+    pq, ldq, rows, heads = _heads("q", q, cache.head_dim, dev)
+    po, ldo, wr, oh = _heads("out", out, cache.head_dim, dev)
+    if wr != rows or oh != heads:
+        raise ValueError("out must have q's rows and heads")
+    _check(_lib.lb_cache_attend(cache.handle, pq, ldq, heads, po, ldo, *_sequences(rows, lengths, table, start, dev),
+                                int(max_length or 0), cache.head_dim ** -0.5 if scale is None else scale,
+                                1 if causal else 0, window, _stream_of(stream, dev)))
+
+
+def lb_cache_destroy(cache: int):
+    _check(load_library().lb_cache_destroy(cache))
+
+
 # --------------------------------------------------------------- owners
 class Layer:
     """Owner of one lb_layer handle."""
@@ -624,6 +789,42 @@ class Route:
 
     def combine(self, y, out, residual=None, stream=None):
         lb_route_combine(y, self.row, self.weights, out, residual, stream)
+
+
+class Cache:
+    """Owner of one lb_cache handle: keys and values in 8 bits, in pages, on the current GPU.
+
+    Rows are tokens: k and v (rows, kv_heads * head_dim), q and out (rows, heads * head_dim), fp16.  ``table``
+    (sequences, columns), ``lengths`` (sequences) and ``start`` (sequences + 1, or None for a row each) are int32.
+    """
+
+    def __init__(self, pages: int, page_tokens: int, kv_heads: int, head_dim: int):
+        self.handle = None
+        self.handle = lb_cache_create(pages, page_tokens, kv_heads, head_dim)
+        self.pages, self.page_tokens, self.kv_heads, self.head_dim, self.device = lb_cache_shape(self.handle)
+
+    def reserve(self, rows: int, heads: int, sequences: int, max_length: int):
+        lb_cache_reserve(self.handle, rows, heads, sequences, max_length)
+
+    def append(self, k, v, lengths, table, start=None, q=None, q_out=None, rope=None, interleaved=False, stream=None):
+        lb_cache_append(self, k, v, lengths, table, start, q, q_out, rope, interleaved, stream)
+
+    def read(self, k, v, lengths, table, start=None, stream=None):
+        lb_cache_read(self, k, v, lengths, table, start, stream)
+
+    def attend(self, q, out, lengths, table, start=None, max_length=None, scale=None, causal=True, window=0, stream=None):
+        lb_cache_attend(self, q, out, lengths, table, start, max_length, scale, causal, window, stream)
+
+    def close(self):
+        if self.handle:
+            lb_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def lb_status_str(status: int) -> str:

@@ -1,0 +1,773 @@
+// Attention over the paged 8-bit cache (lb_cache.h): lb_cache_attend.
+//
+// For a row (token i of a sequence, query head h, key head h / group) at
+// position p = length - rows + i, over the keys t it sees (t < length; t <= p
+// when causal; t > p - window with a window):
+//
+//   z_t = scale * s_k(t) * (q . K_t)        K, V: the bytes - 128, exact in fp16
+//   out = sum_t e^(z_t - m) s_v(t) V_t / sum_t e^(z_t - m)
+//
+// in one pass over the keys with a running reference m and sum l: when the
+// largest z so far exceeds m by more than kSlack (in powers of two), m is set to
+// it and what has been summed is scaled down; in between the weights may
+// exceed 1, which costs nothing and saves most of the scaling.
+//
+// Precision.  q . K is exact products in fp32 sums.  The weight times s_v has
+// to be an fp16 operand: s_v / r, r the largest finite s_v so far (a change of
+// r scales the sums too), keeps it within 2^(kUp + kSlack), and 2^kUp lifts it
+// over fp16's small numbers.  The kernel for few rows, bound by reading the
+// keys, keeps it as two fp16 numbers (22 bits), so its result is that of fp32
+// arithmetic.  l is summed in fp32 from the weights before any rounding.
+// Keys that a row does not see get weight 0 by selection, so that what lies
+// there (numbers of earlier owners, scales that are NaN) does not matter.
+//
+// Both kernels work on S^T = K Q^T and O^T = V^T P^T: a lane has one row of q
+// (column of S^T), its maximum and sum are the lane's own up to one or two
+// exchanges, and the weights come out of the first product in the order in
+// which the second wants them.
+//
+// A row's keys may be split over workgroups (pieces of `chunk` keys): each
+// leaves its m, l and sums in the workspace, and k_attend_join adds them up.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "lb_cache.h"
+
+namespace {
+
+using namespace lbi;
+
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef float float16_t __attribute__((ext_vector_type(16)));
+typedef float4_t __attribute__((aligned(8))) float4a_t;
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr float kUp = 12.f, kSlack = 3.f;
+
+struct AttendArgs {
+  Sequences S;
+  const uint16_t *q;
+  uint16_t *out;
+  int64_t ldq, ldo;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  float *part;  // partial sums of the pieces: per item, piece and row Dp sums, then m and l
+  float qscale;  // scale * log2 e
+  int KV, D, lg;
+  View view;
+  int few;      // rows x heads of a group up to which k_attend_few has a sequence
+  int tiles, frows;  // 16-row tiles a sequence may have there, rows of a tile (16 or fewer)
+  int chunk, pieces;  // keys of a piece, pieces in the grid
+  int row_tiles;      // k_attend_many: row tiles in the grid
+};
+
+// What an item (a sequence's row tile of one key head) sees.
+struct Item {
+  Sequence q;
+  int h, r0, n;    // key head, first row (token * group + head), rows
+  int lo, hi;      // keys, lo a multiple of 16
+};
+
+// Four bytes as fp16 numbers: byte - 128, exact (0x6400 + byte is 1024 + byte).
+__device__ __forceinline__ void to_half4(uint32_t w, half2_t &a, half2_t &b) {
+  const half2_t bias = {(_Float16)-1152.f, (_Float16)-1152.f};
+  a = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + bias;
+  b = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + bias;
+}
+__device__ __forceinline__ half8_t to_half8(uint32_t w0, uint32_t w1) {
+  half2_t a, b, c, d;
+  to_half4(w0, a, b);
+  to_half4(w1, c, d);
+  return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ float lane_xor(float v, int d) { return __shfl_xor(v, d); }
+
+// Item `slot` of k_attend_few: (sequence, key head, 16-row tile), or false.
+__device__ __forceinline__ bool few_item(const AttendArgs &A, unsigned slot, Item &it) {
+  const unsigned s = slot / (unsigned)A.tiles, tile = slot - s * A.tiles;
+  const unsigned b = s / (unsigned)A.KV;
+  it.h = (int)(s - b * A.KV);
+  it.q = sequence(A.S, (int)b);
+  const int64_t rows = (int64_t)it.q.rows * A.view.group;
+  if (rows > A.few) return false;
+  it.r0 = (int)tile * 16;
+  if (it.r0 >= rows) return false;
+  it.n = min(16, (int)rows - it.r0);
+  keys_of_rows(A.view, it.q, it.r0, it.n, &it.lo, &it.hi);
+  return true;
+}
+
+// Item of k_attend_many: row tile `slot` of all sequences' tiles of TR rows, head h.
+template <int TR>
+__device__ __forceinline__ bool many_item(const AttendArgs &A, int slot, int h, Item &it, int *b_out) {
+  constexpr int lg = TR == 256 ? 8 : TR == 128 ? 7 : 6;
+  static_assert(TR == 1 << lg, "a power of two");
+  int64_t first;
+  const int b = find_sequence(A.S, slot, A.view.group, lg, 1, &first);
+  if (b < 0) return false;
+  it.q = sequence(A.S, b);
+  const int64_t rows = (int64_t)it.q.rows * A.view.group, r0 = (slot - first) * TR;
+  if (rows <= A.few || r0 >= rows) return false;
+  it.h = h;
+  it.r0 = (int)r0;
+  it.n = (int)min((int64_t)TR, rows - r0);
+  keys_of_rows(A.view, it.q, it.r0, it.n, &it.lo, &it.hi);
+  *b_out = b;
+  return true;
+}
+
+// The address of row r of a head's group, in q or out.
+__device__ __forceinline__ int64_t row_at(const AttendArgs &A, const Item &it, int r, int64_t ld) {
+  const int tok = r / A.view.group, j = r - tok * A.view.group;
+  return (int64_t)(it.q.row0 + tok) * ld + (int64_t)(it.h * A.view.group + j) * A.D;
+}
+
+__device__ __forceinline__ half8_t load_q(const AttendArgs &A, int64_t at, int d) {
+  u32x4_t w = {0, 0, 0, 0};
+  if (d < A.D) w = *LB_LOOSE128(A.q + at + d);
+  return __builtin_bit_cast(half8_t, w);
+}
+
+// ------------------------------------------------------------- few rows
+// 16 rows a workgroup, four waves that share out the keys of a piece and read
+// them from memory straight into operands; the waves' sums are joined in LDS.
+template <int NC>
+__global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
+  constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = Dp / 16;
+  extern __shared__ float sh[];  // [4][rows][Dp + 4], then m and l [4][16] each
+  const unsigned slot = blockIdx.x / (unsigned)A.pieces;
+  const int piece = (int)(blockIdx.x - slot * A.pieces);
+  const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 15, G = lane >> 4;
+  Item it;
+  if (!few_item(A, slot, it)) return;
+  const int pieces = pieces_of(it.lo, it.hi, A.chunk);
+  if (piece >= pieces) return;
+  const int b = (int)(slot / (unsigned)(A.tiles * A.KV));
+  const int c0 = it.lo + piece * A.chunk, c1 = min(it.hi, c0 + A.chunk);
+  // the wave's units of 16 keys, an even number before the last
+  const int units = (c1 - c0 + 15) >> 4, per = ((units + 7) >> 3) * 2;
+  const int u0 = (c0 >> 4) + min(units, w * per), u1 = (c0 >> 4) + min(units, w * per + per);
+  const int myrow = it.r0 + min(n, it.n - 1);
+  int first, last;
+  keys_of_row(A.view, it.q, myrow, &first, &last);
+  last = min(last, c1);
+
+  half8_t q[NC];
+  {
+    const int64_t at = row_at(A, it, myrow, A.ldq);
+#pragma unroll
+    for (int s = 0; s < NC; ++s) q[s] = load_q(A, at, 32 * s + 8 * G);
+  }
+  float4_t O[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) O[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f, r = 1e-30f;
+
+  const int upp = 1 << (A.lg - 4);
+  struct Frag {
+    u32x4_t pair[kPairs > 0 ? kPairs : 1];
+    u32x2_t odd;
+  };
+  const auto load = [&](const uint8_t *base, int unit, Frag &f) {
+    const uint8_t *p = base + (int64_t)unit * kUnit;
+#pragma unroll
+    for (int c = 0; c < kPairs; ++c)
+      f.pair[c] = *(const u32x4_t __attribute__((address_space(1))) *)(uintptr_t)(p + c * 1024 + lane * 16);
+    if constexpr (kOdd)
+      f.odd = *(const u32x2_t __attribute__((address_space(1))) *)(uintptr_t)(p + kPairs * 1024 + lane * 8);
+  };
+
+  for (int ub = u0; ub < u1; ub += 64) {
+    // up to 64 units: lane i knows where unit ub + i lies, and its scales
+    const int u = ub + lane;
+    const int page = u < u1 ? page_of(A.S, b, u >> (A.lg - 4)) : -1;
+    const bool there = page >= 0;
+    const int blk = (there ? page : 0) * A.KV + it.h;
+    const int mine = blk * upp + (u & (upp - 1));
+    const float ks = there ? A.ks[blk] * A.qscale : 0.f, vs = there ? A.vs[blk] : 0.f;
+    const unsigned long long ok = __ballot(there);
+    float big = vs < INFINITY ? vs : 0.f;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) big = fmaxf(big, lane_xor(big, d));
+    if (big > r) {
+      const float f = r / big;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) O[i] *= f;
+      r = big;
+    }
+    const float ratio = vs / r;
+    const int steps = (min(u1 - ub, 64) + 1) >> 1;
+    Frag K[2], V[2], Kn[2], Vn[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = __builtin_amdgcn_readlane(mine, i);
+      load(A.kc, at, K[i]);
+      load(A.vc, at, V[i]);
+    }
+    for (int st = 0; st < steps; ++st) {
+      if (st + 1 < steps) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = __builtin_amdgcn_readlane(mine, 2 * st + 2 + i);
+          load(A.kc, at, Kn[i]);
+          load(A.vc, at, Vn[i]);
+        }
+      }
+      float z[8];
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8(K[i].pair[c][0], K[i].pair[c][1]), q[2 * c], acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8(K[i].pair[c][2], K[i].pair[c][3]), q[2 * c + 1], acc, 0, 0, 0);
+        }
+        if constexpr (kOdd)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8(K[i].odd[0], K[i].odd[1]), q[NC - 1], acc, 0, 0, 0);
+        const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * st + i));
+        const bool have = (ok >> (2 * st + i)) & 1;
+        const int t0 = (ub + 2 * st + i) * 16 + 4 * G;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = have && t0 + j >= first && t0 + j < last;
+          z[4 * i + j] = in ? acc[j] * s : -INFINITY;
+          top = fmaxf(top, z[4 * i + j]);
+        }
+      }
+      top = fmaxf(top, lane_xor(top, 16));
+      top = fmaxf(top, lane_xor(top, 32));
+      const bool up = top > m + kSlack;  // also the first finite one: m is -inf
+      if (__any(up)) {
+        const float f = up ? exp2f(m - top) : 1.f;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) O[i] *= f;
+        if (up) m = top;
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) - kUp;
+      half8_t ph, pl;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ratio), 2 * st + i));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = z[4 * i + j] != -INFINITY;
+          const float p = __builtin_amdgcn_exp2f(z[4 * i + j] - ref);
+          l += p;
+          const float pv = in ? p * f : 0.f;
+          const _Float16 hi = (_Float16)pv;
+          ph[4 * i + j] = hi;
+          pl[4 * i + j] = (_Float16)(pv - (float)hi);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kPairs; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const half8_t a = to_half8(V[0].pair[c][i], V[1].pair[c][i]);
+          O[4 * c + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph, O[4 * c + i], 0, 0, 0);
+          O[4 * c + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl, O[4 * c + i], 0, 0, 0);
+        }
+      }
+      if constexpr (kOdd) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const half8_t a = to_half8(V[0].odd[i], V[1].odd[i]);
+          O[4 * kPairs + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph, O[4 * kPairs + i], 0, 0, 0);
+          O[4 * kPairs + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl, O[4 * kPairs + i], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        K[i] = Kn[i];
+        V[i] = Vn[i];
+      }
+    }
+  }
+  l += lane_xor(l, 16);
+  l += lane_xor(l, 32);
+
+  // the four waves' sums, in units of 1
+  constexpr int kPitch = Dp + 4;
+  const int rows = A.frows;
+  float *sm = sh + 4 * rows * kPitch, *sl = sm + 64;
+  if (n < it.n) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *(float4_t *)(sh + (w * rows + n) * kPitch + 16 * i + 4 * G) = O[i] * r;
+  }
+  if (G == 0) {
+    sm[w * 16 + n] = m;
+    sl[w * 16 + n] = l;
+  }
+  __syncthreads();
+  float *part = A.part + ((int64_t)slot * A.pieces + piece) * rows * (Dp + 2);
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += 256) {
+    const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
+    float M = sm[row];
+#pragma unroll
+    for (int v = 1; v < 4; ++v) M = fmaxf(M, sm[v * 16 + row]);
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
+    float L = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float mv = sm[v * 16 + row], f = mv == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mv - M);
+      // a wave that saw nothing adds nothing (m may also be -inf beside a NaN sum)
+      o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * (mv == -INFINITY ? 1.f : f);
+      L += sl[v * 16 + row] * (mv == -INFINITY ? 1.f : f);
+    }
+    if (pieces == 1) {
+      if (d >= A.D) continue;
+      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+      u32x2_t o2;
+      o2[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
+      o2[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
+      uint16_t *to = A.out + row_at(A, it, it.r0 + row, A.ldo) + d;
+      typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
+      *(loose64 *)(uintptr_t)to = o2;
+    } else {
+      *(float4a_t *)(part + row * Dp + d) = o;
+      if (d == 0) {
+        part[rows * Dp + row] = M;
+        part[rows * Dp + rows + row] = L;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ many rows
+// 32 rows a wave, NW waves a workgroup; tiles of 64 keys and values go through
+// LDS as fp16 operands (converted once for all waves), the next tile's bytes on
+// their way meanwhile.
+template <int NC, int NW>
+__global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
+  constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = NC, TR = NW * 32;
+  constexpr int kHalf = Dp * 128;  // bytes of a tile's keys, or values
+  extern __shared__ char smem[];   // [2][keys, values], then the scales [2][2][4]
+  float *scales = (float *)(smem + 4 * kHalf);
+  const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 31, G = lane >> 5;
+  // heads vary fastest, so that one head's tiles mostly meet on one XCD; the
+  // last row tiles, which see the most keys, go first
+  const unsigned hs = blockIdx.x / (unsigned)A.KV;
+  const int h = (int)(blockIdx.x - hs * A.KV);
+  const unsigned ts = hs / (unsigned)A.pieces;
+  const int piece = (int)(hs - ts * A.pieces), slot = A.row_tiles - 1 - (int)ts;
+  Item it;
+  int b = 0;
+  if (!many_item<TR>(A, slot, h, it, &b)) return;
+  const int pieces = pieces_of(it.lo, it.hi, A.chunk);
+  if (piece >= pieces) return;
+  const int c0 = it.lo + piece * A.chunk, c1 = min(it.hi, c0 + A.chunk);
+  const int tiles = (c1 - c0 + 63) >> 6;
+  const int myrow = it.r0 + min(w * 32 + n, it.n - 1);
+  int first, last;
+  keys_of_row(A.view, it.q, myrow, &first, &last);
+  last = min(last, c1);
+  // over the wave: the keys that some row sees, and those that all see
+  int some_last, all_first, all_last, some_first;
+  {
+    const int ra = it.r0 + min(w * 32, it.n - 1), rb = it.r0 + min(w * 32 + 31, it.n - 1);
+    keys_of_row(A.view, it.q, ra, &some_first, &all_last);
+    keys_of_row(A.view, it.q, rb, &all_first, &some_last);
+    all_last = min(all_last, c1);
+    some_last = min(some_last, c1);
+  }
+  half8_t q[Dp / 16];
+  {
+    const int64_t at = row_at(A, it, myrow, A.ldq);
+#pragma unroll
+    for (int s = 0; s < Dp / 16; ++s) q[s] = load_q(A, at, 16 * s + 8 * G);
+  }
+  float16_t O[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) O[i][j] = 0.f;
+  float m = -INFINITY, l = 0.f, r = 1e-30f;
+
+  const int upp = 1 << (A.lg - 4);
+  // staging: NW = 8: waves 0..3 have the tile's units of keys, 4..7 of values;
+  // NW = 4: wave w has unit w of both
+  constexpr int kKinds = NW == 8 ? 1 : 2;
+  const int su = w & 3;
+  struct Frag {
+    u32x4_t pair[kPairs > 0 ? kPairs : 1];
+    u32x2_t odd;
+    float scale;
+  };
+  Frag f[kKinds];
+  const auto fetch = [&](int tile) {
+    const int tok = c0 + tile * 64 + su * 16;
+    const int page = tok < c1 ? page_of(A.S, b, tok >> A.lg) : -1;
+    const bool there = page >= 0;
+    const int blk = (there ? page : 0) * A.KV + it.h;
+    const int unit = blk * upp + ((tok >> 4) & (upp - 1));
+#pragma unroll
+    for (int i = 0; i < kKinds; ++i) {
+      const bool values = NW == 8 ? w >= 4 : i == 1;
+      const uint8_t *p = (values ? A.vc : A.kc) + (int64_t)unit * kUnit;
+#pragma unroll
+      for (int c = 0; c < kPairs; ++c)
+        f[i].pair[c] = *(const u32x4_t __attribute__((address_space(1))) *)(uintptr_t)(p + c * 1024 + lane * 16);
+      if constexpr (kOdd)
+        f[i].odd = *(const u32x2_t __attribute__((address_space(1))) *)(uintptr_t)(p + kPairs * 1024 + lane * 8);
+      // a missing unit has scale -1: its keys are not seen
+      f[i].scale = there ? (values ? A.vs[blk] : A.ks[blk] * A.qscale) : -1.f;
+    }
+  };
+  const auto put = [&](int buf) {
+    const int x = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < kKinds; ++i) {
+      const bool values = NW == 8 ? w >= 4 : i == 1;
+      char *to = smem + (2 * buf + (values ? 1 : 0)) * kHalf;
+      if (lane == 0) scales[(2 * buf + (values ? 1 : 0)) * 4 + su] = f[i].scale;
+      if (!values) {
+        // [dim / 8][key 64][8]
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          *(half8_t *)(to + ((8 * c + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].pair[c][0], f[i].pair[c][1]);
+          *(half8_t *)(to + ((8 * c + 4 + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].pair[c][2], f[i].pair[c][3]);
+        }
+        if constexpr (kOdd)
+          *(half8_t *)(to + ((8 * kPairs + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].odd[0], f[i].odd[1]);
+      } else {
+        // [unit 4][half 2][dim][keys 4 half + 0..3, 8 + 4 half + 0..3]
+        const auto half4 = [&](uint32_t word, int d) {
+          half2_t a, bb;
+          to_half4(word, a, bb);
+          u32x2_t o = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, bb)};
+          *(u32x2_t *)(to + ((su * 2 + (g & 1)) * Dp + d) * 16 + (g >> 1) * 8) = o;
+        };
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) half4(f[i].pair[c][j], 64 * c + 16 * j + x);
+        if constexpr (kOdd) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) half4(f[i].odd[j], 64 * kPairs + 16 * j + x);
+        }
+      }
+    }
+  };
+
+  if (tiles > 0) {
+    fetch(0);
+    put(0);
+  }
+  __syncthreads();
+  for (int tile = 0; tile < tiles; ++tile) {
+    const int buf = tile & 1, t0 = c0 + tile * 64;
+    if (tile + 1 < tiles) fetch(tile + 1);
+    if (t0 < some_last && t0 + 64 > some_first) {
+      const char *kb = smem + 2 * buf * kHalf, *vb = kb + kHalf;
+      const float *ksc = scales + 2 * buf * 4, *vsc = ksc + 4;
+      float big = 0.f;
+      bool whole = t0 >= all_first && t0 + 64 <= all_last;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        big = fmaxf(big, vsc[i] < INFINITY ? vsc[i] : 0.f);
+        whole = whole && !(ksc[i] == -1.f);
+      }
+      if (big > r) {
+        const float g = r / big;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) O[i] *= g;
+        r = big;
+      }
+      float16_t z[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[k][j] = 0.f;
+      }
+#pragma unroll
+      for (int s = 0; s < Dp / 16; ++s) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          z[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(kb + ((2 * s + G) * 64 + k * 32 + n) * 16), q[s],
+                                                       z[k], 0, 0, 0);
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float s = ksc[u];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float v = z[u >> 1][8 * (u & 1) + j] * s;
+          if (!whole) {
+            const int t = t0 + 16 * u + 8 * (j >> 2) + 4 * G + (j & 3);
+            if (s == -1.f || t < first || t >= last) v = -INFINITY;
+          }
+          z[u >> 1][8 * (u & 1) + j] = v;
+          top = fmaxf(top, v);
+        }
+      }
+      top = fmaxf(top, lane_xor(top, 32));
+      const bool up = top > m + kSlack;
+      if (__any(up)) {
+        const float g = up ? exp2f(m - top) : 1.f;
+        l *= g;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) O[i] *= g;
+        if (up) m = top;
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) - kUp;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float g = vsc[u] == -1.f ? 0.f : vsc[u] / r;
+        half8_t p8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float v = z[u >> 1][8 * (u & 1) + j];
+          const float p = __builtin_amdgcn_exp2f(v - ref);
+          l += p;
+          p8[j] = (_Float16)(v == -INFINITY ? 0.f : p * g);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          O[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(vb + ((u * 2 + G) * Dp + i * 32 + n) * 16), p8,
+                                                       O[i], 0, 0, 0);
+      }
+    }
+    if (tile + 1 < tiles) put(buf ^ 1);
+    __syncthreads();
+  }
+  l += lane_xor(l, 32);
+  if (w * 32 + n >= it.n) return;
+  if (pieces == 1) {
+    const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * r;
+    uint16_t *to = A.out + row_at(A, it, myrow, A.ldo);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = i * 32 + 8 * j + 4 * G;
+        if (d >= A.D) continue;
+        u32x2_t o;
+        o[0] = f2h(O[i][4 * j] * inv) | (f2h(O[i][4 * j + 1] * inv) << 16);
+        o[1] = f2h(O[i][4 * j + 2] * inv) | (f2h(O[i][4 * j + 3] * inv) << 16);
+        typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
+        *(loose64 *)(uintptr_t)(to + d) = o;
+      }
+    return;
+  }
+  float *part = A.part + (((int64_t)slot * A.KV + h) * A.pieces + piece) * TR * (Dp + 2);
+  const int row = w * 32 + n;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4_t o = {O[i][4 * j], O[i][4 * j + 1], O[i][4 * j + 2], O[i][4 * j + 3]};
+      *(float4a_t *)(part + row * Dp + i * 32 + 8 * j + 4 * G) = o * r;
+    }
+  if (G == 0) {
+    part[TR * Dp + row] = m;
+    part[TR * Dp + TR + row] = l;
+  }
+}
+
+// --------------------------------------------------------------- joining
+// The pieces of a row: a wave has one row, four dims a lane.  TR = 16: of
+// k_attend_few.
+template <int TR>
+__global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
+  const int rows = TR == 16 ? A.frows : TR;  // of an item's partial sums
+  const int lane = threadIdx.x & 63;
+  const unsigned wv = blockIdx.x * 4 + wave_id();
+  const unsigned item = wv / (unsigned)rows;
+  const int row = (int)(wv - item * rows);
+  Item it;
+  if constexpr (TR == 16) {
+    if (item >= (unsigned)(A.S.n * A.KV * A.tiles) || !few_item(A, item, it)) return;
+  } else {
+    const unsigned slot = item / (unsigned)A.KV;
+    int b;
+    if (slot >= (unsigned)A.row_tiles || !many_item<TR>(A, (int)slot, (int)(item - slot * A.KV), it, &b)) return;
+  }
+  const int pieces = pieces_of(it.lo, it.hi, A.chunk);
+  if (pieces == 1 || row >= it.n) return;
+  const int64_t size = (int64_t)rows * (Dp + 2);
+  const float *part = A.part + (int64_t)item * A.pieces * size;
+  float M = -INFINITY;
+  for (int p = lane; p < pieces; p += 64) M = fmaxf(M, part[p * size + rows * Dp + row]);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
+  float4_t o = {0.f, 0.f, 0.f, 0.f};
+  float L = 0.f;
+  const int d = 4 * lane;
+  for (int p = 0; p < pieces; ++p) {
+    const float mv = part[p * size + rows * Dp + row];
+    const float f = mv == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mv - M);
+    L += part[p * size + rows * Dp + rows + row] * f;
+    if (d < Dp) o += *(const float4a_t *)(part + p * size + row * Dp + d) * f;
+  }
+  if (d >= A.D) return;
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  u32x2_t h;
+  h[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
+  h[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
+  typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
+  *(loose64 *)(uintptr_t)(A.out + row_at(A, it, it.r0 + row, A.ldo) + d) = h;
+}
+
+// ------------------------------------------------------------------ host
+lb_status grow(lb_cache *C, size_t need, const char *who, bool in_call, hipStream_t st) {
+  if (need <= C->ws_bytes) return LB_OK;
+  const std::string pre = std::string(who) + ": ";
+  if (in_call) {
+    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(st, &cs);
+    if (e != hipSuccess) return set_error(LB_EHIP, pre + hipGetErrorString(e));
+    if (cs != hipStreamCaptureStatusNone)
+      return set_error(LB_ENOTREADY, pre + "more workspace than reserved while the stream is being captured; call "
+                                           "lb_cache_reserve first");
+  }
+  void *t = nullptr;
+  const hipError_t e = hipMalloc(&t, need);
+  if (e != hipSuccess) return set_error(LB_ENOMEM, pre + "hipMalloc: " + hipGetErrorString(e));
+  if (C->ws) {
+    try {
+      C->retired.push_back(C->ws);
+    } catch (...) {
+      (void)hipFree(t);
+      return set_error(LB_ENOMEM, pre + "host allocation");
+    }
+  }
+  C->ws = t;
+  C->ws_bytes = need;
+  return LB_OK;
+}
+
+template <typename F>
+hipError_t allow_lds(F f, int bytes) {
+  return bytes > 65536 ? hipFuncSetAttribute((const void *)f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
+}
+
+template <int NC>
+hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
+  const int lds = (4 * p.frows * (NC * 32 + 4) + 128) * 4;
+  hipError_t e = allow_lds(k_attend_few<NC>, lds);
+  if (e != hipSuccess) return e;
+  k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(256), lds, st>>>(A);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.few_pieces == 1) return e;
+  k_attend_join<16><<<dim3((unsigned)((p.few_items * p.frows + 3) / 4)), dim3(256), 0, st>>>(A, NC * 32);
+  return hipGetLastError();
+}
+
+template <int NC>
+hipError_t launch_many(const AttendArgs &A, const Plan &p, hipStream_t st) {
+  constexpr int NW = NC <= 4 ? 8 : 4, lds = 4 * NC * 32 * 128 + 64;
+  hipError_t e = allow_lds(k_attend_many<NC, NW>, lds);
+  if (e != hipSuccess) return e;
+  k_attend_many<NC, NW><<<dim3((unsigned)(p.many_items * p.many_pieces)), dim3(NW * 64), lds, st>>>(A);
+  e = hipGetLastError();
+  if (e != hipSuccess || p.many_pieces == 1) return e;
+  k_attend_join<NW * 32><<<dim3((unsigned)(p.many_items * (NW * 32) / 4)), dim3(256), 0, st>>>(A, NC * 32);
+  return hipGetLastError();
+}
+
+// The chunk of 32 dims as a constant.
+template <typename F>
+hipError_t with_dims(int Dp, F f) {
+  switch (Dp / 32) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
+
+}  // namespace
+
+extern "C" lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int64_t sequences, int64_t max_length) {
+  const auto refuse = [](const char *why) { return set_error(LB_EINVAL, std::string("lb_cache_reserve: ") + why); };
+  if (!C) return refuse("NULL cache");
+  if (rows < 0 || rows > kMaxRows || sequences < 0 || sequences > kMaxRows || max_length < 0 || max_length > kMaxRows)
+    return refuse("rows, sequences and max_length must be in [0, 2^30]");
+  if (heads < 1 || heads > 65536 || heads % C->KV) return refuse("heads must be a multiple of the cache's key heads");
+  if (rows == 0 || sequences == 0) return LB_OK;
+  const size_t need = reserve_bytes(C->KV, C->Dp, C->cus, rows, heads / C->KV, max_length);
+  DeviceGuard dg(C->device);
+  return grow(C, need, "lb_cache_reserve", false, nullptr);
+}
+
+extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, int heads, void *out, int64_t ldo,
+                                     const int32_t *start, const int32_t *lengths, const int32_t *table, int64_t ldt,
+                                     int columns, int sequences, int64_t rows, int64_t max_length, float scale,
+                                     int causal, int window, void *stream) {
+  const auto refuse = [](const char *why) { return set_error(LB_EINVAL, std::string("lb_cache_attend: ") + why); };
+  if (!C) return refuse("NULL cache");
+  if (rows < 0 || rows > kMaxRows || sequences < 0 || sequences > kMaxRows)
+    return refuse("rows and sequences must be in [0, 2^30]");
+  if (heads < 1 || heads > 65536 || heads % C->KV) return refuse("heads must be a multiple of the cache's key heads");
+  if (!(scale >= 0.f) || !(scale < INFINITY)) return refuse("scale must be finite and not negative");
+  if (window < 0 || (window && !causal)) return refuse("a window is not negative and needs causal");
+  if (max_length < 0 || max_length > kMaxRows) return refuse("max_length must be in [0, 2^30]");
+  if (rows == 0) return LB_OK;
+  const Sequences S = {start, lengths, table, ldt, sequences, (int)rows, columns, (int)C->pages};
+  lb_status st = check_sequences(C, S, "lb_cache_attend");
+  if (st != LB_OK) return st;
+  if (!q || !out) return refuse("NULL q or out");
+  const int64_t qw = (int64_t)heads * C->D, most_ld = (int64_t)1 << 31;
+  if (ldq < qw || ldo < qw) return refuse("a row stride is smaller than the row");
+  if (ldq > most_ld || ldo > most_ld) return refuse("a row stride exceeds 2^31");
+  if (((uintptr_t)q | (uintptr_t)out) % 2) return refuse("misaligned pointer");
+  const Rows o = {out, rows, (size_t)ldo * 2, (size_t)qw * 2};
+  if (meet({q, rows, (size_t)ldq * 2, (size_t)qw * 2}, o)) return refuse("q and out overlap");
+  if ((start && meet({start, 1, 0, (size_t)(sequences + 1) * 4}, o)) || meet({lengths, 1, 0, (size_t)sequences * 4}, o) ||
+      meet({table, sequences, (size_t)ldt * 4, (size_t)columns * 4}, o))
+    return refuse("an input and out overlap");
+  if (sequences == 0) return LB_OK;
+  int64_t most = (int64_t)columns * C->P;
+  if (max_length) most = std::min(most, max_length);
+  View view = {heads / C->KV, causal != 0, window, (int)most};
+  if (rows * (int64_t)view.group > 0x7fffffff)
+    return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
+  const Plan p = plan_of(C->KV, C->Dp, C->cus, start != nullptr, rows, sequences, view);
+  if (p.few_items * p.few_pieces > 0x7fffffff / 256 || p.many_items * p.many_pieces > 0x7fffffff / 512 ||
+      p.many_items * p.tr > 0x7fffffff)
+    return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
+  DeviceGuard dg(C->device);
+  hipStream_t stm = (hipStream_t)stream;
+  st = grow(C, p.ws, "lb_cache_attend", true, stm);
+  if (st != LB_OK) return st;
+  AttendArgs A = {};
+  A.S = S;
+  A.q = (const uint16_t *)q;
+  A.out = (uint16_t *)out;
+  A.ldq = ldq; A.ldo = ldo;
+  A.kc = C->k; A.vc = C->v; A.ks = C->ks; A.vs = C->vs;
+  A.part = (float *)C->ws;
+  A.qscale = scale * 1.44269504088896340736f;
+  A.KV = C->KV; A.D = C->D; A.lg = C->lg;
+  A.view = view;
+  A.few = p.few_rows;
+  A.tiles = p.tiles;
+  A.frows = p.frows;
+  A.row_tiles = p.row_tiles;
+  hipError_t e = hipSuccess;
+  if (p.few) {
+    AttendArgs F = A;
+    F.chunk = p.few_chunk;
+    F.pieces = p.few_pieces;
+    e = with_dims(C->Dp, [&](auto nc) { return launch_few<decltype(nc)::value>(F, p, stm); });
+  }
+  if (e == hipSuccess && p.many) {
+    AttendArgs M = A;
+    M.chunk = p.many_chunk;
+    M.pieces = p.many_pieces;
+    e = with_dims(C->Dp, [&](auto nc) { return launch_many<decltype(nc)::value>(M, p, stm); });
+  }
+  if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_cache_attend: ") + hipGetErrorString(e));
+  return LB_OK;
+}

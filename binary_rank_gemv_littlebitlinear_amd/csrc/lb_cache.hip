@@ -1,0 +1,542 @@
+// The paged 8-bit cache: storage, appending (with the position rotation) and
+// reading back.  See lb_cache.h for the layout.
+//
+// lb_cache_append: rows k, v of new tokens at positions p of their sequences.
+//
+//   k'   = R(p) k       pairs of the first `rot` dims turned by the angles of
+//                       p's row of the table, in fp32
+//   s'   = max(s, max |k'| / 127)   over the page's new tokens, s = 0 where the
+//                       page's first token is among them
+//   byte = rint(k' / s') + 128, and rint(byte s / s') for the page's earlier
+//                       tokens where s' > s
+//
+// and the same for v without R; q' = R(p) q, rounded once to fp16.  A page that
+// grows token by token therefore has the scale it would have got at once, and
+// its numbers are off by half a step for each time the scale grew.  A page with
+// a value that is not finite gets the scale NaN: all of it reads as NaN.
+//
+// A workgroup (one wave of it where tokens come one at a time) has one head of
+// one page: it reads the page's new rows once for the largest value and once
+// more, from its cache, to round them.  Bound by latency for single tokens and
+// by reading and writing for prompts.
+#include <algorithm>
+#include <new>
+
+#include "lb_cache.h"
+
+namespace {
+
+using namespace lbi;
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
+struct AppendArgs {
+  Sequences S;
+  const uint16_t *k, *v, *q;
+  uint16_t *qo;
+  int64_t ldk, ldv, ldq, ldqo;
+  const float *rope;  // positions x rot: cosines, then sines
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  int heads, KV, D, Dp, P, lg, rot, inter;
+  int64_t items;   // page slots of the launch
+  int64_t kvwgs;   // workgroups of keys and values; the others turn queries
+  int qparts;      // waves a row of queries has
+};
+
+// Dims 8 e .. 8 e + 7 of a head's row x, turned by the cosines and sines at cs
+// (rot / 2 of each).
+__device__ __forceinline__ void turn8(const uint16_t *x, int e, int D, const float *cs, int rot, int inter,
+                                      float (&o)[8]) {
+  const int d0 = 8 * e, half = rot >> 1;
+  const u32x4_t own = *LB_LOOSE128(x + d0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = h2f((uint16_t)(own[i] & 0xffffu));
+    o[2 * i + 1] = h2f((uint16_t)(own[i] >> 16));
+  }
+  if (d0 >= rot) return;
+  if (inter) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pair = (d0 >> 1) + i;
+      if (pair >= half) break;
+      const float c = cs[pair], s = cs[half + pair], a = o[2 * i], b = o[2 * i + 1];
+      o[2 * i] = a * c - b * s;
+      o[2 * i + 1] = a * s + b * c;
+    }
+    return;
+  }
+  if ((half & 7) == 0) {  // the partners are a group of 8 too
+    const bool low = d0 < half;
+    const u32x4_t other = *LB_LOOSE128(x + (low ? d0 + half : d0 - half));
+    const float *cp = cs + (low ? d0 : d0 - half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = h2f((uint16_t)(i & 1 ? other[i >> 1] >> 16 : other[i >> 1] & 0xffffu));
+      const float c = cp[i], s = cp[half + i];
+      o[i] = low ? o[i] * c - p * s : p * s + o[i] * c;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int d = d0 + i;
+    if (d < half)
+      o[i] = o[i] * cs[d] - h2f(x[d + half]) * cs[half + d];
+    else if (d < rot)
+      o[i] = h2f(x[d - half]) * cs[d] + o[i] * cs[d - half];
+  }
+}
+
+__device__ __forceinline__ uint32_t to_byte(float v, float s) {
+  // s = 0: the page holds zeros alone.  A NaN (of a page without a finite
+  // scale) becomes 0.
+  const float q = s > 0.f ? rintf(v / s) : 0.f;
+  return (uint32_t)((int)fminf(fmaxf(q, -127.f), 127.f) + 128);
+}
+__device__ __forceinline__ uint32_t again(uint32_t byte, float f) {
+  return (uint32_t)((int)rintf((float)((int)byte - 128) * f) + 128);
+}
+
+__device__ __forceinline__ float wave_amax(float v) {
+  // keeps NaN, which fmaxf would drop
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const float o = __shfl_xor(v, d);
+    v = o > v || o != o ? o : v;
+  }
+  return v;
+}
+__device__ __forceinline__ float amax(float m, float v) {
+  v = fabsf(v);
+  return v > m || v != v ? v : m;
+}
+
+// One head of one page, by NT threads: new tokens a .. e - 1 of the page, whose
+// first row is `row` (of token a).
+template <int NT, bool KEYS>
+__device__ void append_block(const AppendArgs &A, int64_t page, int h, int a, int e, int64_t row, int pos, float *part) {
+  const int t = threadIdx.x % NT;
+  const uint16_t *x = (KEYS ? A.k : A.v) + row * (KEYS ? A.ldk : A.ldv) + (int64_t)h * A.D;
+  const int64_t ld = KEYS ? A.ldk : A.ldv;
+  const int groups = A.D / 8, rot = KEYS ? A.rot : 0;
+  float m = 0.f;
+  for (int i = t; i < (e - a) * groups; i += NT) {
+    const int tok = i / groups, g = i - tok * groups;
+    float o[8];
+    turn8(x + tok * ld, g, A.D, rot ? A.rope + (int64_t)(pos + tok) * rot : nullptr, rot, A.inter, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = amax(m, o[j]);
+  }
+  m = wave_amax(m);
+  if constexpr (NT > 64) {
+    if ((t & 63) == 0) part[t >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) m = amax(m, part[i]);
+  }
+  float *scale = (KEYS ? A.ks : A.vs) + page * A.KV + h;
+  const float before = a > 0 ? *scale : 0.f;
+  float s = m / 127.f;
+  if (!(s < INFINITY)) s = __uint_as_float(0x7fc00000u);
+  if (!(s > before) && s == s) s = before;
+  const bool grown = a > 0 && s > before;
+  const float f = grown ? before / s : 1.f;
+  if constexpr (NT > 64) __syncthreads();  // every thread has read the scale
+  if (t == 0) *scale = s;
+
+  // the page's bytes: pieces of 16 (a pair of 32 dims) and 8 (the odd 32)
+  uint8_t *out = (KEYS ? A.kc : A.vc) + (page * A.KV + h) * (int64_t)A.P * A.Dp;
+  const int pairs = A.Dp / 64, odd = (A.Dp / 32) & 1, per = (pairs + odd) * 64;  // pieces of a unit
+  const int u0 = grown ? 0 : a >> 4, u1 = (e - 1) >> 4;
+  for (int i = t; i < (u1 - u0 + 1) * per; i += NT) {
+    const int u = u0 + i / per, piece = i % per, c = piece >> 6, lane = piece & 63, G = lane >> 4, xx = lane & 15;
+    const bool full = c < pairs;
+    uint8_t *to = out + (int64_t)u * 16 * A.Dp + (full ? piece * 16 : pairs * 1024 + lane * 8);
+    u32x4_t w = {0, 0, 0, 0};
+    if (KEYS) {
+      const int tok = u * 16 + xx;
+      if (tok >= e || (tok < a && !grown)) continue;
+      if (tok < a) {
+        if (full)
+          w = *(const u32x4_t *)to;
+        else
+          *(u32x2_t *)&w = *(const u32x2_t *)to;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t n = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) n |= again((w[d] >> (8 * j)) & 255u, f) << (8 * j);
+          w[d] = n;
+        }
+      } else {
+        const float *cs = rot ? A.rope + (int64_t)(pos + tok - a) * rot : nullptr;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int g = 8 * c + 4 * hh + G;
+          if ((!full && hh) || g >= groups) continue;
+          float o[8];
+          turn8(x + (tok - a) * ld, g, A.D, cs, rot, A.inter, o);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[2 * hh + (j >> 2)] |= to_byte(o[j], s) << (8 * (j & 3));
+        }
+      }
+    } else {
+      const int tok0 = u * 16 + 4 * G;
+      if (tok0 >= e || (tok0 + 3 < a && !grown)) continue;
+      if (tok0 < a || tok0 + 3 >= e) {  // bytes of other tokens stay
+        if (full)
+          w = *(const u32x4_t *)to;
+        else
+          *(u32x2_t *)&w = *(const u32x2_t *)to;
+      }
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const int d = 64 * c + 16 * ii + xx;
+        if ((!full && ii > 1) || d >= A.D) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int tok = tok0 + j;
+          const uint32_t was = (w[ii] >> (8 * j)) & 255u;
+          const uint32_t b = tok >= e ? was : tok < a ? (grown ? again(was, f) : was)
+                                                     : to_byte(h2f(x[(tok - a) * ld + d]), s);
+          w[ii] = (w[ii] & ~(255u << (8 * j))) | (b << (8 * j));
+        }
+      }
+    }
+    if (full)
+      *(u32x4_t *)to = w;
+    else
+      *(u32x2_t *)to = *(const u32x2_t *)&w;
+  }
+}
+
+// NT threads a block; a workgroup of 256 has 256 / NT of them.  Block = (page
+// slot, head, keys or values).
+template <int NT>
+__global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
+  __shared__ float part[256 / 64];
+  const Sequences &S = A.S;
+  if (blockIdx.x < A.kvwgs) {
+    const unsigned block = NT == 64 ? blockIdx.x * 4 + wave_id() : blockIdx.x;
+    const unsigned item = block / (unsigned)(2 * A.KV);
+    const int which = (int)(block - item * (2 * A.KV)), h = which >> 1;
+    if (item >= A.items) return;
+    int b = (int)item;
+    int64_t first = item;
+    if (S.start) b = find_sequence(S, item, 1, A.lg, 2, &first);
+    if (b < 0) return;
+    const Sequence q = sequence(S, b);
+    int p0, p1, col, a, e;
+    row_tokens(S, q, A.lg, &p0, &p1);
+    if (!touched(p0, p1, A.lg, item - first, &col, &a, &e)) return;
+    const int page = page_of(S, b, col);
+    if (page < 0) return;
+    const int pos = (col << A.lg) + a;
+    const int64_t row = row_of(q, pos);
+    if (which & 1)
+      append_block<NT, false>(A, page, h, a, e, row, pos, part);
+    else
+      append_block<NT, true>(A, page, h, a, e, row, pos, part);
+    return;
+  }
+  // queries: a wave turns 4 x hpi heads of a row, hpi whole heads at a time, so
+  // that a group's partner is read in the same step (q may be turned in place)
+  const unsigned wv = (blockIdx.x - (unsigned)A.kvwgs) * 4 + wave_id();
+  const unsigned row = wv / (unsigned)A.qparts;
+  const int qp = (int)(wv - row * A.qparts), lane = threadIdx.x & 63, groups = A.D / 8, hpi = 64 / groups;
+  if (row >= (unsigned)S.rows) return;
+  int b = (int)row;
+  int64_t first;
+  if (S.start) b = find_sequence(S, row, 1, 0, 0, &first);
+  if (b < 0) return;
+  const Sequence q = sequence(S, b);
+  int p0, p1;
+  row_tokens(S, q, A.lg, &p0, &p1);
+  const int pos = (int)row - q.row0 + (q.length - q.rows);
+  if (pos < p0 || pos >= p1) return;
+  const float *cs = A.rot ? A.rope + (int64_t)pos * A.rot : nullptr;
+  const int hl = lane / groups, g = lane - hl * groups;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int h = (qp * 4 + i) * hpi + hl;
+    const bool mine = hl < hpi && h < A.heads;
+    float o[8];
+    if (mine) turn8(A.q + row * A.ldq + (int64_t)h * A.D, g, A.D, cs, A.rot, A.inter, o);
+    __builtin_amdgcn_wave_barrier();  // all lanes have read before any writes
+    if (mine) {
+      u32x4_t w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = f2h(o[2 * j]) | (f2h(o[2 * j + 1]) << 16);
+      *LB_LOOSE128(A.qo + row * A.ldqo + (int64_t)h * A.D + 8 * g) = w;
+    }
+  }
+}
+
+// -------------------------------------------------------------- reading
+struct ReadArgs {
+  Sequences S;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  uint16_t *k, *v;
+  int64_t ldk, ldv, items;
+  int KV, D, Dp, lg;
+};
+
+// A wave has one unit of 16 tokens of one head, keys or values.
+__global__ void __launch_bounds__(256) k_cache_read(ReadArgs A) {
+  const Sequences &S = A.S;
+  const unsigned block = blockIdx.x * 4 + wave_id();
+  const unsigned item = block / (unsigned)(2 * A.KV);
+  const int which = (int)(block - item * (2 * A.KV)), h = which >> 1, lane = threadIdx.x & 63;
+  if (item >= A.items) return;
+  int b = (int)item;
+  int64_t first = item;
+  if (S.start) b = find_sequence(S, item, 1, 4, 2, &first);
+  if (b < 0) return;
+  const Sequence q = sequence(S, b);
+  int u, a, e;
+  if (!touched(max(0, q.length - q.rows), q.length, 4, item - first, &u, &a, &e)) return;
+  const int page = page_of(S, b, u >> (A.lg - 4));
+  const bool there = page >= 0;  // otherwise the tokens read as zeros
+  const int64_t block_of = (int64_t)(there ? page : 0) * A.KV + h;
+  const bool values = which & 1;
+  const float s = there ? (values ? A.vs : A.ks)[block_of] : 0.f;
+  const uint8_t *from = (values ? A.vc : A.kc) + ((block_of << A.lg) + ((u & ((1 << (A.lg - 4)) - 1)) << 4)) * A.Dp;
+  const int64_t row0 = row_of(q, u << 4);  // of the unit's first token
+  const int pairs = A.Dp / 64, n = pairs + ((A.Dp / 32) & 1), G = lane >> 4, x = lane & 15;
+  for (int c = 0; c < n; ++c) {
+    u32x4_t w = {0, 0, 0, 0};
+    if (c < pairs)
+      w = *(const u32x4_t *)(from + c * 1024 + lane * 16);
+    else
+      *(u32x2_t *)&w = *(const u32x2_t *)(from + c * 1024 + lane * 8);
+    const auto value = [&](int i) { return f2h((float)((int)((w[i >> 2] >> (8 * (i & 3))) & 255u) - 128) * s); };
+    const int parts = c < pairs ? 2 : 1;
+    if (values) {
+      for (int i = 0; i < 2 * parts; ++i) {
+        const int d = 64 * c + 16 * i + x;
+        if (d >= A.D) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (4 * G + j < a || 4 * G + j >= e) continue;
+          uint32_t word = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+          const float f = there ? (float)((int)((word >> (8 * j)) & 255u) - 128) * s : 0.f;
+          A.v[(row0 + 4 * G + j) * A.ldv + (int64_t)h * A.D + d] = (uint16_t)f2h(f);
+        }
+      }
+    } else {
+      if (x < a || x >= e) continue;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int g = 8 * c + 4 * hh + G;
+        if (hh >= parts || g * 8 >= A.D) continue;
+        u32x4_t o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = there ? value(8 * hh + 2 * j) | (value(8 * hh + 2 * j + 1) << 16) : 0u;
+        *LB_LOOSE128(A.k + (row0 + x) * A.ldk + (int64_t)h * A.D + 8 * g) = o;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+// Every number 0 and every scale 0: tokens that were never written read as 0.
+__global__ void __launch_bounds__(256) k_cache_clear(uint8_t *k, uint8_t *v, int64_t pieces, float *ks, float *vs, int64_t n) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  const u32x4_t zero = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+  for (int64_t i = at; i < pieces; i += step) ((u32x4_t *)k)[i] = ((u32x4_t *)v)[i] = zero;
+  for (int64_t i = at; i < n; i += step) ks[i] = vs[i] = 0.f;
+}
+
+Rows strided(const void *p, int64_t rows, int64_t ld, int64_t width) {
+  return {p, p ? rows : 0, (size_t)ld * 2, (size_t)width * 2};
+}
+
+// Memory of the call's own that must not be among what it writes.
+bool meets_sequences(const Sequences &S, const Rows &w) {
+  return (S.start && meet({S.start, 1, 0, (size_t)(S.n + 1) * 4}, w)) || meet({S.lengths, 1, 0, (size_t)S.n * 4}, w) ||
+         meet({S.table, S.n, (size_t)S.ldt * 4, (size_t)S.columns * 4}, w);
+}
+
+}  // namespace
+
+lb_status lbi::check_sequences(const lb_cache *C, const Sequences &S, const char *who) {
+  const auto refuse = [who](const std::string &why) { return set_error(LB_EINVAL, std::string(who) + ": " + why); };
+  if (S.n && (!S.lengths || !S.table)) return refuse("NULL lengths or table");
+  if (!S.start && S.rows != S.n) return refuse("without start there is one row for each sequence");
+  if (S.columns < 1 || (int64_t)S.columns * C->P > kMaxRows) return refuse("the table must hold 1 to 2^30 tokens");
+  if (S.n > 1 && S.ldt < S.columns) return refuse("the table's row stride is smaller than its row");
+  if (S.ldt > (int64_t)1 << 31) return refuse("the table's row stride exceeds 2^31");
+  if (((uintptr_t)S.start | (uintptr_t)S.lengths | (uintptr_t)S.table) % 4) return refuse("misaligned pointer");
+  return LB_OK;
+}
+
+extern "C" lb_status lb_cache_create(int64_t pages, int page_tokens, int kv_heads, int head_dim, lb_cache **out) {
+  const auto refuse = [](const char *why) { return set_error(LB_EINVAL, std::string("lb_cache_create: ") + why); };
+  if (!out) return refuse("out is NULL");
+  if (page_tokens < 16 || page_tokens > 256 || (page_tokens & (page_tokens - 1)))
+    return refuse("page_tokens must be a power of two from 16 to 256");
+  if (kv_heads < 1 || kv_heads > 1024) return refuse("need 1 to 1024 key heads");
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8) return refuse("head_dim must be a multiple of 8 from 8 to 256");
+  // units are numbered by 32-bit numbers
+  if (pages < 1 || pages > ((int64_t)0x7fffffff) / kv_heads / (page_tokens / 16)) return refuse("too few or too many pages");
+  lb_cache *C = nullptr;
+  try {
+    C = new lb_cache();
+  } catch (...) {
+    return set_error(LB_ENOMEM, "lb_cache_create: host allocation");
+  }
+  C->pages = pages;
+  C->P = page_tokens;
+  C->lg = __builtin_ctz((unsigned)page_tokens);
+  C->KV = kv_heads;
+  C->D = head_dim;
+  C->Dp = (head_dim + 31) / 32 * 32;
+  hipError_t e = hipGetDevice(&C->device);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&C->cus, hipDeviceAttributeMultiprocessorCount, C->device);
+  if (e != hipSuccess) {
+    delete C;
+    return set_error(LB_EHIP, std::string("lb_cache_create: ") + hipGetErrorString(e));
+  }
+  const size_t blocks = (size_t)pages * kv_heads, bytes = blocks * page_tokens * C->Dp;
+  void **to[] = {(void **)&C->k, (void **)&C->v, (void **)&C->ks, (void **)&C->vs};
+  for (int i = 0; i < 4 && e == hipSuccess; ++i) e = hipMalloc(to[i], i < 2 ? bytes : blocks * 4);
+  if (e != hipSuccess) {
+    lb_cache_destroy(C);
+    return set_error(LB_ENOMEM, std::string("lb_cache_create: hipMalloc: ") + hipGetErrorString(e));
+  }
+  k_cache_clear<<<dim3((unsigned)std::min<size_t>((bytes / 16 + 255) / 256, 8192)), dim3(256), 0, nullptr>>>(
+      C->k, C->v, (int64_t)(bytes / 16), C->ks, C->vs, (int64_t)blocks);
+  e = hipGetLastError();
+  if (e == hipSuccess) e = hipDeviceSynchronize();
+  if (e != hipSuccess) {
+    lb_cache_destroy(C);
+    return set_error(LB_EHIP, std::string("lb_cache_create: ") + hipGetErrorString(e));
+  }
+  *out = C;
+  return LB_OK;
+}
+
+extern "C" lb_status lb_cache_destroy(lb_cache *C) {
+  if (!C) return LB_OK;
+  DeviceGuard dg(C->device);
+  for (void *p : {(void *)C->k, (void *)C->v, (void *)C->ks, (void *)C->vs, C->ws})
+    if (p) (void)hipFree(p);
+  for (void *p : C->retired) (void)hipFree(p);
+  delete C;
+  return LB_OK;
+}
+
+extern "C" lb_status lb_cache_shape(const lb_cache *C, int64_t *pages, int *page_tokens, int *kv_heads, int *head_dim,
+                                    int *device) {
+  if (!C) return set_error(LB_EINVAL, "lb_cache_shape: NULL cache");
+  if (pages) *pages = C->pages;
+  if (page_tokens) *page_tokens = C->P;
+  if (kv_heads) *kv_heads = C->KV;
+  if (head_dim) *head_dim = C->D;
+  if (device) *device = C->device;
+  return LB_OK;
+}
+
+extern "C" lb_status lb_cache_append(lb_cache *C, const void *k, int64_t ldk, const void *v, int64_t ldv, const void *q,
+                                     int64_t ldq, void *q_out, int64_t ldqo, int heads, const float *rope,
+                                     int64_t positions, int rot, int interleaved, const int32_t *start,
+                                     const int32_t *lengths, const int32_t *table, int64_t ldt, int columns,
+                                     int sequences, int64_t rows, void *stream) {
+  const auto refuse = [](const char *why) { return set_error(LB_EINVAL, std::string("lb_cache_append: ") + why); };
+  if (!C) return refuse("NULL cache");
+  if (rows < 0 || rows > kMaxRows || sequences < 0 || sequences > kMaxRows)
+    return refuse("rows and sequences must be in [0, 2^30]");
+  if (rows == 0) return LB_OK;
+  const Sequences S = {start, lengths, table, ldt, sequences, (int)rows, columns, (int)C->pages};
+  const lb_status st = check_sequences(C, S, "lb_cache_append");
+  if (st != LB_OK) return st;
+  if (!k || !v) return refuse("NULL k or v");
+  if (!q != !q_out) return refuse("q and q_out go together");
+  if (q && (heads < 1 || heads > 65536)) return refuse("need 1 to 65536 heads of q");
+  if (rot < 0 || rot > C->D || rot % 2) return refuse("rot must be even and at most head_dim");
+  if (rot && !rope) return refuse("NULL rope");
+  if (rot && positions < (int64_t)columns * C->P) return refuse("rope needs a row for every token that the table can hold");
+  const int64_t kw = (int64_t)C->KV * C->D, qw = (int64_t)heads * C->D, most = (int64_t)1 << 31;
+  if (ldk < kw || ldv < kw || (q && (ldq < qw || ldqo < qw))) return refuse("a row stride is smaller than the row");
+  if (ldk > most || ldv > most || (q && (ldq > most || ldqo > most))) return refuse("a row stride exceeds 2^31");
+  if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)q | (uintptr_t)q_out) % 2 || (uintptr_t)rope % 4)
+    return refuse("misaligned pointer");
+  if (q) {
+    const Rows w = strided(q_out, rows, ldqo, qw);
+    if (!(q == q_out && ldq == ldqo) && meet(strided(q, rows, ldq, qw), w))
+      return refuse("q and q_out overlap (they may be the same rows)");
+    if (meet(strided(k, rows, ldk, kw), w) || meet(strided(v, rows, ldv, kw), w)) return refuse("k or v and q_out overlap");
+    if ((rot && meet({rope, 1, 0, (size_t)positions * rot * 4}, w)) || meets_sequences(S, w))
+      return refuse("an input and q_out overlap");
+  }
+  AppendArgs A = {};
+  A.S = S;
+  A.k = (const uint16_t *)k;
+  A.v = (const uint16_t *)v;
+  A.q = (const uint16_t *)q;
+  A.qo = (uint16_t *)q_out;
+  A.ldk = ldk; A.ldv = ldv; A.ldq = ldq; A.ldqo = ldqo;
+  A.rope = rope;
+  A.kc = C->k; A.vc = C->v; A.ks = C->ks; A.vs = C->vs;
+  A.heads = heads; A.KV = C->KV; A.D = C->D; A.Dp = C->Dp; A.P = C->P; A.lg = C->lg;
+  A.rot = rot;
+  A.inter = interleaved != 0;
+  // sequence b begins a new page at most every P rows, and touches one more at each end
+  A.items = start ? (rows >> C->lg) + 2 * (int64_t)sequences : sequences;
+  const bool single = rows <= 2 * (int64_t)sequences;
+  const int64_t blocks = A.items * 2 * C->KV;
+  A.kvwgs = single ? (blocks + 3) / 4 : blocks;
+  const int hpi = 64 / (C->D / 8);
+  A.qparts = q ? (heads + 4 * hpi - 1) / (4 * hpi) : 0;
+  const int64_t qwgs = (rows * A.qparts + 3) / 4;
+  if (A.kvwgs + qwgs > 0x7fffffff / 256 || blocks > 0x7fffffff)
+    return set_error(LB_EUNSUPPORTED, "lb_cache_append: too many rows and heads for one call");
+  DeviceGuard dg(C->device);
+  const dim3 grid((unsigned)(A.kvwgs + qwgs));
+  if (single)
+    k_cache_append<64><<<grid, dim3(256), 0, (hipStream_t)stream>>>(A);
+  else
+    k_cache_append<256><<<grid, dim3(256), 0, (hipStream_t)stream>>>(A);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_cache_append: ") + hipGetErrorString(e));
+  return LB_OK;
+}
+
+extern "C" lb_status lb_cache_read(const lb_cache *C, void *k, int64_t ldk, void *v, int64_t ldv, const int32_t *start,
+                                   const int32_t *lengths, const int32_t *table, int64_t ldt, int columns,
+                                   int sequences, int64_t rows, void *stream) {
+  const auto refuse = [](const char *why) { return set_error(LB_EINVAL, std::string("lb_cache_read: ") + why); };
+  if (!C) return refuse("NULL cache");
+  if (rows < 0 || rows > kMaxRows || sequences < 0 || sequences > kMaxRows)
+    return refuse("rows and sequences must be in [0, 2^30]");
+  if (rows == 0) return LB_OK;
+  const Sequences S = {start, lengths, table, ldt, sequences, (int)rows, columns, (int)C->pages};
+  const lb_status st = check_sequences(C, S, "lb_cache_read");
+  if (st != LB_OK) return st;
+  if (!k || !v) return refuse("NULL k or v");
+  const int64_t kw = (int64_t)C->KV * C->D, most = (int64_t)1 << 31;
+  if (ldk < kw || ldv < kw) return refuse("a row stride is smaller than the row");
+  if (ldk > most || ldv > most) return refuse("a row stride exceeds 2^31");
+  if (((uintptr_t)k | (uintptr_t)v) % 2) return refuse("misaligned pointer");
+  const Rows kr = strided(k, rows, ldk, kw), vr = strided(v, rows, ldv, kw);
+  if (meet(kr, vr)) return refuse("k and v overlap");
+  if (meets_sequences(S, kr) || meets_sequences(S, vr)) return refuse("an input and k or v overlap");
+  ReadArgs A = {};
+  A.S = S;
+  A.kc = C->k; A.vc = C->v; A.ks = C->ks; A.vs = C->vs;
+  A.k = (uint16_t *)k;
+  A.v = (uint16_t *)v;
+  A.ldk = ldk; A.ldv = ldv;
+  A.items = start ? (rows >> 4) + 2 * (int64_t)sequences : sequences;
+  A.KV = C->KV; A.D = C->D; A.Dp = C->Dp; A.lg = C->lg;
+  const int64_t blocks = A.items * 2 * C->KV;
+  if (blocks > (int64_t)0x7fffffff / 64) return set_error(LB_EUNSUPPORTED, "lb_cache_read: too many rows and heads for one call");
+  DeviceGuard dg(C->device);
+  k_cache_read<<<dim3((unsigned)((blocks + 3) / 4)), dim3(256), 0, (hipStream_t)stream>>>(A);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_cache_read: ") + hipGetErrorString(e));
+  return LB_OK;
+}

@@ -1,0 +1,179 @@
+// Which rows, pages and keys the work items of the cache calls have: integer
+// arithmetic alone, the same on the host (where it is tested) and the device.
+// Starts, lengths and pages come from device memory and may hold anything: what
+// is computed from them stays inside the call's rows, the table and the cache.
+#pragma once
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+#if defined(__HIPCC__)
+#define LB_HD __host__ __device__ __forceinline__
+#else
+#define LB_HD inline
+#endif
+
+namespace lbi {
+
+constexpr int kMaxTokens = 1 << 30;
+
+LB_HD int imin(int a, int b) { return a < b ? a : b; }
+LB_HD int imax(int a, int b) { return a > b ? a : b; }
+
+// The sequences of a call, on the device: sequence b's rows are start[b] ..
+// start[b + 1] - 1 (row b alone without start), its last tokens of lengths[b].
+struct Sequences {
+  const int *start, *lengths, *table;
+  int64_t ldt;
+  int n, rows, columns, pages;
+};
+
+struct Sequence {
+  int row0, rows, length;  // the length as given, within [0, 2^30]
+};
+
+LB_HD Sequence sequence(const Sequences &S, int b) {
+  Sequence q;
+  q.row0 = S.start ? imin(imax(S.start[b], 0), S.rows) : b;
+  q.rows = S.start ? imin(imax(S.start[b + 1], q.row0), S.rows) - q.row0 : 1;
+  q.length = imin(imax(S.lengths[b], 0), kMaxTokens);
+  return q;
+}
+
+// Work items of all sequences in one row: those of sequence b begin here, which
+// leaves it floor(rows * mul / 2^lg) + extra of them or more.
+LB_HD int64_t first_item(const Sequences &S, int b, int mul, int lg, int extra) {
+  return (((int64_t)imin(imax(S.start[b], 0), S.rows) * mul) >> lg) + (int64_t)extra * b;
+}
+
+// Tokens before the table's end that the sequence's rows are, by position; rows at
+// positions below 0 or past the table are none.
+LB_HD void row_tokens(const Sequences &S, const Sequence &q, int lg, int *p0, int *p1) {
+  *p0 = imax(0, q.length - q.rows);
+  *p1 = imin(q.length, S.columns << lg);
+}
+
+// The row of the token at position p.
+LB_HD int row_of(const Sequence &q, int p) { return q.row0 + (q.rows - q.length) + p; }
+
+// The index-th block of 2^lg tokens (page or unit) that the tokens p0 .. p1 - 1
+// touch: its number, and the first and last + 1 of them in it; false past the last.
+LB_HD bool touched(int p0, int p1, int lg, int64_t index, int *block, int *a, int *e) {
+  if (p0 >= p1) return false;
+  const int64_t at = (p0 >> lg) + index;
+  if (at > (p1 - 1) >> lg) return false;
+  const int base = (int)at << lg;
+  *block = (int)at;
+  *a = imax(0, p0 - base);
+  *e = imin(1 << lg, p1 - base);
+  return true;
+}
+
+// The page of a sequence's column, -1 if there is none.
+LB_HD int page_of(const Sequences &S, int b, int column) {
+  const int page = column < S.columns ? S.table[b * S.ldt + column] : -1;
+  return page >= 0 && page < S.pages ? page : -1;
+}
+
+// What an attention call looks at.
+struct View {
+  int group;           // rows of a key head for each token
+  int causal, window;  // window 0: none
+  int most;            // keys of a sequence, at most what the table holds
+};
+
+// Rows are token * group + head.  The keys [first, last) that row r sees.
+LB_HD void keys_of_row(const View &A, const Sequence &q, int r, int *first, int *last) {
+  const int keys = imin(q.length, A.most), p = q.length - q.rows + r / A.group;
+  *last = A.causal ? imax(0, imin(keys, p + 1)) : keys;
+  *first = A.window ? imax(0, p - A.window + 1) : 0;
+}
+
+// The keys [lo, hi) that rows r0 .. r0 + n - 1 see together, lo a multiple of 16;
+// 0, 0 if there are none.
+LB_HD void keys_of_rows(const View &A, const Sequence &q, int r0, int n, int *lo, int *hi) {
+  int unused;
+  keys_of_row(A, q, r0, lo, &unused);
+  keys_of_row(A, q, r0 + n - 1, &unused, hi);
+  *lo &= ~15;
+  if (*lo >= *hi) *lo = *hi = 0;
+}
+
+LB_HD int pieces_of(int lo, int hi, int chunk) { return imax(1, (int)(((int64_t)hi - lo + chunk - 1) / chunk)); }
+
+// How an attention call is cut up.  A sequence of up to few_rows rows (tokens x
+// group) has tiles of 16 rows in k_attend_few, one with more has tiles of tr rows
+// in k_attend_many; the keys of each are cut into pieces.
+struct Plan {
+  bool few = false, many = false;
+  int few_rows = 0, tiles = 0, frows = 0;  // tiles a sequence may have, rows of a tile
+  int few_chunk = 0, few_pieces = 1, many_chunk = 0, many_pieces = 1, row_tiles = 0, tr = 0;
+  int64_t few_items = 0, many_items = 0;
+  size_t ws = 0;  // bytes of partial sums
+};
+
+constexpr int kFewChunk = 256;    // keys of the smallest piece of k_attend_few
+constexpr int kManyChunk = 512;   // and of k_attend_many
+constexpr int kFewPieces = 2048;  // pieces that a call of k_attend_few has, if it has fewer items
+
+inline int many_tile(int Dp) { return Dp <= 128 ? 256 : 128; }
+
+// Pieces of an item's keys: about `target` for all items together, of `least`
+// keys or more; `span` bounds an item's keys.
+inline int cut(int64_t items, int64_t span, int64_t target, int64_t least, int *chunk) {
+  const int64_t each = std::max<int64_t>(1, target / items);
+  const int64_t c = std::max<int64_t>(least, ((span + each - 1) / each + 63) / 64 * 64);
+  *chunk = (int)c;
+  return (int)std::max<int64_t>(1, (span + c - 1) / c);
+}
+
+inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t n, const View &A) {
+  Plan p;
+  const int group = A.group;
+  const int64_t per_row = (int64_t)Dp + 2;
+  p.tr = many_tile(Dp);
+  if (!starts) {
+    p.few = true;
+    p.few_rows = group;
+    p.tiles = (group + 15) / 16;
+  } else {
+    p.tiles = std::max(2, (group + 15) / 16);
+    p.few_rows = 16 * p.tiles;
+    p.many = rows * group > p.few_rows;
+    p.few = n > 1 || !p.many;
+    if (!p.few) p.few_rows = 0;
+    if (!p.many) p.tiles = (int)((rows * group + 15) / 16);
+  }
+  p.frows = std::min(16, std::max(1, p.few_rows));
+  // the keys of tile_rows rows: from the first's window, cut down to a unit, to the last's position
+  const auto span_of = [&](int64_t tile_rows) {
+    return A.window ? std::min<int64_t>(A.most, A.window + tile_rows / group + 1 + 16) : (int64_t)A.most;
+  };
+  if (p.few) {
+    p.few_items = n * KV * p.tiles;
+    p.few_pieces = cut(p.few_items, span_of(p.frows), kFewPieces, kFewChunk, &p.few_chunk);
+    if (p.few_pieces > 1) p.ws = (size_t)(p.few_items * p.few_pieces * p.frows * per_row) * 4;
+  }
+  if (p.many) {
+    p.row_tiles = (int)(rows * group / p.tr + n);
+    p.many_items = (int64_t)p.row_tiles * KV;
+    p.many_pieces = cut(p.many_items, span_of(p.tr), cus, kManyChunk, &p.many_chunk);
+    if (p.many_pieces > 1) p.ws = std::max(p.ws, (size_t)(p.many_items * p.many_pieces * p.tr * per_row) * 4);
+  }
+  return p;
+}
+
+// Workspace that is enough for every call of up to `rows` rows, any number of
+// sequences and `most` keys: an item has more than one piece only while all of
+// them together stay below the target.
+inline size_t reserve_bytes(int KV, int Dp, int cus, int64_t rows, int group, int64_t most) {
+  const int64_t per_row = (int64_t)Dp + 2;
+  (void)KV;
+  size_t need = 0;
+  if (most > kFewChunk) need = (size_t)(kFewPieces * 16 * per_row) * 4;
+  if (most > kManyChunk && rows * group > 32)
+    need = std::max(need, (size_t)((int64_t)cus * many_tile(Dp) * per_row) * 4);
+  return need;
+}
+
+}  // namespace lbi

@@ -70,6 +70,7 @@ extern "C" {
 typedef struct lb_layer lb_layer; /* opaque, library-owned */
 typedef struct lb_stack lb_stack; /* opaque, library-owned */
 typedef struct lb_bank lb_bank;   /* opaque, library-owned */
+typedef struct lb_cache lb_cache; /* opaque, library-owned */
 
 typedef enum {
   LB_OK = 0,
@@ -497,6 +498,114 @@ lb_status lb_route_combine(const void *y, int64_t y_rows, int64_t ldy, const int
                            const float *weights, int64_t tokens, int k, int64_t width,
                            const void *residual, int64_t ldr, void *out, int64_t ldo, int out_type,
                            void *stream);
+
+/* --------------------------------------------------------------- norms */
+/* The end of a block and the beginning of the next, on the current device:
+ *
+ *     u = y, or with post  N(y) * post_weight + post_bias
+ *     r' = scale * r + gate * u
+ *     x  = N(r') * weight + bias
+ *
+ * N(v) = v / sqrt(mean(v^2) + eps) (LB_NORM_RMS), or the same of v less its
+ * mean (LB_NORM_LAYER).  fp32 throughout; x is the norm of r' before r' is
+ * rounded, and out and x are rounded once.
+ *   y         device, rows x width of y_type, row stride ldy, or NULL
+ *   gate      device fp16, rows x width with row stride ldg, or with ldg = 0
+ *             one row for all of them, or NULL
+ *   r         device, rows x width of r_type, row stride ldr, or NULL (r' is
+ *             gate * u then); y or r must be given
+ *   out       r' of r_type, row stride ldo, or NULL
+ *   x         fp16, row stride ldx, or NULL; out or x must be given
+ *   post_weight, post_bias, weight, bias   device fp16, width, or NULL
+ * out and x may be the same rows as y or r (same pointer, stride and type) and
+ * must overlap nothing otherwise (column blocks of one buffer with the same
+ * row stride in bytes do not).  1 <= width <= 32768. */
+typedef enum { LB_NORM_RMS = 0, LB_NORM_LAYER = 1 } lb_norm_kind;
+lb_status lb_norm(int kind, const void *y, int y_type, int64_t ldy, int post, const void *post_weight,
+                  const void *post_bias, const void *gate, int64_t ldg, const void *r, int64_t ldr,
+                  float scale, int r_type, const void *weight, const void *bias, float eps, void *out,
+                  int64_t ldo, void *x, int64_t ldx, int64_t rows, int64_t width, void *stream);
+
+/* -------------------------------------------------------------- caches */
+/* A cache holds keys and values of attention in 8 bits, in pages of
+ * page_tokens tokens (a power of two, 16 to 256) of kv_heads heads of
+ * head_dim numbers (a multiple of 8, at most 256), with one fp32 scale for
+ * the keys and one for the values of each page and head:
+ * value = number * scale, numbers -127 .. 127, scale = largest / 127.
+ * Which page belongs to whom is the caller's: a call gets its sequences as
+ *   table     device int32, sequences x columns, row stride ldt: the pages
+ *             of every sequence in the order of its tokens.  Pages may be
+ *             shared between sequences, but not written by two in one call
+ *   lengths   device int32: tokens of every sequence, the call's included
+ *   start     device int32, sequences + 1 non-decreasing values in
+ *             [0, rows]: rows start[b] .. start[b + 1] - 1 are the last tokens
+ *             of sequence b, at positions lengths[b] - count .. lengths[b] - 1;
+ *             or NULL: row b is the last token of sequence b (rows =
+ *             sequences)
+ * These are read on the device only.  Rows outside [start[0],
+ * start[sequences]) are left as they were; a page outside the cache is no
+ * page (nothing is written there, nothing attended, zeros read), nor is what
+ * lies past the table; rows at positions below 0 are dropped.
+ *
+ * The cache belongs to the device that is current at lb_cache_create; all
+ * pointers and streams of its calls belong to it too.  lb_cache_attend uses
+ * a workspace of the cache's own: order a cache's calls on one stream.  They
+ * launch kernels only, unless lb_cache_attend needs more workspace than was
+ * reserved or used before: then it grows (as a bank's), or, under capture,
+ * the call returns LB_ENOTREADY. */
+/* All numbers of a new cache are 0.  Allocates and synchronises the device. */
+lb_status lb_cache_create(int64_t pages, int page_tokens, int kv_heads, int head_dim, lb_cache **out);
+
+/* Any pointer may be NULL. */
+lb_status lb_cache_shape(const lb_cache *C, int64_t *pages, int *page_tokens, int *kv_heads, int *head_dim,
+                         int *device);
+
+/* Append keys and values, turned by their positions, to the cache.
+ *   k, v      device fp16, rows x (kv_heads * head_dim), row strides ldk, ldv
+ *   q, q_out  device fp16, rows x (heads * head_dim): q turned as k is and
+ *             rounded once; both NULL, or q_out may be q itself with the same
+ *             stride
+ *   rope      device fp32, positions x rot: of each position rot / 2 cosines,
+ *             then rot / 2 sines, at least columns * page_tokens positions;
+ *             rot even, at most head_dim, 0 for no rotation.  Pair i is dims
+ *             (i, i + rot / 2), or (2i, 2i + 1) when interleaved:
+ *             (a, b) -> (a cos - b sin, a sin + b cos), in fp32
+ * A page whose first token is written starts a new scale; otherwise its scale
+ * grows as needed and its earlier numbers are rounded again, by half a step
+ * each time.  A page that receives a NaN or an infinity reads as NaN from then
+ * on.  Appending the same rows twice leaves what appending them once does. */
+lb_status lb_cache_append(lb_cache *C, const void *k, int64_t ldk, const void *v, int64_t ldv, const void *q,
+                          int64_t ldq, void *q_out, int64_t ldqo, int heads, const float *rope,
+                          int64_t positions, int rot, int interleaved, const int32_t *start,
+                          const int32_t *lengths, const int32_t *table, int64_t ldt, int columns,
+                          int sequences, int64_t rows, void *stream);
+
+/* The values of the sequences' last tokens: k, v (device fp16, rows x
+ * (kv_heads * head_dim), row strides ldk, ldv), each rounded once. */
+lb_status lb_cache_read(const lb_cache *C, void *k, int64_t ldk, void *v, int64_t ldv, const int32_t *start,
+                        const int32_t *lengths, const int32_t *table, int64_t ldt, int columns, int sequences,
+                        int64_t rows, void *stream);
+
+/* Workspace for lb_cache_attend calls of up to `rows` rows of `heads` heads,
+ * `sequences` sequences and max_length tokens, now. */
+lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int64_t sequences, int64_t max_length);
+
+/* out = softmax(scale * q K^T) V over the cache, fp32 inside, rounded once.
+ *   q, out    device fp16, rows x (heads * head_dim), row strides ldq, ldo;
+ *             heads a multiple of kv_heads: head h reads key head
+ *             h / (heads / kv_heads).  out must not overlap the inputs
+ *   max_length  a bound on lengths that the call is cut up for (tokens past it
+ *             are not seen), or 0: what the table can hold
+ *   causal    a row sees its sequence's tokens up to its own position;
+ *             otherwise all of them
+ *   window    with causal: the last `window` of those only; 0 for all
+ * A row that sees no token gets zeros. */
+lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, int heads, void *out, int64_t ldo,
+                          const int32_t *start, const int32_t *lengths, const int32_t *table, int64_t ldt,
+                          int columns, int sequences, int64_t rows, int64_t max_length, float scale, int causal,
+                          int window, void *stream);
+
+lb_status lb_cache_destroy(lb_cache *C);
 
 /* ---------------------------------------------------------- diagnostics */
 const char *lb_status_str(lb_status st);
