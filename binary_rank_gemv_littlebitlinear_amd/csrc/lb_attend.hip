@@ -46,6 +46,10 @@ typedef float4_t __attribute__((aligned(8))) float4a_t;
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr float kUp = 12.f, kSlack = 3.f;
+// Of k_attend_many: the scale of a page that is not there, and the smallest
+// reference of the values' scales (all are above 2^-32).
+constexpr float kMissing = -1e9f, kLeast = -100.f;
+constexpr int kJoinWave = 8;  // pieces of a row up to which a wave joins it, not a workgroup
 
 struct AttendArgs {
   Sequences S;
@@ -85,6 +89,15 @@ __device__ __forceinline__ half8_t to_half8(uint32_t w0, uint32_t w1) {
 }
 
 __device__ __forceinline__ float lane_xor(float v, int d) { return __shfl_xor(v, d); }
+// The values of lanes 16 and 32 away, without a trip through LDS.
+__device__ __forceinline__ float other16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 16 ? r[0] : r[1]);
+}
+__device__ __forceinline__ float other32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
 
 // Item `slot` of k_attend_few: (sequence, key head, 16-row tile), or false.
 __device__ __forceinline__ bool few_item(const AttendArgs &A, unsigned slot, Item &it) {
@@ -190,6 +203,12 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
     const int mine = blk * upp + (u & (upp - 1));
     const float ks = there ? A.ks[blk] * A.qscale : 0.f, vs = there ? A.vs[blk] : 0.f;
     const unsigned long long ok = __ballot(there);
+    const int steps = (min(u1 - ub, 64) + 1) >> 1;
+    Frag K[2], V[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load(A.kc, __builtin_amdgcn_readlane(mine, i), K[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load(A.vc, __builtin_amdgcn_readlane(mine, i), V[i]);
     float big = vs < INFINITY ? vs : 0.f;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) big = fmaxf(big, lane_xor(big, d));
@@ -200,23 +219,10 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
       r = big;
     }
     const float ratio = vs / r;
-    const int steps = (min(u1 - ub, 64) + 1) >> 1;
-    Frag K[2], V[2], Kn[2], Vn[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = __builtin_amdgcn_readlane(mine, i);
-      load(A.kc, at, K[i]);
-      load(A.vc, at, V[i]);
-    }
     for (int st = 0; st < steps; ++st) {
-      if (st + 1 < steps) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = __builtin_amdgcn_readlane(mine, 2 * st + 2 + i);
-          load(A.kc, at, Kn[i]);
-          load(A.vc, at, Vn[i]);
-        }
-      }
+      // the next step's units, this one's again behind the last
+      const int n0 = __builtin_amdgcn_readlane(mine, min(2 * st + 2, 2 * steps - 2));
+      const int n1 = __builtin_amdgcn_readlane(mine, min(2 * st + 3, 2 * steps - 1));
       float z[8];
       float top = -INFINITY;
 #pragma unroll
@@ -229,6 +235,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
         }
         if constexpr (kOdd)
           acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8(K[i].odd[0], K[i].odd[1]), q[NC - 1], acc, 0, 0, 0);
+        load(A.kc, i ? n1 : n0, K[i]);
         const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * st + i));
         const bool have = (ok >> (2 * st + i)) & 1;
         const int t0 = (ub + 2 * st + i) * 16 + 4 * G;
@@ -239,8 +246,8 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
           top = fmaxf(top, z[4 * i + j]);
         }
       }
-      top = fmaxf(top, lane_xor(top, 16));
-      top = fmaxf(top, lane_xor(top, 32));
+      top = fmaxf(top, other16(top));
+      top = fmaxf(top, other32(top));
       const bool up = top > m + kSlack;  // also the first finite one: m is -inf
       if (__any(up)) {
         const float f = up ? exp2f(m - top) : 1.f;
@@ -282,15 +289,12 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
           O[4 * kPairs + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl, O[4 * kPairs + i], 0, 0, 0);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        K[i] = Kn[i];
-        V[i] = Vn[i];
-      }
+      load(A.vc, n0, V[0]);
+      load(A.vc, n1, V[1]);
     }
   }
-  l += lane_xor(l, 16);
-  l += lane_xor(l, 32);
+  l += other16(l);
+  l += other32(l);
 
   // the four waves' sums, in units of 1
   constexpr int kPitch = Dp + 4;
@@ -341,13 +345,17 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
 
 // ------------------------------------------------------------ many rows
 // 32 rows a wave, NW waves a workgroup; tiles of 64 keys and values go through
-// LDS as fp16 operands (converted once for all waves), the next tile's bytes on
-// their way meanwhile.
+// LDS as fp16 operands (converted once for all waves), the bytes of a later tile
+// on their way meanwhile.  A step weighs and adds up tile t (exponentials, then
+// the second product) while the matrix cores have the first product of tile
+// t + 1, so keys are staged a tile ahead of values.
 template <int NC, int NW>
 __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = NC, TR = NW * 32;
   constexpr int kHalf = Dp * 128;  // bytes of a tile's keys, or values
-  extern __shared__ char smem[];   // [2][keys, values], then the scales [2][2][4]
+  // [2] tiles of keys, [2] of values, then scales: of keys [4][4] (read a step
+  // after the keys themselves, while those of two tiles on are written), of values [2][4]
+  extern __shared__ char smem[];
   float *scales = (float *)(smem + 4 * kHalf);
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 31, G = lane >> 5;
   // heads vary fastest, so that one head's tiles mostly meet on one XCD; the
@@ -373,8 +381,10 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
     const int ra = it.r0 + min(w * 32, it.n - 1), rb = it.r0 + min(w * 32 + 31, it.n - 1);
     keys_of_row(A.view, it.q, ra, &some_first, &all_last);
     keys_of_row(A.view, it.q, rb, &all_first, &some_last);
-    all_last = min(all_last, c1);
-    some_last = min(some_last, c1);
+    some_first = __builtin_amdgcn_readfirstlane(some_first);
+    all_first = __builtin_amdgcn_readfirstlane(all_first);
+    all_last = __builtin_amdgcn_readfirstlane(min(all_last, c1));
+    some_last = __builtin_amdgcn_readfirstlane(min(some_last, c1));
   }
   half8_t q[Dp / 16];
   {
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) O[i][j] = 0.f;
-  float m = -INFINITY, l = 0.f, r = 1e-30f;
+  float m = -INFINITY, l = 0.f, lr = kLeast;
 
   const int upp = 1 << (A.lg - 4);
   // staging: NW = 8: waves 0..3 have the tile's units of keys, 4..7 of values;
@@ -400,32 +410,41 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
     float scale;
   };
   Frag f[kKinds];
+  const auto is_values = [&](int i) { return NW == 8 ? w >= 4 : i == 1; };
+  // Requests tile `tile` of values and the one behind it of keys.
   const auto fetch = [&](int tile) {
-    const int tok = c0 + tile * 64 + su * 16;
-    const int page = tok < c1 ? page_of(A.S, b, tok >> A.lg) : -1;
-    const bool there = page >= 0;
-    const int blk = (there ? page : 0) * A.KV + it.h;
-    const int unit = blk * upp + ((tok >> 4) & (upp - 1));
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
-      const bool values = NW == 8 ? w >= 4 : i == 1;
+      const bool values = is_values(i);
+      const int tok = c0 + (tile + (values ? 0 : 1)) * 64 + su * 16;
+      const int page = tok >= c0 && tok < c1 ? page_of(A.S, b, tok >> A.lg) : -1;
+      const bool there = page >= 0;
+      const int blk = (there ? page : 0) * A.KV + it.h;
+      const int unit = blk * upp + ((tok >> 4) & (upp - 1));
       const uint8_t *p = (values ? A.vc : A.kc) + (int64_t)unit * kUnit;
 #pragma unroll
       for (int c = 0; c < kPairs; ++c)
         f[i].pair[c] = *(const u32x4_t __attribute__((address_space(1))) *)(uintptr_t)(p + c * 1024 + lane * 16);
       if constexpr (kOdd)
         f[i].odd = *(const u32x2_t __attribute__((address_space(1))) *)(uintptr_t)(p + kPairs * 1024 + lane * 8);
-      // a missing unit has scale -1: its keys are not seen
-      f[i].scale = there ? (values ? A.vs[blk] : A.ks[blk] * A.qscale) : -1.f;
+      f[i].scale = (values ? A.vs : A.ks)[blk];
+      if (!there) f[i].scale = kMissing;
     }
   };
-  const auto put = [&](int buf) {
+  const auto put = [&](int tile) {
     const int x = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
-      const bool values = NW == 8 ? w >= 4 : i == 1;
-      char *to = smem + (2 * buf + (values ? 1 : 0)) * kHalf;
-      if (lane == 0) scales[(2 * buf + (values ? 1 : 0)) * 4 + su] = f[i].scale;
+      const bool values = is_values(i);
+      const int buf = (tile + (values ? 0 : 1)) & 1;
+      char *to = smem + (2 * (values ? 1 : 0) + buf) * kHalf;
+      if (lane == 0) {
+        // Keys: the factor of a score, tiny instead of 0 (of a page of zeros, whose
+        // scores are 0) so that it keeps a masked -inf.  Values: log2 of the scale.
+        float v = f[i].scale;
+        if (v != kMissing) v = values ? __log2f(v) : v * A.qscale == 0.f ? 1e-30f : v * A.qscale;
+        scales[(values ? 16 + buf * 4 : ((tile + 1) & 3) * 4) + su] = v;
+      }
       if (!values) {
         // [dim / 8][key 64][8]
 #pragma unroll
@@ -454,91 +473,124 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
       }
     }
   };
+  const float16_t none = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // The first product of a tile.
+  const auto score = [&](int tile, float16_t (&z)[2]) {
+    const char *kb = smem + (tile & 1) * kHalf + (G * 64 + n) * 16;
+#pragma unroll
+    for (int s = 0; s < Dp / 16; ++s) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        z[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(kb + (s * 128 + k * 32) * 16), q[s],
+                                                     s ? z[k] : none, 0, 0, 0);
+    }
+  };
 
+  float16_t z[2];
   if (tiles > 0) {
+    fetch(-1);  // keys of tile 0 (and values of none)
+    put(-1);
     fetch(0);
     put(0);
   }
   __syncthreads();
+  if (tiles > 0) score(0, z);
   for (int tile = 0; tile < tiles; ++tile) {
-    const int buf = tile & 1, t0 = c0 + tile * 64;
-    if (tile + 1 < tiles) fetch(tile + 1);
+    const int t0 = c0 + tile * 64;
+    fetch(tile + 1);
+    float16_t zn[2];
     if (t0 < some_last && t0 + 64 > some_first) {
-      const char *kb = smem + 2 * buf * kHalf, *vb = kb + kHalf;
-      const float *ksc = scales + 2 * buf * 4, *vsc = ksc + 4;
-      float big = 0.f;
+      const float4_t ks = *(const float4_t *)(scales + (tile & 3) * 4);
+      const float4_t vs = *(const float4_t *)(scales + 16 + (tile & 1) * 4);
       bool whole = t0 >= all_first && t0 + 64 <= all_last;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        big = fmaxf(big, vsc[i] < INFINITY ? vsc[i] : 0.f);
-        whole = whole && !(ksc[i] == -1.f);
-      }
-      if (big > r) {
-        const float g = r / big;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) O[i] *= g;
-        r = big;
-      }
-      float16_t z[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) z[k][j] = 0.f;
-      }
-#pragma unroll
-      for (int s = 0; s < Dp / 16; ++s) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          z[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(kb + ((2 * s + G) * 64 + k * 32 + n) * 16), q[s],
-                                                       z[k], 0, 0, 0);
-      }
-      float top = -INFINITY;
+      bool odd = false;  // a page without a finite scale
+      float big = kLeast;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float s = ksc[u];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v = z[u >> 1][8 * (u & 1) + j] * s;
-          if (!whole) {
-            const int t = t0 + 16 * u + 8 * (j >> 2) + 4 * G + (j & 3);
-            if (s == -1.f || t < first || t >= last) v = -INFINITY;
-          }
-          z[u >> 1][8 * (u & 1) + j] = v;
-          top = fmaxf(top, v);
-        }
+        whole = whole && ks[u] != kMissing;
+        odd = odd || ks[u] != ks[u] || vs[u] != vs[u];
+        if (vs[u] != kMissing) big = fmaxf(big, vs[u]);
       }
-      top = fmaxf(top, lane_xor(top, 32));
+      whole = __builtin_amdgcn_readfirstlane(whole);
+      odd = __builtin_amdgcn_readfirstlane(odd);
+      float top = -INFINITY;
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int t = t0 + 16 * u + 8 * (j >> 2) + 4 * G + (j & 3);
+            const bool in = ks[u] != kMissing && t >= first && t < last;
+            z[u >> 1][8 * (u & 1) + j] = in ? z[u >> 1][8 * (u & 1) + j] : -INFINITY;
+          }
+      }
+      float factor[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        factor[u] = ks[u] > 0.f ? ks[u] : 1.f;  // 1: missing, or not finite (see odd)
+        float t = z[u >> 1][8 * (u & 1)];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) t = fmaxf(t, z[u >> 1][8 * (u & 1) + j]);
+        top = fmaxf(top, t * factor[u]);
+      }
+      top = fmaxf(top, other32(top));
       const bool up = top > m + kSlack;
-      if (__any(up)) {
-        const float g = up ? exp2f(m - top) : 1.f;
+      if (__any(up || big > lr)) {
+        float g = up ? __builtin_amdgcn_exp2f(m - top) : 1.f;
         l *= g;
+        if (up) m = top;
+        big = fmaxf(big, lr);
+        g *= __builtin_amdgcn_exp2f(lr - big);
+        lr = big;
 #pragma unroll
         for (int i = 0; i < NT; ++i) O[i] *= g;
-        if (up) m = top;
       }
       const float ref = (m == -INFINITY ? 0.f : m) - kUp;
+      score(tile + 1, zn);
+      half8_t p8[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float g = vsc[u] == -1.f ? 0.f : vsc[u] / r;
-        half8_t p8;
+        // weight times scale: the scale's share in the exponent, and out again for l
+        const float c = vs[u] == kMissing ? 0.f : fmaxf(vs[u] - lr, -60.f), add = c - ref;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float v = z[u >> 1][8 * (u & 1) + j];
-          const float p = __builtin_amdgcn_exp2f(v - ref);
-          l += p;
-          p8[j] = (_Float16)(v == -INFINITY ? 0.f : p * g);
+          const float p = __builtin_amdgcn_exp2f(fmaf(z[u >> 1][8 * (u & 1) + j], factor[u], add));
+          if (j & 1)
+            s1 += p;
+          else
+            s0 += p;
+          p8[u][j] = (_Float16)p;
         }
+        l = fmaf(s0 + s1, __builtin_amdgcn_exp2f(-c), l);
+      }
+      if (odd) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (ks[u] != ks[u] || vs[u] != vs[u])
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (z[u >> 1][8 * (u & 1) + j] != -INFINITY) p8[u][j] = (_Float16)NAN;
+      }
+      const char *vb = smem + (2 + (tile & 1)) * kHalf + (G * Dp + n) * 16;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-          O[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(vb + ((u * 2 + G) * Dp + i * 32 + n) * 16), p8,
-                                                       O[i], 0, 0, 0);
-      }
+          O[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(vb + (u * 2 * Dp + i * 32) * 16), p8[u], O[i], 0,
+                                                       0, 0);
+    } else {
+      score(tile + 1, zn);
     }
-    if (tile + 1 < tiles) put(buf ^ 1);
+    // keys of tile + 2 in the place of tile's, values of tile + 1 in that of tile - 1's
+    put(tile + 1);
     __syncthreads();
+    z[0] = zn[0];
+    z[1] = zn[1];
   }
-  l += lane_xor(l, 32);
+  l += other32(l);
   if (w * 32 + n >= it.n) return;
+  const float r = __builtin_amdgcn_exp2f(lr);
   if (pieces == 1) {
     const float inv = (l > 0.f || l != l ? 1.f / l : 0.f) * r;
     uint16_t *to = A.out + row_at(A, it, myrow, A.ldo);
@@ -572,15 +624,21 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
 }
 
 // --------------------------------------------------------------- joining
-// The pieces of a row: a wave has one row, four dims a lane.  TR = 16: of
-// k_attend_few.
-template <int TR>
+// The pieces of a row, by NT threads: their weights first, then each group of
+// Dp / 4 threads adds up every so-manieth piece, and the groups meet in LDS.
+// TR = 16: of k_attend_few.  (One wave a row that went through the pieces in
+// turn took 127 us for 256 pieces of 64 rows of 128.)
+template <int TR, int NT>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
+  constexpr int kPer = 256 / NT, kMost = TR == 16 ? kFewPieces : 512;
+  __shared__ float weight[kPer][NT == 64 ? kJoinWave : kMost];
+  __shared__ float4_t sums[256];
+  __shared__ float wave[2][4];
   const int rows = TR == 16 ? A.frows : TR;  // of an item's partial sums
-  const int lane = threadIdx.x & 63;
-  const unsigned wv = blockIdx.x * 4 + wave_id();
-  const unsigned item = wv / (unsigned)rows;
-  const int row = (int)(wv - item * rows);
+  const int t = threadIdx.x % NT, mine = threadIdx.x / NT;
+  const unsigned at = blockIdx.x * kPer + (NT == 64 ? wave_id() : 0);
+  const unsigned item = at / (unsigned)rows;
+  const int row = (int)(at - item * rows);
   Item it;
   if constexpr (TR == 16) {
     if (item >= (unsigned)(A.S.n * A.KV * A.tiles) || !few_item(A, item, it)) return;
@@ -593,26 +651,76 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   if (pieces == 1 || row >= it.n) return;
   const int64_t size = (int64_t)rows * (Dp + 2);
   const float *part = A.part + (int64_t)item * A.pieces * size;
+  const float *ml = part + rows * Dp + row;
   float M = -INFINITY;
-  for (int p = lane; p < pieces; p += 64) M = fmaxf(M, part[p * size + rows * Dp + row]);
+  for (int p = t; p < pieces; p += NT) {
+    const float v = ml[p * size];
+    weight[mine][p] = v;
+    M = fmaxf(M, v);
+  }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
-  float4_t o = {0.f, 0.f, 0.f, 0.f};
-  float L = 0.f;
-  const int d = 4 * lane;
-  for (int p = 0; p < pieces; ++p) {
-    const float mv = part[p * size + rows * Dp + row];
-    const float f = mv == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mv - M);
-    L += part[p * size + rows * Dp + rows + row] * f;
-    if (d < Dp) o += *(const float4a_t *)(part + p * size + row * Dp + d) * f;
+  if constexpr (NT > 64) {
+    if ((t & 63) == 0) wave[0][t >> 6] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(wave[0][0], wave[0][1]), fmaxf(wave[0][2], wave[0][3]));
   }
-  if (d >= A.D) return;
+  float L = 0.f;
+  for (int p = t; p < pieces; p += NT) {
+    const float v = weight[mine][p];
+    // a piece that saw nothing has sums of 0 (or NaN, which is to stay)
+    const float f = v == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(v - M);
+    weight[mine][p] = f;
+    L += ml[p * size + rows] * f;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) L += lane_xor(L, d);
+  if constexpr (NT > 64) {
+    if ((t & 63) == 0) wave[1][t >> 6] = L;
+    __syncthreads();
+    L = wave[1][0] + wave[1][1] + wave[1][2] + wave[1][3];
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  const int per = Dp / 4, groups = NT / per, g = t / per, d = (t - g * per) * 4;
+  float4_t o = {0.f, 0.f, 0.f, 0.f};
+  if (g < groups) {
+    const float *from = part + row * Dp + d;
+    int p = g;
+    for (; p + 3 * groups < pieces; p += 4 * groups) {
+      float4_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *(const float4a_t *)(from + (p + i * groups) * size);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o += v[i] * weight[mine][p + i * groups];
+    }
+    for (; p < pieces; p += groups) o += *(const float4a_t *)(from + p * size) * weight[mine][p];
+  }
+  sums[threadIdx.x] = o;
+  if constexpr (NT > 64) {
+    __syncthreads();
+  } else {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (g > 0 || d >= A.D) return;
+  for (int i = 1; i < groups; ++i) o += sums[threadIdx.x + i * per];
   const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
   u32x2_t h;
   h[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
   h[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
   typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
   *(loose64 *)(uintptr_t)(A.out + row_at(A, it, it.r0 + row, A.ldo) + d) = h;
+}
+
+template <int TR>
+hipError_t launch_join(const AttendArgs &A, int64_t rows, int Dp, hipStream_t st) {
+  if (A.pieces <= kJoinWave)
+    k_attend_join<TR, 64><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(A, Dp);
+  else
+    k_attend_join<TR, 256><<<dim3((unsigned)rows), dim3(256), 0, st>>>(A, Dp);
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ host
@@ -656,20 +764,18 @@ hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
   k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(256), lds, st>>>(A);
   e = hipGetLastError();
   if (e != hipSuccess || p.few_pieces == 1) return e;
-  k_attend_join<16><<<dim3((unsigned)((p.few_items * p.frows + 3) / 4)), dim3(256), 0, st>>>(A, NC * 32);
-  return hipGetLastError();
+  return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
 }
 
 template <int NC>
 hipError_t launch_many(const AttendArgs &A, const Plan &p, hipStream_t st) {
-  constexpr int NW = NC <= 4 ? 8 : 4, lds = 4 * NC * 32 * 128 + 64;
+  constexpr int NW = NC <= 4 ? 8 : 4, lds = 4 * NC * 32 * 128 + 96;
   hipError_t e = allow_lds(k_attend_many<NC, NW>, lds);
   if (e != hipSuccess) return e;
   k_attend_many<NC, NW><<<dim3((unsigned)(p.many_items * p.many_pieces)), dim3(NW * 64), lds, st>>>(A);
   e = hipGetLastError();
   if (e != hipSuccess || p.many_pieces == 1) return e;
-  k_attend_join<NW * 32><<<dim3((unsigned)(p.many_items * (NW * 32) / 4)), dim3(256), 0, st>>>(A, NC * 32);
-  return hipGetLastError();
+  return launch_join<NW * 32>(A, p.many_items * (NW * 32), NC * 32, st);
 }
 
 // The chunk of 32 dims as a constant.
