@@ -40,12 +40,16 @@ using namespace lbi;
 
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef float4_t __attribute__((aligned(8))) float4a_t;
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr float kUp = 12.f, kSlack = 3.f;
+// The reference before there is one, below every score: e^(-inf - kNothing) is 0,
+// and so is the share of what has seen nothing in a sum with what has.
+constexpr float kNothing = -1e30f;
 // Of k_attend_many: the scale of a page that is not there, and the smallest
 // reference of the values' scales (all are above 2^-32).
 constexpr float kMissing = -1e9f, kLeast = -100.f;
@@ -93,6 +97,14 @@ __device__ __forceinline__ float lane_xor(float v, int d) { return __shfl_xor(v,
 __device__ __forceinline__ float other16(float v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(threadIdx.x & 16 ? r[0] : r[1]);
+}
+__device__ __forceinline__ float max32(float v) {  // of a lane and that one
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 __device__ __forceinline__ float other32(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -178,7 +190,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   float4_t O[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) O[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f, r = 1e-30f;
+  float m = kNothing, l = 0.f, r = 1e-30f;
 
   const int upp = 1 << (A.lg - 4);
   struct Frag {
@@ -246,9 +258,8 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
           top = fmaxf(top, z[4 * i + j]);
         }
       }
-      top = fmaxf(top, other16(top));
-      top = fmaxf(top, other32(top));
-      const bool up = top > m + kSlack;  // also the first finite one: m is -inf
+      top = max32(max16(top));
+      const bool up = top > m + kSlack;
       if (__any(up)) {
         const float f = up ? exp2f(m - top) : 1.f;
         l *= f;
@@ -256,7 +267,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
         for (int i = 0; i < NT; ++i) O[i] *= f;
         if (up) m = top;
       }
-      const float ref = (m == -INFINITY ? 0.f : m) - kUp;
+      const float ref = m - kUp;
       half8_t ph, pl;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -319,10 +330,9 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
     float L = 0.f;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float mv = sm[v * 16 + row], f = mv == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mv - M);
-      // a wave that saw nothing adds nothing (m may also be -inf beside a NaN sum)
-      o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * (mv == -INFINITY ? 1.f : f);
-      L += sl[v * 16 + row] * (mv == -INFINITY ? 1.f : f);
+      const float f = __builtin_amdgcn_exp2f(sm[v * 16 + row] - M);
+      o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * f;
+      L += sl[v * 16 + row] * f;
     }
     if (pieces == 1) {
       if (d >= A.D) continue;
@@ -343,18 +353,30 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   }
 }
 
+// Nothing but an order: v is computed before what comes after.  (No
+// instruction reads it here, so a matrix instruction's result needs no wait.)
+template <typename T>
+__device__ __forceinline__ void here(const T &v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" ::"v"(v));
+#endif
+}
+
 // ------------------------------------------------------------ many rows
 // 32 rows a wave, NW waves a workgroup; tiles of 64 keys and values go through
 // LDS as fp16 operands (converted once for all waves), the bytes of a later tile
-// on their way meanwhile.  A step weighs and adds up tile t (exponentials, then
-// the second product) while the matrix cores have the first product of tile
-// t + 1, so keys are staged a tile ahead of values.
+// on their way meanwhile.  A step weighs and adds up half a tile, h (exponentials,
+// then the second product), while the matrix cores have the first product of half
+// h + 1.  Between two barriers (tile t) the waves read keys of halves 2 t + 1 and
+// 2 t + 2 and values of halves 2 t and 2 t + 1, and write keys of the two halves
+// behind and values of tile t + 1: there is room for four halves of keys and two
+// tiles of values, so nothing is written that a slower wave may still read.
 template <int NC, int NW>
 __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = NC, TR = NW * 32;
   constexpr int kHalf = Dp * 128;  // bytes of a tile's keys, or values
-  // [2] tiles of keys, [2] of values, then scales: of keys [4][4] (read a step
-  // after the keys themselves, while those of two tiles on are written), of values [2][4]
+  // [4] halves of keys, [2] tiles of values, then scales: of keys [8][2] (read a
+  // step after the keys themselves), of values [2][4]
   extern __shared__ char smem[];
   float *scales = (float *)(smem + 4 * kHalf);
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 31, G = lane >> 5;
@@ -397,9 +419,8 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) O[i][j] = 0.f;
-  float m = -INFINITY, l = 0.f, lr = kLeast;
+  float m = kNothing, l = 0.f, lr = kLeast;
 
-  const int upp = 1 << (A.lg - 4);
   // staging: NW = 8: waves 0..3 have the tile's units of keys, 4..7 of values;
   // NW = 4: wave w has unit w of both
   constexpr int kKinds = NW == 8 ? 1 : 2;
@@ -411,15 +432,26 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   };
   Frag f[kKinds];
   const auto is_values = [&](int i) { return NW == 8 ? w >= 4 : i == 1; };
-  // Requests tile `tile` of values and the one behind it of keys.
-  const auto fetch = [&](int tile) {
+  // Requests tile `tile` of values and halves 2 tile + 1, 2 tile + 2 of keys; their pages
+  // were looked up a step before (a look-up and its wait in the same step took a
+  // tenth of the step).
+  const int *table = A.S.table + b * A.S.ldt;
+  const int upp = 1 << (A.lg - 4);
+  const auto look_up = [&](int tile, int (&page)[kKinds]) {
+#pragma unroll
+    for (int i = 0; i < kKinds; ++i) {
+      const int tok = c0 + tile * 64 + (is_values(i) ? 0 : 32) + su * 16;
+      page[i] = -1;
+      if (tok >= c0 && tok < c1) page[i] = table[tok >> A.lg];  // c1 is inside the table
+    }
+  };
+  const auto fetch = [&](int tile, const int (&page)[kKinds]) {
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
       const bool values = is_values(i);
-      const int tok = c0 + (tile + (values ? 0 : 1)) * 64 + su * 16;
-      const int page = tok >= c0 && tok < c1 ? page_of(A.S, b, tok >> A.lg) : -1;
-      const bool there = page >= 0;
-      const int blk = (there ? page : 0) * A.KV + it.h;
+      const int tok = c0 + tile * 64 + (values ? 0 : 32) + su * 16;
+      const bool there = page[i] >= 0 && page[i] < A.S.pages;
+      const int blk = (there ? page[i] : 0) * A.KV + it.h;
       const int unit = blk * upp + ((tok >> 4) & (upp - 1));
       const uint8_t *p = (values ? A.vc : A.kc) + (int64_t)unit * kUnit;
 #pragma unroll
@@ -436,24 +468,25 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
       const bool values = is_values(i);
-      const int buf = (tile + (values ? 0 : 1)) & 1;
-      char *to = smem + (2 * (values ? 1 : 0) + buf) * kHalf;
+      const int part = 2 * tile + 1 + (su >> 1);  // of keys
+      char *to = smem + (values ? (2 + (tile & 1)) * kHalf : (part & 3) * (kHalf / 2));
       if (lane == 0) {
         // Keys: the factor of a score, tiny instead of 0 (of a page of zeros, whose
         // scores are 0) so that it keeps a masked -inf.  Values: log2 of the scale.
         float v = f[i].scale;
         if (v != kMissing) v = values ? __log2f(v) : v * A.qscale == 0.f ? 1e-30f : v * A.qscale;
-        scales[(values ? 16 + buf * 4 : ((tile + 1) & 3) * 4) + su] = v;
+        scales[values ? 16 + (tile & 1) * 4 + su : (part & 7) * 2 + (su & 1)] = v;
       }
       if (!values) {
-        // [dim / 8][key 64][8]
+        // [dim / 8][key 32][8]
+        to += ((su & 1) * 16 + x) * 16;
 #pragma unroll
         for (int c = 0; c < kPairs; ++c) {
-          *(half8_t *)(to + ((8 * c + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].pair[c][0], f[i].pair[c][1]);
-          *(half8_t *)(to + ((8 * c + 4 + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].pair[c][2], f[i].pair[c][3]);
+          *(half8_t *)(to + (8 * c + g) * 512) = to_half8(f[i].pair[c][0], f[i].pair[c][1]);
+          *(half8_t *)(to + (8 * c + 4 + g) * 512) = to_half8(f[i].pair[c][2], f[i].pair[c][3]);
         }
         if constexpr (kOdd)
-          *(half8_t *)(to + ((8 * kPairs + g) * 64 + su * 16 + x) * 16) = to_half8(f[i].odd[0], f[i].odd[1]);
+          *(half8_t *)(to + (8 * kPairs + g) * 512) = to_half8(f[i].odd[0], f[i].odd[1]);
       } else {
         // [unit 4][half 2][dim][keys 4 half + 0..3, 8 + 4 half + 0..3]
         const auto half4 = [&](uint32_t word, int d) {
@@ -474,119 +507,145 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
     }
   };
   const float16_t none = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  // The first product of a tile.
-  const auto score = [&](int tile, float16_t (&z)[2]) {
-    const char *kb = smem + (tile & 1) * kHalf + (G * 64 + n) * 16;
+  // Operands of a step: those of the next half's first product (keys, 16 dims
+  // each), then those of this half's second (values, 16 keys and 32 dims each).
+  // They are read from LDS kAhead matrix instructions before their use.
+  constexpr int kSteps = Dp / 16, kAhead = NC > 1 ? 4 : 2;
+  const auto operand = [&](const char *kb, const char *vb, int i) {
+    if (i < kSteps) return *(const half8_t *)(kb + i * 1024);
+    i -= kSteps;
+    return *(const half8_t *)(vb + (i / NT * 2 * Dp + i % NT * 32) * 16);
+  };
+  const auto keys_at = [&](int part) { return smem + (part & 3) * (kHalf / 2) + lane * 16; };
+  // The first product of half a tile (32 keys) alone.
+  const auto score = [&](int part) {
+    const char *kb = keys_at(part);
+    float16_t z = none;
 #pragma unroll
-    for (int s = 0; s < Dp / 16; ++s) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        z[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(kb + (s * 128 + k * 32) * 16), q[s],
-                                                     s ? z[k] : none, 0, 0, 0);
-    }
+    for (int s = 0; s < kSteps; ++s)
+      z = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(kb + s * 1024), q[s], z, 0, 0, 0);
+    return z;
   };
 
-  float16_t z[2];
+  // Weighs the scores z of half a tile and adds up its values; returns the next
+  // half's scores.
+  const auto step = [&](int tile, int half, float16_t z) {
+    const int t0 = c0 + tile * 64 + half * 32, part = 2 * tile + half;
+    if (t0 >= some_last || t0 + 32 <= some_first) return score(part + 1);
+    const char *kb = keys_at(part + 1), *vb = smem + (2 + (tile & 1)) * kHalf + ((half * 4 + G) * Dp + n) * 16;
+    half8_t ring[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ring[i] = operand(kb, vb, i);
+    const float2_t ks = *(const float2_t *)(scales + (part & 7) * 2);
+    const float2_t vs = *(const float2_t *)(scales + 16 + (tile & 1) * 4 + half * 2);
+    // Units that are missing or have no finite scale are rare: the rest of the step
+    // gets stand-ins for their scales.
+    float2_t factor = ks, share = vs;
+    const bool usual = t0 >= all_first && t0 + 32 <= all_last && !__any(!(ks[0] > 0.f && ks[1] > 0.f && vs[0] > kMissing && vs[1] > kMissing));
+    bool odd = false;
+    if (!usual) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        odd = odd || ks[u] != ks[u] || vs[u] != vs[u];
+        if (!(ks[u] > 0.f)) factor[u] = 1.f;
+        if (!(vs[u] > kMissing)) share[u] = lr;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = t0 + 16 * u + 8 * (j >> 2) + 4 * G + (j & 3);
+          const bool in = ks[u] != kMissing && t >= first && t < last;
+          z[8 * u + j] = in ? z[8 * u + j] : -INFINITY;
+        }
+      }
+      odd = __any(odd);
+    }
+    float top[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      top[u] = z[8 * u];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top[u] = fmaxf(top[u], z[8 * u + j]);
+    }
+    const float best = max32(fmaxf(top[0] * factor[0], top[1] * factor[1]));
+    const float big = fmaxf(lr, fmaxf(share[0], share[1]));
+    const bool up = best > m + kSlack;
+    if (__any(up || big > lr)) {
+      float g = up ? __builtin_amdgcn_exp2f(m - best) : 1.f;
+      l *= g;
+      if (up) m = best;
+      g *= __builtin_amdgcn_exp2f(lr - big);
+      lr = big;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) O[i] *= g;
+    }
+    // weight times scale: the scale's share in the exponent, and out again for l
+    float add[2], sums[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      share[u] = fmaxf(share[u] - lr, -60.f);
+      add[u] = share[u] - (m - kUp);
+    }
+    half8_t p8[2];
+    float16_t zn = none;
+    // The order is fixed: exponentials after each matrix instruction, in whose time
+    // they run.  Left alone, the compiler puts all of the one before all of the other.
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      zn = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[s % kAhead], q[s], zn, 0, 0, 0);
+      here(zn);
+      if (s + kAhead < 2 * kSteps) ring[s % kAhead] = operand(kb, vb, s + kAhead);
+#pragma unroll
+      for (int e = 2 * (s * 8 / kSteps); e < 2 * ((s + 1) * 8 / kSteps); e += 2) {
+        const int u = e >> 3, j = e & 7;
+        const float pa = __builtin_amdgcn_exp2f(fmaf(z[e], factor[u], add[u]));
+        const float pb = __builtin_amdgcn_exp2f(fmaf(z[e + 1], factor[u], add[u]));
+        sums[u][0] = j ? sums[u][0] + pa : pa;
+        sums[u][1] = j ? sums[u][1] + pb : pb;
+        p8[u][j] = (_Float16)pa;
+        p8[u][j + 1] = (_Float16)pb;
+        here(half2_t{p8[u][j], p8[u][j + 1]});
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) l = fmaf(sums[u][0] + sums[u][1], __builtin_amdgcn_exp2f(-share[u]), l);
+    if (odd) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (ks[u] != ks[u] || vs[u] != vs[u])
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (z[8 * u + j] != -INFINITY) p8[u][j] = (_Float16)NAN;
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      O[i % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[(kSteps + i) % kAhead], p8[i / NT], O[i % NT], 0, 0, 0);
+      if (i + kAhead < kSteps) ring[(kSteps + i) % kAhead] = operand(kb, vb, kSteps + i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    return zn;
+  };
+
+  float16_t z = none;
+  int page[kKinds];
   if (tiles > 0) {
-    fetch(-1);  // keys of tile 0 (and values of none)
+    int p0[kKinds];
+    look_up(-1, p0);
+    look_up(0, page);
+    fetch(-1, p0);  // keys of half 0 (and values of none)
     put(-1);
-    fetch(0);
+    fetch(0, page);
+    look_up(1, page);
     put(0);
   }
   __syncthreads();
-  if (tiles > 0) score(0, z);
+  if (tiles > 0) z = score(0);
   for (int tile = 0; tile < tiles; ++tile) {
-    const int t0 = c0 + tile * 64;
-    fetch(tile + 1);
-    float16_t zn[2];
-    if (t0 < some_last && t0 + 64 > some_first) {
-      const float4_t ks = *(const float4_t *)(scales + (tile & 3) * 4);
-      const float4_t vs = *(const float4_t *)(scales + 16 + (tile & 1) * 4);
-      bool whole = t0 >= all_first && t0 + 64 <= all_last;
-      bool odd = false;  // a page without a finite scale
-      float big = kLeast;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        whole = whole && ks[u] != kMissing;
-        odd = odd || ks[u] != ks[u] || vs[u] != vs[u];
-        if (vs[u] != kMissing) big = fmaxf(big, vs[u]);
-      }
-      whole = __builtin_amdgcn_readfirstlane(whole);
-      odd = __builtin_amdgcn_readfirstlane(odd);
-      float top = -INFINITY;
-      if (!whole) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int t = t0 + 16 * u + 8 * (j >> 2) + 4 * G + (j & 3);
-            const bool in = ks[u] != kMissing && t >= first && t < last;
-            z[u >> 1][8 * (u & 1) + j] = in ? z[u >> 1][8 * (u & 1) + j] : -INFINITY;
-          }
-      }
-      float factor[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        factor[u] = ks[u] > 0.f ? ks[u] : 1.f;  // 1: missing, or not finite (see odd)
-        float t = z[u >> 1][8 * (u & 1)];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) t = fmaxf(t, z[u >> 1][8 * (u & 1) + j]);
-        top = fmaxf(top, t * factor[u]);
-      }
-      top = fmaxf(top, other32(top));
-      const bool up = top > m + kSlack;
-      if (__any(up || big > lr)) {
-        float g = up ? __builtin_amdgcn_exp2f(m - top) : 1.f;
-        l *= g;
-        if (up) m = top;
-        big = fmaxf(big, lr);
-        g *= __builtin_amdgcn_exp2f(lr - big);
-        lr = big;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) O[i] *= g;
-      }
-      const float ref = (m == -INFINITY ? 0.f : m) - kUp;
-      score(tile + 1, zn);
-      half8_t p8[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        // weight times scale: the scale's share in the exponent, and out again for l
-        const float c = vs[u] == kMissing ? 0.f : fmaxf(vs[u] - lr, -60.f), add = c - ref;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(z[u >> 1][8 * (u & 1) + j], factor[u], add));
-          if (j & 1)
-            s1 += p;
-          else
-            s0 += p;
-          p8[u][j] = (_Float16)p;
-        }
-        l = fmaf(s0 + s1, __builtin_amdgcn_exp2f(-c), l);
-      }
-      if (odd) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (ks[u] != ks[u] || vs[u] != vs[u])
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (z[u >> 1][8 * (u & 1) + j] != -INFINITY) p8[u][j] = (_Float16)NAN;
-      }
-      const char *vb = smem + (2 + (tile & 1)) * kHalf + (G * Dp + n) * 16;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          O[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8_t *)(vb + (u * 2 * Dp + i * 32) * 16), p8[u], O[i], 0,
-                                                       0, 0);
-    } else {
-      score(tile + 1, zn);
-    }
-    // keys of tile + 2 in the place of tile's, values of tile + 1 in that of tile - 1's
+    fetch(tile + 1, page);
+    look_up(tile + 2, page);
+    z = step(tile, 0, z);
+    z = step(tile, 1, z);
     put(tile + 1);
     __syncthreads();
-    z[0] = zn[0];
-    z[1] = zn[1];
   }
   l += other32(l);
   if (w * 32 + n >= it.n) return;
@@ -652,7 +711,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   const int64_t size = (int64_t)rows * (Dp + 2);
   const float *part = A.part + (int64_t)item * A.pieces * size;
   const float *ml = part + rows * Dp + row;
-  float M = -INFINITY;
+  float M = kNothing;
   for (int p = t; p < pieces; p += NT) {
     const float v = ml[p * size];
     weight[mine][p] = v;
@@ -667,9 +726,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   }
   float L = 0.f;
   for (int p = t; p < pieces; p += NT) {
-    const float v = weight[mine][p];
-    // a piece that saw nothing has sums of 0 (or NaN, which is to stay)
-    const float f = v == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(v - M);
+    const float f = __builtin_amdgcn_exp2f(weight[mine][p] - M);
     weight[mine][p] = f;
     L += ml[p * size + rows] * f;
   }
