@@ -636,15 +636,19 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
     fetch(0, page);
     look_up(1, page);
     put(0);
+    fetch(1, page);
+    look_up(2, page);
   }
   __syncthreads();
   if (tiles > 0) z = score(0);
   for (int tile = 0; tile < tiles; ++tile) {
-    fetch(tile + 1, page);
-    look_up(tile + 2, page);
     z = step(tile, 0, z);
-    z = step(tile, 1, z);
+    // here rather than before the barrier, so that one wave's conversions run
+    // beside another's matrix instructions
     put(tile + 1);
+    fetch(tile + 2, page);
+    look_up(tile + 3, page);
+    z = step(tile, 1, z);
     __syncthreads();
   }
   l += other32(l);
