@@ -53,6 +53,11 @@ constexpr float kNothing = -1e30f;
 // Of k_attend_many: the scale of a page that is not there, and the smallest
 // reference of the values' scales (all are above 2^-32).
 constexpr float kMissing = -1e9f, kLeast = -100.f;
+constexpr int kJoinHere = 64;  // pieces up to which the last workgroup of k_attend_few to arrive joins them
+// LDS of k_attend_few: the waves' sums, or the weights of the pieces.
+__host__ __device__ constexpr int few_floats(int rows, int Dp) {
+  return 4 * rows * (Dp + 4) > 2 * kJoinHere * 16 ? 4 * rows * (Dp + 4) : 2 * kJoinHere * 16;
+}
 constexpr int kJoinWave = 8;  // pieces of a row up to which a wave joins it, not a workgroup
 
 struct AttendArgs {
@@ -62,7 +67,8 @@ struct AttendArgs {
   int64_t ldq, ldo;
   const uint8_t *kc, *vc;
   const float *ks, *vs;
-  float *part;  // partial sums of the pieces: per item, piece and row Dp sums, then m and l
+  float *part;      // partial sums of the pieces: per item and piece rows x Dp sums, then m and l of each row
+  unsigned *count;  // arrivals at each item of k_attend_few, 0 between launches; NULL: k_attend_join does it
   float qscale;  // scale * log2 e
   int KV, D, lg;
   View view;
@@ -155,6 +161,34 @@ __device__ __forceinline__ half8_t load_q(const AttendArgs &A, int64_t at, int d
   u32x4_t w = {0, 0, 0, 0};
   if (d < A.D) w = *LB_LOOSE128(A.q + at + d);
   return __builtin_bit_cast(half8_t, w);
+}
+
+// Four of a row's outputs, from its sum and weights.
+__device__ __forceinline__ void write4(const AttendArgs &A, const Item &it, int row, int d, float4_t o, float L) {
+  if (d >= A.D) return;
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+  u32x2_t h;
+  h[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
+  h[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
+  typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
+  *(loose64 *)(uintptr_t)(A.out + row_at(A, it, it.r0 + row, A.ldo) + d) = h;
+}
+
+// Numbers for and from workgroups elsewhere on the GPU: past this CU's and XCD's caches.
+__device__ __forceinline__ void store2(float *p, float a, float b) {
+  __hip_atomic_store((unsigned long long *)p, __builtin_bit_cast(unsigned long long, float2_t{a, b}), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2_t load2(const float *p) {
+  return __builtin_bit_cast(float2_t, __hip_atomic_load((unsigned long long *)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void store4(float *p, float4_t v) {
+  store2(p, v[0], v[1]);
+  store2(p + 2, v[2], v[3]);
+}
+__device__ __forceinline__ float4_t load4(const float *p) {
+  const float2_t a = load2(p), b = load2(p + 2);
+  return float4_t{a[0], a[1], b[0], b[1]};
 }
 
 // ------------------------------------------------------------- few rows
@@ -310,7 +344,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   // the four waves' sums, in units of 1
   constexpr int kPitch = Dp + 4;
   const int rows = A.frows;
-  float *sm = sh + 4 * rows * kPitch, *sl = sm + 64;
+  float *sm = sh + few_floats(rows, Dp), *sl = sm + 64;
   if (n < it.n) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) *(float4_t *)(sh + (w * rows + n) * kPitch + 16 * i + 4 * G) = O[i] * r;
@@ -334,22 +368,72 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
       o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * f;
       L += sl[v * 16 + row] * f;
     }
-    if (pieces == 1) {
-      if (d >= A.D) continue;
-      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-      u32x2_t o2;
-      o2[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
-      o2[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
-      uint16_t *to = A.out + row_at(A, it, it.r0 + row, A.ldo) + d;
-      typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
-      *(loose64 *)(uintptr_t)to = o2;
+    if (pieces == 1)
+      write4(A, it, row, d, o, L);
+    else if (A.count) {
+      store4(part + row * Dp + d, o);
+      if (d == 0) store2(part + rows * Dp + 2 * row, M, L);
     } else {
       *(float4a_t *)(part + row * Dp + d) = o;
-      if (d == 0) {
-        part[rows * Dp + row] = M;
-        part[rows * Dp + rows + row] = L;
-      }
+      if (d == 0) *(float2_t *)(part + rows * Dp + 2 * row) = float2_t{M, L};
     }
+  }
+  if (pieces == 1 || !A.count) return;
+
+  // The item's last workgroup to arrive joins its pieces (a launch of its own for
+  // that took 4 to 6 us more).  Partial sums go past the caches, every wave's before
+  // the workgroup counts itself, and are read the same way.
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  int *flag = (int *)(sl + 64);
+  if (threadIdx.x == 0) {
+    const unsigned before = __hip_atomic_fetch_add(A.count + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *flag = before == (unsigned)pieces - 1;
+    if (*flag) __hip_atomic_store(A.count + slot, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!*flag) return;
+  const int64_t size = (int64_t)rows * (Dp + 2);
+  const float *all = A.part + (int64_t)slot * A.pieces * size;
+  float *wm = sh, *wl = sh + kJoinHere * 16;  // [piece][16]; the sums of the waves are no longer needed
+  for (int i = threadIdx.x; i < pieces * 16; i += 256) {
+    const int row = i & 15;
+    float2_t ml = {kNothing, 0.f};
+    if (row < it.n) ml = load2(all + (i >> 4) * size + rows * Dp + 2 * row);
+    wm[i] = ml[0];
+    wl[i] = ml[1];
+  }
+  __syncthreads();
+  {
+    const int row = threadIdx.x >> 4, p0 = threadIdx.x & 15;
+    float M = kNothing, L = 0.f;
+    for (int p = p0; p < pieces; p += 16) M = fmaxf(M, wm[p * 16 + row]);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
+    for (int p = p0; p < pieces; p += 16) {
+      const float f = __builtin_amdgcn_exp2f(wm[p * 16 + row] - M);
+      wm[p * 16 + row] = f;
+      L += wl[p * 16 + row] * f;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) L += lane_xor(L, d);
+    if (p0 == 0) wl[row] = L;  // (piece 0's, read by this row's threads alone, before)
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += 256) {
+    const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
+    const float *from = all + row * Dp + d;
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
+    int p = 0;
+    for (; p + 7 < pieces; p += 8) {
+      float4_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = load4(from + (p + j) * size);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o += v[j] * wm[(p + j) * 16 + row];
+    }
+    for (; p < pieces; ++p) o += load4(from + p * size) * wm[p * 16 + row];
+    write4(A, it, row, d, o, wl[row]);
   }
 }
 
@@ -681,8 +765,8 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
       *(float4a_t *)(part + row * Dp + i * 32 + 8 * j + 4 * G) = o * r;
     }
   if (G == 0) {
-    part[TR * Dp + row] = m;
-    part[TR * Dp + TR + row] = l;
+    part[TR * Dp + 2 * row] = m;
+    part[TR * Dp + 2 * row + 1] = l;
   }
 }
 
@@ -714,7 +798,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   if (pieces == 1 || row >= it.n) return;
   const int64_t size = (int64_t)rows * (Dp + 2);
   const float *part = A.part + (int64_t)item * A.pieces * size;
-  const float *ml = part + rows * Dp + row;
+  const float *ml = part + rows * Dp + 2 * row;
   float M = kNothing;
   for (int p = t; p < pieces; p += NT) {
     const float v = ml[p * size];
@@ -732,7 +816,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   for (int p = t; p < pieces; p += NT) {
     const float f = __builtin_amdgcn_exp2f(weight[mine][p] - M);
     weight[mine][p] = f;
-    L += ml[p * size + rows] * f;
+    L += ml[p * size + 1] * f;
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) L += lane_xor(L, d);
@@ -765,14 +849,9 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
-  if (g > 0 || d >= A.D) return;
+  if (g > 0) return;
   for (int i = 1; i < groups; ++i) o += sums[threadIdx.x + i * per];
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-  u32x2_t h;
-  h[0] = f2h(o[0] * inv) | (f2h(o[1] * inv) << 16);
-  h[1] = f2h(o[2] * inv) | (f2h(o[3] * inv) << 16);
-  typedef u32x2_t __attribute__((aligned(2), address_space(1))) loose64;
-  *(loose64 *)(uintptr_t)(A.out + row_at(A, it, it.r0 + row, A.ldo) + d) = h;
+  write4(A, it, row, d, o, L);
 }
 
 template <int TR>
@@ -785,8 +864,14 @@ hipError_t launch_join(const AttendArgs &A, int64_t rows, int Dp, hipStream_t st
 }
 
 // ------------------------------------------------------------------ host
+// The workspace begins with the counts of arrivals, which every launch leaves 0.
+constexpr size_t kCountBytes = (size_t)kFewPieces * 4;
+__global__ void k_attend_clear(unsigned *count) {
+  for (int i = threadIdx.x; i < kFewPieces; i += blockDim.x) count[i] = 0;
+}
+
 lb_status grow(lb_cache *C, size_t need, const char *who, bool in_call, hipStream_t st) {
-  if (need <= C->ws_bytes) return LB_OK;
+  if (need == 0 || need <= C->ws_bytes) return LB_OK;
   const std::string pre = std::string(who) + ": ";
   if (in_call) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -797,8 +882,16 @@ lb_status grow(lb_cache *C, size_t need, const char *who, bool in_call, hipStrea
                                            "lb_cache_reserve first");
   }
   void *t = nullptr;
-  const hipError_t e = hipMalloc(&t, need);
+  hipError_t e = hipMalloc(&t, kCountBytes + need);
   if (e != hipSuccess) return set_error(LB_ENOMEM, pre + "hipMalloc: " + hipGetErrorString(e));
+  k_attend_clear<<<dim3(1), dim3(1024), 0, st>>>((unsigned *)t);
+  e = hipGetLastError();
+  // (a reservation's later calls may be on any stream)
+  if (e == hipSuccess && !in_call) e = hipStreamSynchronize(st);
+  if (e != hipSuccess) {
+    (void)hipFree(t);
+    return set_error(LB_EHIP, pre + hipGetErrorString(e));
+  }
   if (C->ws) {
     try {
       C->retired.push_back(C->ws);
@@ -819,12 +912,12 @@ hipError_t allow_lds(F f, int bytes) {
 
 template <int NC>
 hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
-  const int lds = (4 * p.frows * (NC * 32 + 4) + 128) * 4;
+  const int lds = (few_floats(p.frows, NC * 32) + 132) * 4;
   hipError_t e = allow_lds(k_attend_few<NC>, lds);
   if (e != hipSuccess) return e;
   k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(256), lds, st>>>(A);
   e = hipGetLastError();
-  if (e != hipSuccess || p.few_pieces == 1) return e;
+  if (e != hipSuccess || p.few_pieces == 1 || A.count) return e;
   return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
 }
 
@@ -914,7 +1007,7 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   A.out = (uint16_t *)out;
   A.ldq = ldq; A.ldo = ldo;
   A.kc = C->k; A.vc = C->v; A.ks = C->ks; A.vs = C->vs;
-  A.part = (float *)C->ws;
+  A.part = (float *)((char *)C->ws + kCountBytes);
   A.qscale = scale * 1.44269504088896340736f;
   A.KV = C->KV; A.D = C->D; A.lg = C->lg;
   A.view = view;
@@ -927,6 +1020,7 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
     AttendArgs F = A;
     F.chunk = p.few_chunk;
     F.pieces = p.few_pieces;
+    if (p.few_pieces > 1 && p.few_pieces <= kJoinHere) F.count = (unsigned *)C->ws;
     e = with_dims(C->Dp, [&](auto nc) { return launch_few<decltype(nc)::value>(F, p, stm); });
   }
   if (e == hipSuccess && p.many) {

@@ -114,7 +114,7 @@ struct Plan {
 
 constexpr int kFewChunk = 256;    // keys of the smallest piece of k_attend_few
 constexpr int kManyChunk = 512;   // and of k_attend_many
-constexpr int kFewPieces = 2048;  // pieces that a call of k_attend_few has, if it has fewer items
+constexpr int kFewPieces = 1024;  // pieces that a call of k_attend_few has, if it has fewer items
 
 inline int many_tile(int Dp) { return Dp <= 128 ? 256 : 128; }
 
