@@ -53,10 +53,11 @@ constexpr float kNothing = -1e30f;
 // Of k_attend_many: the scale of a page that is not there, and the smallest
 // reference of the values' scales (all are above 2^-32).
 constexpr float kMissing = -1e9f, kLeast = -100.f;
+constexpr int kFewWaves = 8;   // of a workgroup of k_attend_few
 constexpr int kJoinHere = 64;  // pieces up to which the last workgroup of k_attend_few to arrive joins them
 // LDS of k_attend_few: the waves' sums, or the weights of the pieces.
 __host__ __device__ constexpr int few_floats(int rows, int Dp) {
-  return 4 * rows * (Dp + 4) > 2 * kJoinHere * 16 ? 4 * rows * (Dp + 4) : 2 * kJoinHere * 16;
+  return kFewWaves * rows * (Dp + 4) > 2 * kJoinHere * 16 ? kFewWaves * rows * (Dp + 4) : 2 * kJoinHere * 16;
 }
 constexpr int kJoinWave = 8;  // pieces of a row up to which a wave joins it, not a workgroup
 
@@ -192,12 +193,12 @@ __device__ __forceinline__ float4_t load4(const float *p) {
 }
 
 // ------------------------------------------------------------- few rows
-// 16 rows a workgroup, four waves that share out the keys of a piece and read
-// them from memory straight into operands; the waves' sums are joined in LDS.
+// 16 rows a workgroup, whose waves share out the keys of a piece and read them
+// from memory straight into operands; the waves' sums are joined in LDS.
 template <int NC>
-__global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
+__global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(AttendArgs A) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = Dp / 16;
-  extern __shared__ float sh[];  // [4][rows][Dp + 4], then m and l [4][16] each
+  extern __shared__ float sh[];  // [waves][rows][Dp + 4], then m and l [waves][16] each
   const unsigned slot = blockIdx.x / (unsigned)A.pieces;
   const int piece = (int)(blockIdx.x - slot * A.pieces);
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 15, G = lane >> 4;
@@ -208,12 +209,20 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   const int b = (int)(slot / (unsigned)(A.tiles * A.KV));
   const int c0 = it.lo + piece * A.chunk, c1 = min(it.hi, c0 + A.chunk);
   // the wave's units of 16 keys, an even number before the last
-  const int units = (c1 - c0 + 15) >> 4, per = ((units + 7) >> 3) * 2;
+  const int units = (c1 - c0 + 15) >> 4, per = (units + 2 * kFewWaves - 1) / (2 * kFewWaves) * 2;
   const int u0 = (c0 >> 4) + min(units, w * per), u1 = (c0 >> 4) + min(units, w * per + per);
   const int myrow = it.r0 + min(n, it.n - 1);
   int first, last;
   keys_of_row(A.view, it.q, myrow, &first, &last);
   last = min(last, c1);
+  int all_first, all_last;  // the keys that all rows see
+  {
+    int unused;
+    keys_of_row(A.view, it.q, it.r0, &unused, &all_last);
+    keys_of_row(A.view, it.q, it.r0 + it.n - 1, &all_first, &unused);
+    all_first = __builtin_amdgcn_readfirstlane(all_first);
+    all_last = __builtin_amdgcn_readfirstlane(min(all_last, c1));
+  }
 
   half8_t q[NC];
   {
@@ -269,8 +278,11 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
       // the next step's units, this one's again behind the last
       const int n0 = __builtin_amdgcn_readlane(mine, min(2 * st + 2, 2 * steps - 2));
       const int n1 = __builtin_amdgcn_readlane(mine, min(2 * st + 3, 2 * steps - 1));
-      float z[8];
-      float top = -INFINITY;
+      const int t0 = (ub + 2 * st) * 16;
+      const unsigned both = (unsigned)(ok >> (2 * st)) & 3u;
+      const bool usual = both == 3u && t0 >= all_first && t0 + 32 <= all_last;
+      float4_t z[2];
+      float factor[2], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float4_t acc = {0.f, 0.f, 0.f, 0.f};
@@ -282,14 +294,24 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
         if constexpr (kOdd)
           acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_half8(K[i].odd[0], K[i].odd[1]), q[NC - 1], acc, 0, 0, 0);
         load(A.kc, i ? n1 : n0, K[i]);
-        const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * st + i));
-        const bool have = (ok >> (2 * st + i)) & 1;
-        const int t0 = (ub + 2 * st + i) * 16 + 4 * G;
+        factor[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 2 * st + i));
+        z[i] = acc;
+      }
+      if (usual) {  // the scale (not negative) goes into the exponent's multiply-add
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = have && t0 + j >= first && t0 + j < last;
-          z[4 * i + j] = in ? acc[j] * s : -INFINITY;
-          top = fmaxf(top, z[4 * i + j]);
+        for (int i = 0; i < 2; ++i)
+          top = fmaxf(top, fmaxf(fmaxf(z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3])) * factor[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = t0 + 16 * i + 4 * G + j;
+            const bool in = ((both >> i) & 1u) && t >= first && t < last;
+            z[i][j] = in ? z[i][j] * factor[i] : -INFINITY;
+            top = fmaxf(top, z[i][j]);
+          }
+          factor[i] = 1.f;
         }
       }
       top = max32(max16(top));
@@ -308,10 +330,9 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
         const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ratio), 2 * st + i));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool in = z[4 * i + j] != -INFINITY;
-          const float p = __builtin_amdgcn_exp2f(z[4 * i + j] - ref);
+          const float p = __builtin_amdgcn_exp2f(fmaf(z[i][j], factor[i], -ref));
           l += p;
-          const float pv = in ? p * f : 0.f;
+          const float pv = usual || z[i][j] != -INFINITY ? p * f : 0.f;
           const _Float16 hi = (_Float16)pv;
           ph[4 * i + j] = hi;
           pl[4 * i + j] = (_Float16)(pv - (float)hi);
@@ -344,7 +365,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   // the four waves' sums, in units of 1
   constexpr int kPitch = Dp + 4;
   const int rows = A.frows;
-  float *sm = sh + few_floats(rows, Dp), *sl = sm + 64;
+  float *sm = sh + few_floats(rows, Dp), *sl = sm + 16 * kFewWaves;
   if (n < it.n) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) *(float4_t *)(sh + (w * rows + n) * kPitch + 16 * i + 4 * G) = O[i] * r;
@@ -355,15 +376,15 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   }
   __syncthreads();
   float *part = A.part + ((int64_t)slot * A.pieces + piece) * rows * (Dp + 2);
-  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += 256) {
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += kFewWaves * 64) {
     const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
     float M = sm[row];
 #pragma unroll
-    for (int v = 1; v < 4; ++v) M = fmaxf(M, sm[v * 16 + row]);
+    for (int v = 1; v < kFewWaves; ++v) M = fmaxf(M, sm[v * 16 + row]);
     float4_t o = {0.f, 0.f, 0.f, 0.f};
     float L = 0.f;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    for (int v = 0; v < kFewWaves; ++v) {
       const float f = __builtin_amdgcn_exp2f(sm[v * 16 + row] - M);
       o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * f;
       L += sl[v * 16 + row] * f;
@@ -385,7 +406,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   // the workgroup counts itself, and are read the same way.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  int *flag = (int *)(sl + 64);
+  int *flag = (int *)(sl + 16 * kFewWaves);
   if (threadIdx.x == 0) {
     const unsigned before = __hip_atomic_fetch_add(A.count + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *flag = before == (unsigned)pieces - 1;
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   const int64_t size = (int64_t)rows * (Dp + 2);
   const float *all = A.part + (int64_t)slot * A.pieces * size;
   float *wm = sh, *wl = sh + kJoinHere * 16;  // [piece][16]; the sums of the waves are no longer needed
-  for (int i = threadIdx.x; i < pieces * 16; i += 256) {
+  for (int i = threadIdx.x; i < pieces * 16; i += kFewWaves * 64) {
     const int row = i & 15;
     float2_t ml = {kNothing, 0.f};
     if (row < it.n) ml = load2(all + (i >> 4) * size + rows * Dp + 2 * row);
@@ -405,22 +426,23 @@ __global__ void __launch_bounds__(256) k_attend_few(AttendArgs A) {
   }
   __syncthreads();
   {
-    const int row = threadIdx.x >> 4, p0 = threadIdx.x & 15;
+    constexpr int kLanes = kFewWaves * 4;  // of a row
+    const int row = threadIdx.x / kLanes, p0 = threadIdx.x % kLanes;
     float M = kNothing, L = 0.f;
-    for (int p = p0; p < pieces; p += 16) M = fmaxf(M, wm[p * 16 + row]);
+    for (int p = p0; p < pieces; p += kLanes) M = fmaxf(M, wm[p * 16 + row]);
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
-    for (int p = p0; p < pieces; p += 16) {
+    for (int d = kLanes / 2; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
+    for (int p = p0; p < pieces; p += kLanes) {
       const float f = __builtin_amdgcn_exp2f(wm[p * 16 + row] - M);
       wm[p * 16 + row] = f;
       L += wl[p * 16 + row] * f;
     }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) L += lane_xor(L, d);
+    for (int d = kLanes / 2; d > 0; d >>= 1) L += lane_xor(L, d);
     if (p0 == 0) wl[row] = L;  // (piece 0's, read by this row's threads alone, before)
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += 256) {
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += kFewWaves * 64) {
     const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
     const float *from = all + row * Dp + d;
     float4_t o = {0.f, 0.f, 0.f, 0.f};
@@ -912,10 +934,10 @@ hipError_t allow_lds(F f, int bytes) {
 
 template <int NC>
 hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
-  const int lds = (few_floats(p.frows, NC * 32) + 132) * 4;
+  const int lds = (few_floats(p.frows, NC * 32) + 32 * kFewWaves + 4) * 4;
   hipError_t e = allow_lds(k_attend_few<NC>, lds);
   if (e != hipSuccess) return e;
-  k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(256), lds, st>>>(A);
+  k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(kFewWaves * 64), lds, st>>>(A);
   e = hipGetLastError();
   if (e != hipSuccess || p.few_pieces == 1 || A.count) return e;
   return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
@@ -994,7 +1016,7 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   if (rows * (int64_t)view.group > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
   const Plan p = plan_of(C->KV, C->Dp, C->cus, start != nullptr, rows, sequences, view);
-  if (p.few_items * p.few_pieces > 0x7fffffff / 256 || p.many_items * p.many_pieces > 0x7fffffff / 512 ||
+  if (p.few_items * p.few_pieces > 0x7fffffff / 512 || p.many_items * p.many_pieces > 0x7fffffff / 512 ||
       p.many_items * p.tr > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
   DeviceGuard dg(C->device);
