@@ -77,6 +77,7 @@ struct AttendArgs {
   int tiles, frows;  // 16-row tiles a sequence may have there, rows of a tile (16 or fewer)
   int chunk, pieces;  // keys of a piece, pieces in the grid
   int row_tiles;      // k_attend_many: row tiles in the grid
+  int b0;             // k_attend_few: first sequence of the grid
 };
 
 // What an item (a sequence's row tile of one key head) sees.
@@ -118,15 +119,14 @@ __device__ __forceinline__ float other32(float v) {
   return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
 }
 
-// Item `slot` of k_attend_few: (sequence, key head, 16-row tile), or false.
-__device__ __forceinline__ bool few_item(const AttendArgs &A, unsigned slot, Item &it) {
-  const unsigned s = slot / (unsigned)A.tiles, tile = slot - s * A.tiles;
-  const unsigned b = s / (unsigned)A.KV;
-  it.h = (int)(s - b * A.KV);
-  it.q = sequence(A.S, (int)b);
+// Item of k_attend_few: 16-row tile `tile` of sequence b's rows of key head h, or
+// false.  Items are numbered (b KV + h) tiles + tile.
+__device__ __forceinline__ bool few_item(const AttendArgs &A, int b, int h, int tile, Item &it) {
+  it.h = h;
+  it.q = sequence(A.S, b);
   const int64_t rows = (int64_t)it.q.rows * A.view.group;
   if (rows > A.few) return false;
-  it.r0 = (int)tile * 16;
+  it.r0 = tile * 16;
   if (it.r0 >= rows) return false;
   it.n = min(16, (int)rows - it.r0);
   keys_of_rows(A.view, it.q, it.r0, it.n, &it.lo, &it.hi);
@@ -199,18 +199,24 @@ template <int NC>
 __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(AttendArgs A) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = Dp / 16;
   extern __shared__ float sh[];  // [waves][rows][Dp + 4], then m and l [waves][16] each
-  const unsigned slot = blockIdx.x / (unsigned)A.pieces;
-  const int piece = (int)(blockIdx.x - slot * A.pieces);
+  const int b = A.b0 + (int)blockIdx.y, piece = (int)blockIdx.z;
+  const int h = A.tiles == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)A.tiles), tile = (int)blockIdx.x - h * A.tiles;
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 15, G = lane >> 4;
+  const int upp = 1 << (A.lg - 4);
+  // Wave w has pairs of units w, w + kFewWaves, ... of the piece.  Up to 32 pairs a
+  // time: lane i looks up the page of one unit.  The first look-up waits for the
+  // lengths only where a window moves the piece (its column is clamped to the table).
+  const auto unit_at = [&](int c0, int batch) { return (c0 >> 4) + 2 * (w + kFewWaves * (batch * 32 + (lane >> 1))) + (lane & 1); };
+  const auto look_up = [&](int u) { return A.S.table[b * A.S.ldt + min(u >> (A.lg - 4), A.S.columns - 1)]; };
+  int page = A.view.window ? -1 : look_up(unit_at(piece * A.chunk, 0));
   Item it;
-  if (!few_item(A, slot, it)) return;
+  if (!few_item(A, b, h, tile, it)) return;
   const int pieces = pieces_of(it.lo, it.hi, A.chunk);
   if (piece >= pieces) return;
-  const int b = (int)(slot / (unsigned)(A.tiles * A.KV));
+  const int64_t slot = ((int64_t)b * A.KV + h) * A.tiles + tile;
   const int c0 = it.lo + piece * A.chunk, c1 = min(it.hi, c0 + A.chunk);
-  // the wave's units of 16 keys, an even number before the last
-  const int units = (c1 - c0 + 15) >> 4, per = (units + 2 * kFewWaves - 1) / (2 * kFewWaves) * 2;
-  const int u0 = (c0 >> 4) + min(units, w * per), u1 = (c0 >> 4) + min(units, w * per + per);
+  if (A.view.window) page = look_up(unit_at(c0, 0));
+  const int all_pairs = (c1 - c0 + 31) >> 5, pairs = max(0, (all_pairs - w + kFewWaves - 1) / kFewWaves);  // the wave's
   const int myrow = it.r0 + min(n, it.n - 1);
   int first, last;
   keys_of_row(A.view, it.q, myrow, &first, &last);
@@ -235,7 +241,6 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   for (int i = 0; i < NT; ++i) O[i] = float4_t{0.f, 0.f, 0.f, 0.f};
   float m = kNothing, l = 0.f, r = 1e-30f;
 
-  const int upp = 1 << (A.lg - 4);
   struct Frag {
     u32x4_t pair[kPairs > 0 ? kPairs : 1];
     u32x2_t odd;
@@ -249,16 +254,16 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
       f.odd = *(const u32x2_t __attribute__((address_space(1))) *)(uintptr_t)(p + kPairs * 1024 + lane * 8);
   };
 
-  for (int ub = u0; ub < u1; ub += 64) {
-    // up to 64 units: lane i knows where unit ub + i lies, and its scales
-    const int u = ub + lane;
-    const int page = u < u1 ? page_of(A.S, b, u >> (A.lg - 4)) : -1;
-    const bool there = page >= 0;
+  for (int batch = 0; batch * 32 < pairs; ++batch) {
+    // lane i: where its unit lies, and its scales
+    const int u = unit_at(c0, batch);
+    if (batch) page = look_up(u);
+    const bool there = u * 16 < c1 && page >= 0 && page < A.S.pages;
     const int blk = (there ? page : 0) * A.KV + it.h;
     const int mine = blk * upp + (u & (upp - 1));
     const float ks = there ? A.ks[blk] * A.qscale : 0.f, vs = there ? A.vs[blk] : 0.f;
     const unsigned long long ok = __ballot(there);
-    const int steps = (min(u1 - ub, 64) + 1) >> 1;
+    const int steps = min(32, pairs - batch * 32);
     Frag K[2], V[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) load(A.kc, __builtin_amdgcn_readlane(mine, i), K[i]);
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
       // the next step's units, this one's again behind the last
       const int n0 = __builtin_amdgcn_readlane(mine, min(2 * st + 2, 2 * steps - 2));
       const int n1 = __builtin_amdgcn_readlane(mine, min(2 * st + 3, 2 * steps - 1));
-      const int t0 = (ub + 2 * st) * 16;
+      const int t0 = c0 + 32 * (w + kFewWaves * (batch * 32 + st));
       const unsigned both = (unsigned)(ok >> (2 * st)) & 3u;
       const bool usual = both == 3u && t0 >= all_first && t0 + 32 <= all_last;
       float4_t z[2];
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
     sl[w * 16 + n] = l;
   }
   __syncthreads();
-  float *part = A.part + ((int64_t)slot * A.pieces + piece) * rows * (Dp + 2);
+  float *part = A.part + (slot * A.pieces + piece) * rows * (Dp + 2);
   for (int i = threadIdx.x; i < it.n * (Dp / 4); i += kFewWaves * 64) {
     const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
     float M = sm[row];
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   __syncthreads();
   if (!*flag) return;
   const int64_t size = (int64_t)rows * (Dp + 2);
-  const float *all = A.part + (int64_t)slot * A.pieces * size;
+  const float *all = A.part + slot * A.pieces * size;
   float *wm = sh, *wl = sh + kJoinHere * 16;  // [piece][16]; the sums of the waves are no longer needed
   for (int i = threadIdx.x; i < pieces * 16; i += kFewWaves * 64) {
     const int row = i & 15;
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
 // turn took 127 us for 256 pieces of 64 rows of 128.)
 template <int TR, int NT>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
-  constexpr int kPer = 256 / NT, kMost = TR == 16 ? kFewPieces : 512;
+  constexpr int kPer = 256 / NT, kMost = TR == 16 ? kFewPieces : kManyPieces;
   __shared__ float weight[kPer][NT == 64 ? kJoinWave : kMost];
   __shared__ float4_t sums[256];
   __shared__ float wave[2][4];
@@ -810,7 +815,8 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   const int row = (int)(at - item * rows);
   Item it;
   if constexpr (TR == 16) {
-    if (item >= (unsigned)(A.S.n * A.KV * A.tiles) || !few_item(A, item, it)) return;
+    const unsigned bh = item / (unsigned)A.tiles, b = bh / (unsigned)A.KV;
+    if (b >= (unsigned)A.S.n || !few_item(A, (int)b, (int)(bh - b * A.KV), (int)(item - bh * A.tiles), it)) return;
   } else {
     const unsigned slot = item / (unsigned)A.KV;
     int b;
@@ -937,8 +943,16 @@ hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
   const int lds = (few_floats(p.frows, NC * 32) + 32 * kFewWaves + 4) * 4;
   hipError_t e = allow_lds(k_attend_few<NC>, lds);
   if (e != hipSuccess) return e;
-  k_attend_few<NC><<<dim3((unsigned)(p.few_items * p.few_pieces)), dim3(kFewWaves * 64), lds, st>>>(A);
-  e = hipGetLastError();
+  // The heads of a page lie side by side, and so do the workgroups that read them
+  // (sequences first: 64 sequences took 58 us, not 55; 64 of up to 16384 220, not 200).
+  // Windows of sequences keep the grid within its bounds.
+  for (int64_t b0 = 0; b0 < A.S.n && e == hipSuccess; b0 += 65535) {
+    AttendArgs W = A;
+    W.b0 = (int)b0;
+    k_attend_few<NC><<<dim3((unsigned)(A.KV * A.tiles), (unsigned)std::min<int64_t>(65535, A.S.n - b0), (unsigned)p.few_pieces),
+                       dim3(kFewWaves * 64), lds, st>>>(W);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || p.few_pieces == 1 || A.count) return e;
   return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
 }

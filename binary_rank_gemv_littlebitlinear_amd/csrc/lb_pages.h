@@ -112,9 +112,11 @@ struct Plan {
   size_t ws = 0;  // bytes of partial sums
 };
 
-constexpr int kFewChunk = 256;    // keys of the smallest piece of k_attend_few
+constexpr int kFewWhole = 1024;   // keys that k_attend_few does not cut
+constexpr int kFewChunk = 256;    // keys of its smallest piece
 constexpr int kManyChunk = 512;   // and of k_attend_many
-constexpr int kFewPieces = 1024;  // pieces that a call of k_attend_few has, if it has fewer items
+constexpr int kFewPieces = 256;  // pieces that a call of k_attend_few has, if it has fewer items
+constexpr int kManyPieces = 512;  // the most of a call of k_attend_many, which has one for each CU
 
 inline int many_tile(int Dp) { return Dp <= 128 ? 256 : 128; }
 
@@ -151,13 +153,14 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
   };
   if (p.few) {
     p.few_items = n * KV * p.tiles;
-    p.few_pieces = cut(p.few_items, span_of(p.frows), kFewPieces, kFewChunk, &p.few_chunk);
+    const int64_t span = span_of(p.frows);
+    p.few_pieces = cut(p.few_items, span, kFewPieces, span <= kFewWhole ? kFewWhole : kFewChunk, &p.few_chunk);
     if (p.few_pieces > 1) p.ws = (size_t)(p.few_items * p.few_pieces * p.frows * per_row) * 4;
   }
   if (p.many) {
     p.row_tiles = (int)(rows * group / p.tr + n);
     p.many_items = (int64_t)p.row_tiles * KV;
-    p.many_pieces = cut(p.many_items, span_of(p.tr), cus, kManyChunk, &p.many_chunk);
+    p.many_pieces = cut(p.many_items, span_of(p.tr), std::min(cus, kManyPieces), kManyChunk, &p.many_chunk);
     if (p.many_pieces > 1) p.ws = std::max(p.ws, (size_t)(p.many_items * p.many_pieces * p.tr * per_row) * 4);
   }
   return p;
