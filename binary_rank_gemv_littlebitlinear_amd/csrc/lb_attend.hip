@@ -56,8 +56,8 @@ constexpr float kMissing = -1e9f, kLeast = -100.f;
 constexpr int kFewWaves = 8;   // of a workgroup of k_attend_few
 constexpr int kJoinHere = 64;  // pieces up to which the last workgroup of k_attend_few to arrive joins them
 // LDS of k_attend_few: the waves' sums, or the weights of the pieces.
-__host__ __device__ constexpr int few_floats(int rows, int Dp) {
-  return kFewWaves * rows * (Dp + 4) > 2 * kJoinHere * 16 ? kFewWaves * rows * (Dp + 4) : 2 * kJoinHere * 16;
+__host__ __device__ constexpr int few_floats(int rows, int Dp, int waves) {
+  return waves * rows * (Dp + 4) > 2 * kJoinHere * 16 ? waves * rows * (Dp + 4) : 2 * kJoinHere * 16;
 }
 constexpr int kJoinWave = 8;  // pieces of a row up to which a wave joins it, not a workgroup
 
@@ -68,16 +68,20 @@ struct AttendArgs {
   int64_t ldq, ldo;
   const uint8_t *kc, *vc;
   const float *ks, *vs;
-  float *part;      // partial sums of the pieces: per item and piece rows x Dp sums, then m and l of each row
+  // partial sums of the pieces, of each kernel: per item and piece rows x Dp sums,
+  // then m and l of each row
+  float *few_part, *part;
   unsigned *count;  // arrivals at each item of k_attend_few, 0 between launches; NULL: k_attend_join does it
   float qscale;  // scale * log2 e
   int KV, D, lg;
   View view;
   int few;      // rows x heads of a group up to which k_attend_few has a sequence
   int tiles, frows;  // 16-row tiles a sequence may have there, rows of a tile (16 or fewer)
-  int chunk, pieces;  // keys of a piece, pieces in the grid
+  int few_chunk, few_pieces;  // keys of a piece, pieces in the grid
+  int chunk, pieces;          // the same of k_attend_many
   int row_tiles;      // k_attend_many: row tiles in the grid
   int b0;             // k_attend_few: first sequence of the grid
+  unsigned blocks;    // k_attend_many: workgroups with many rows; those behind them have few
 };
 
 // What an item (a sequence's row tile of one key head) sees.
@@ -195,28 +199,27 @@ __device__ __forceinline__ float4_t load4(const float *p) {
 // ------------------------------------------------------------- few rows
 // 16 rows a workgroup, whose waves share out the keys of a piece and read them
 // from memory straight into operands; the waves' sums are joined in LDS.
-template <int NC>
-__global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(AttendArgs A) {
+// Row tile `tile` of key head h of sequence b, one piece of its keys, by W waves.
+template <int NC, int W>
+__device__ __forceinline__ void few_rows(const AttendArgs &A, int b, int h, int tile, int piece, float *sh) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = Dp / 16;
-  extern __shared__ float sh[];  // [waves][rows][Dp + 4], then m and l [waves][16] each
-  const int b = A.b0 + (int)blockIdx.y, piece = (int)blockIdx.z;
-  const int h = A.tiles == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)A.tiles), tile = (int)blockIdx.x - h * A.tiles;
+  // sh: [waves][rows][Dp + 4], then m and l [waves][16] each
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 15, G = lane >> 4;
   const int upp = 1 << (A.lg - 4);
-  // Wave w has pairs of units w, w + kFewWaves, ... of the piece.  Up to 32 pairs a
+  // Wave w has pairs of units w, w + W, ... of the piece.  Up to 32 pairs a
   // time: lane i looks up the page of one unit.  The first look-up waits for the
   // lengths only where a window moves the piece (its column is clamped to the table).
-  const auto unit_at = [&](int c0, int batch) { return (c0 >> 4) + 2 * (w + kFewWaves * (batch * 32 + (lane >> 1))) + (lane & 1); };
+  const auto unit_at = [&](int c0, int batch) { return (c0 >> 4) + 2 * (w + W * (batch * 32 + (lane >> 1))) + (lane & 1); };
   const auto look_up = [&](int u) { return A.S.table[b * A.S.ldt + min(u >> (A.lg - 4), A.S.columns - 1)]; };
-  int page = A.view.window ? -1 : look_up(unit_at(piece * A.chunk, 0));
+  int page = A.view.window ? -1 : look_up(unit_at(piece * A.few_chunk, 0));
   Item it;
   if (!few_item(A, b, h, tile, it)) return;
-  const int pieces = pieces_of(it.lo, it.hi, A.chunk);
+  const int pieces = pieces_of(it.lo, it.hi, A.few_chunk);
   if (piece >= pieces) return;
   const int64_t slot = ((int64_t)b * A.KV + h) * A.tiles + tile;
-  const int c0 = it.lo + piece * A.chunk, c1 = min(it.hi, c0 + A.chunk);
+  const int c0 = it.lo + piece * A.few_chunk, c1 = min(it.hi, c0 + A.few_chunk);
   if (A.view.window) page = look_up(unit_at(c0, 0));
-  const int all_pairs = (c1 - c0 + 31) >> 5, pairs = max(0, (all_pairs - w + kFewWaves - 1) / kFewWaves);  // the wave's
+  const int all_pairs = (c1 - c0 + 31) >> 5, pairs = max(0, (all_pairs - w + W - 1) / W);  // the wave's
   const int myrow = it.r0 + min(n, it.n - 1);
   int first, last;
   keys_of_row(A.view, it.q, myrow, &first, &last);
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
       // the next step's units, this one's again behind the last
       const int n0 = __builtin_amdgcn_readlane(mine, min(2 * st + 2, 2 * steps - 2));
       const int n1 = __builtin_amdgcn_readlane(mine, min(2 * st + 3, 2 * steps - 1));
-      const int t0 = c0 + 32 * (w + kFewWaves * (batch * 32 + st));
+      const int t0 = c0 + 32 * (w + W * (batch * 32 + st));
       const unsigned both = (unsigned)(ok >> (2 * st)) & 3u;
       const bool usual = both == 3u && t0 >= all_first && t0 + 32 <= all_last;
       float4_t z[2];
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   // the four waves' sums, in units of 1
   constexpr int kPitch = Dp + 4;
   const int rows = A.frows;
-  float *sm = sh + few_floats(rows, Dp), *sl = sm + 16 * kFewWaves;
+  float *sm = sh + few_floats(rows, Dp, W), *sl = sm + 16 * W;
   if (n < it.n) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) *(float4_t *)(sh + (w * rows + n) * kPitch + 16 * i + 4 * G) = O[i] * r;
@@ -380,16 +383,16 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
     sl[w * 16 + n] = l;
   }
   __syncthreads();
-  float *part = A.part + (slot * A.pieces + piece) * rows * (Dp + 2);
-  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += kFewWaves * 64) {
+  float *part = A.few_part + (slot * A.few_pieces + piece) * rows * (Dp + 2);
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += W * 64) {
     const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
     float M = sm[row];
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) M = fmaxf(M, sm[v * 16 + row]);
+    for (int v = 1; v < W; ++v) M = fmaxf(M, sm[v * 16 + row]);
     float4_t o = {0.f, 0.f, 0.f, 0.f};
     float L = 0.f;
 #pragma unroll
-    for (int v = 0; v < kFewWaves; ++v) {
+    for (int v = 0; v < W; ++v) {
       const float f = __builtin_amdgcn_exp2f(sm[v * 16 + row] - M);
       o += *(const float4_t *)(sh + (v * rows + row) * kPitch + d) * f;
       L += sl[v * 16 + row] * f;
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   // the workgroup counts itself, and are read the same way.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  int *flag = (int *)(sl + 16 * kFewWaves);
+  int *flag = (int *)(sl + 16 * W);
   if (threadIdx.x == 0) {
     const unsigned before = __hip_atomic_fetch_add(A.count + slot, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *flag = before == (unsigned)pieces - 1;
@@ -420,9 +423,9 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   __syncthreads();
   if (!*flag) return;
   const int64_t size = (int64_t)rows * (Dp + 2);
-  const float *all = A.part + slot * A.pieces * size;
+  const float *all = A.few_part + slot * A.few_pieces * size;
   float *wm = sh, *wl = sh + kJoinHere * 16;  // [piece][16]; the sums of the waves are no longer needed
-  for (int i = threadIdx.x; i < pieces * 16; i += kFewWaves * 64) {
+  for (int i = threadIdx.x; i < pieces * 16; i += W * 64) {
     const int row = i & 15;
     float2_t ml = {kNothing, 0.f};
     if (row < it.n) ml = load2(all + (i >> 4) * size + rows * Dp + 2 * row);
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
   }
   __syncthreads();
   {
-    constexpr int kLanes = kFewWaves * 4;  // of a row
+    constexpr int kLanes = W * 4;  // of a row
     const int row = threadIdx.x / kLanes, p0 = threadIdx.x % kLanes;
     float M = kNothing, L = 0.f;
     for (int p = p0; p < pieces; p += kLanes) M = fmaxf(M, wm[p * 16 + row]);
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
     if (p0 == 0) wl[row] = L;  // (piece 0's, read by this row's threads alone, before)
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += kFewWaves * 64) {
+  for (int i = threadIdx.x; i < it.n * (Dp / 4); i += W * 64) {
     const int row = i / (Dp / 4), d = (i - row * (Dp / 4)) * 4;
     const float *from = all + row * Dp + d;
     float4_t o = {0.f, 0.f, 0.f, 0.f};
@@ -462,6 +465,13 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
     for (; p < pieces; ++p) o += load4(from + p * size) * wm[p * 16 + row];
     write4(A, it, row, d, o, wl[row]);
   }
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(AttendArgs A) {
+  extern __shared__ char smem[];
+  const unsigned h = A.tiles == 1 ? blockIdx.x : blockIdx.x / (unsigned)A.tiles;
+  few_rows<NC, kFewWaves>(A, A.b0 + (int)blockIdx.y, (int)h, (int)(blockIdx.x - h * A.tiles), (int)blockIdx.z, (float *)smem);
 }
 
 // Nothing but an order: v is computed before what comes after.  (No
@@ -483,12 +493,11 @@ __device__ __forceinline__ void here(const T &v) {
 // behind and values of tile t + 1: there is room for four halves of keys and two
 // tiles of values, so nothing is written that a slower wave may still read.
 template <int NC, int NW>
-__global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
+__device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = NC, TR = NW * 32;
   constexpr int kHalf = Dp * 128;  // bytes of a tile's keys, or values
-  // [4] halves of keys, [2] tiles of values, then scales: of keys [8][2] (read a
-  // step after the keys themselves), of values [2][4]
-  extern __shared__ char smem[];
+  // smem: [4] halves of keys, [2] tiles of values, then scales: of keys [8][2] (read
+  // a step after the keys themselves), of values [2][4]
   float *scales = (float *)(smem + 4 * kHalf);
   const int lane = threadIdx.x & 63, w = wave_id(), n = lane & 31, G = lane >> 5;
   // heads vary fastest, so that one head's tiles mostly meet on one XCD; the
@@ -797,6 +806,18 @@ __global__ void __launch_bounds__(NW * 64) k_attend_many(AttendArgs A) {
   }
 }
 
+// Both kinds of sequences of a call: those with few rows run on what the others
+// leave idle (15 single tokens beside 8 chunks of 251 of 24 heads of 80: 51 us, 64 in
+// two launches).
+template <int NC, int NW>
+__global__ void __launch_bounds__(NW * 64, NC <= 4 ? 2 : 1) k_attend_many(AttendArgs A) {
+  extern __shared__ char smem[];
+  if (blockIdx.x < A.blocks) return many_rows<NC, NW>(A, smem);
+  const unsigned i = blockIdx.x - A.blocks, ht = (unsigned)(A.KV * A.tiles), bp = i / ht, x = i - bp * ht;
+  const unsigned piece = bp / (unsigned)A.S.n, h = x / (unsigned)A.tiles;
+  few_rows<NC, NW>(A, (int)(bp - piece * A.S.n), (int)h, (int)(x - h * A.tiles), (int)piece, (float *)smem);
+}
+
 // --------------------------------------------------------------- joining
 // The pieces of a row, by NT threads: their weights first, then each group of
 // Dp / 4 threads adds up every so-manieth piece, and the groups meet in LDS.
@@ -822,10 +843,10 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
     int b;
     if (slot >= (unsigned)A.row_tiles || !many_item<TR>(A, (int)slot, (int)(item - slot * A.KV), it, &b)) return;
   }
-  const int pieces = pieces_of(it.lo, it.hi, A.chunk);
+  const int pieces = pieces_of(it.lo, it.hi, TR == 16 ? A.few_chunk : A.chunk);
   if (pieces == 1 || row >= it.n) return;
   const int64_t size = (int64_t)rows * (Dp + 2);
-  const float *part = A.part + (int64_t)item * A.pieces * size;
+  const float *part = TR == 16 ? A.few_part + (int64_t)item * A.few_pieces * size : A.part + (int64_t)item * A.pieces * size;
   const float *ml = part + rows * Dp + 2 * row;
   float M = kNothing;
   for (int p = t; p < pieces; p += NT) {
@@ -884,7 +905,7 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
 
 template <int TR>
 hipError_t launch_join(const AttendArgs &A, int64_t rows, int Dp, hipStream_t st) {
-  if (A.pieces <= kJoinWave)
+  if ((TR == 16 ? A.few_pieces : A.pieces) <= kJoinWave)
     k_attend_join<TR, 64><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(A, Dp);
   else
     k_attend_join<TR, 256><<<dim3((unsigned)rows), dim3(256), 0, st>>>(A, Dp);
@@ -940,9 +961,8 @@ hipError_t allow_lds(F f, int bytes) {
 
 template <int NC>
 hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
-  const int lds = (few_floats(p.frows, NC * 32) + 32 * kFewWaves + 4) * 4;
+  const int lds = (few_floats(p.frows, NC * 32, kFewWaves) + 32 * kFewWaves + 4) * 4;
   hipError_t e = allow_lds(k_attend_few<NC>, lds);
-  if (e != hipSuccess) return e;
   // The heads of a page lie side by side, and so do the workgroups that read them
   // (sequences first: 64 sequences took 58 us, not 55; 64 of up to 16384 220, not 200).
   // Windows of sequences keep the grid within its bounds.
@@ -953,19 +973,34 @@ hipError_t launch_few(const AttendArgs &A, const Plan &p, hipStream_t st) {
                        dim3(kFewWaves * 64), lds, st>>>(W);
     e = hipGetLastError();
   }
-  if (e != hipSuccess || p.few_pieces == 1 || A.count) return e;
-  return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
+  return e;
 }
 
-template <int NC>
-hipError_t launch_many(const AttendArgs &A, const Plan &p, hipStream_t st) {
-  constexpr int NW = NC <= 4 ? 8 : 4, lds = 4 * NC * 32 * 128 + 96;
+template <int NC, int NW>
+hipError_t launch_many(AttendArgs A, const Plan &p, hipStream_t st) {
+  constexpr int many = 4 * NC * 32 * 128 + 96;
+  const int lds = p.few ? std::max(many, (few_floats(p.frows, NC * 32, NW) + 32 * NW + 4) * 4) : many;
   hipError_t e = allow_lds(k_attend_many<NC, NW>, lds);
   if (e != hipSuccess) return e;
-  k_attend_many<NC, NW><<<dim3((unsigned)(p.many_items * p.many_pieces)), dim3(NW * 64), lds, st>>>(A);
+  A.blocks = (unsigned)(p.many_items * p.many_pieces);
+  k_attend_many<NC, NW><<<dim3((unsigned)(A.blocks + p.few_items * p.few_pieces)), dim3(NW * 64), lds, st>>>(A);
   e = hipGetLastError();
   if (e != hipSuccess || p.many_pieces == 1) return e;
   return launch_join<NW * 32>(A, p.many_items * (NW * 32), NC * 32, st);
+}
+
+template <int NC>
+hipError_t launch(const AttendArgs &A, const Plan &p, hipStream_t st) {
+  hipError_t e;
+  if (!p.many) {
+    e = launch_few<NC>(A, p, st);
+  } else if constexpr (NC <= 4) {
+    e = p.tr == 256 ? launch_many<NC, 8>(A, p, st) : launch_many<NC, 4>(A, p, st);
+  } else {
+    e = launch_many<NC, 4>(A, p, st);
+  }
+  if (e != hipSuccess || !p.few || p.few_pieces == 1 || A.count) return e;
+  return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
 }
 
 // The chunk of 32 dims as a constant.
@@ -992,7 +1027,7 @@ extern "C" lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int6
     return refuse("rows, sequences and max_length must be in [0, 2^30]");
   if (heads < 1 || heads > 65536 || heads % C->KV) return refuse("heads must be a multiple of the cache's key heads");
   if (rows == 0 || sequences == 0) return LB_OK;
-  const size_t need = reserve_bytes(C->KV, C->Dp, C->cus, rows, heads / C->KV, max_length);
+  const size_t need = reserve_bytes(C->Dp, C->cus, rows, heads / C->KV, max_length);
   DeviceGuard dg(C->device);
   return grow(C, need, "lb_cache_reserve", false, nullptr);
 }
@@ -1030,12 +1065,11 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   if (rows * (int64_t)view.group > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
   const Plan p = plan_of(C->KV, C->Dp, C->cus, start != nullptr, rows, sequences, view);
-  if (p.few_items * p.few_pieces > 0x7fffffff / 512 || p.many_items * p.many_pieces > 0x7fffffff / 512 ||
-      p.many_items * p.tr > 0x7fffffff)
+  if ((p.few_items * p.few_pieces + p.many_items * p.many_pieces) > 0x7fffffff / 512 || p.many_items * p.tr > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");
   DeviceGuard dg(C->device);
   hipStream_t stm = (hipStream_t)stream;
-  st = grow(C, p.ws, "lb_cache_attend", true, stm);
+  st = grow(C, p.few_ws + p.many_ws, "lb_cache_attend", true, stm);
   if (st != LB_OK) return st;
   AttendArgs A = {};
   A.S = S;
@@ -1043,7 +1077,7 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   A.out = (uint16_t *)out;
   A.ldq = ldq; A.ldo = ldo;
   A.kc = C->k; A.vc = C->v; A.ks = C->ks; A.vs = C->vs;
-  A.part = (float *)((char *)C->ws + kCountBytes);
+  A.few_part = (float *)((char *)C->ws + kCountBytes);
   A.qscale = scale * 1.44269504088896340736f;
   A.KV = C->KV; A.D = C->D; A.lg = C->lg;
   A.view = view;
@@ -1051,20 +1085,13 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   A.tiles = p.tiles;
   A.frows = p.frows;
   A.row_tiles = p.row_tiles;
-  hipError_t e = hipSuccess;
-  if (p.few) {
-    AttendArgs F = A;
-    F.chunk = p.few_chunk;
-    F.pieces = p.few_pieces;
-    if (p.few_pieces > 1 && p.few_pieces <= kJoinHere) F.count = (unsigned *)C->ws;
-    e = with_dims(C->Dp, [&](auto nc) { return launch_few<decltype(nc)::value>(F, p, stm); });
-  }
-  if (e == hipSuccess && p.many) {
-    AttendArgs M = A;
-    M.chunk = p.many_chunk;
-    M.pieces = p.many_pieces;
-    e = with_dims(C->Dp, [&](auto nc) { return launch_many<decltype(nc)::value>(M, p, stm); });
-  }
+  A.few_chunk = p.few_chunk;
+  A.few_pieces = p.few_pieces;
+  A.chunk = p.many_chunk;
+  A.pieces = p.many_pieces;
+  A.part = A.few_part + p.few_ws / 4;
+  if (p.few_pieces > 1 && p.few_pieces <= kJoinHere) A.count = (unsigned *)C->ws;
+  const hipError_t e = with_dims(C->Dp, [&](auto nc) { return launch<decltype(nc)::value>(A, p, stm); });
   if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_cache_attend: ") + hipGetErrorString(e));
   return LB_OK;
 }

@@ -109,7 +109,7 @@ struct Plan {
   int few_rows = 0, tiles = 0, frows = 0;  // tiles a sequence may have, rows of a tile
   int few_chunk = 0, few_pieces = 1, many_chunk = 0, many_pieces = 1, row_tiles = 0, tr = 0;
   int64_t few_items = 0, many_items = 0;
-  size_t ws = 0;  // bytes of partial sums
+  size_t few_ws = 0, many_ws = 0;  // bytes of partial sums
 };
 
 constexpr int kFewWhole = 1024;   // keys that k_attend_few does not cut
@@ -118,7 +118,11 @@ constexpr int kManyChunk = 512;   // and of k_attend_many
 constexpr int kFewPieces = 256;  // pieces that a call of k_attend_few has, if it has fewer items
 constexpr int kManyPieces = 512;  // the most of a call of k_attend_many, which has one for each CU
 
-inline int many_tile(int Dp) { return Dp <= 128 ? 256 : 128; }
+// Rows of a tile of k_attend_many: 256 where registers allow it (Dp <= 128) and
+// such tiles fill the GPU twice, else 128 (two workgroups a CU).  32 heads of 128,
+// 256 against 128 rows: a prompt of 4096 (544 items of 256) 183 us against 205, of
+// 2048 (288) 87 against 78, of 1024 (160) 51 against 42, of 256 (64) 19 against 16.
+inline int many_tile(int Dp, int cus, int64_t items256) { return Dp <= 128 && items256 > 2 * cus ? 256 : 128; }
 
 // Pieces of an item's keys: about `target` for all items together, of `least`
 // keys or more; `span` bounds an item's keys.
@@ -133,7 +137,7 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
   Plan p;
   const int group = A.group;
   const int64_t per_row = (int64_t)Dp + 2;
-  p.tr = many_tile(Dp);
+  p.tr = many_tile(Dp, cus, (rows * group / 256 + n) * KV);
   if (!starts) {
     p.few = true;
     p.few_rows = group;
@@ -155,13 +159,13 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
     p.few_items = n * KV * p.tiles;
     const int64_t span = span_of(p.frows);
     p.few_pieces = cut(p.few_items, span, kFewPieces, span <= kFewWhole ? kFewWhole : kFewChunk, &p.few_chunk);
-    if (p.few_pieces > 1) p.ws = (size_t)(p.few_items * p.few_pieces * p.frows * per_row) * 4;
+    if (p.few_pieces > 1) p.few_ws = (size_t)(p.few_items * p.few_pieces * p.frows * per_row) * 4;
   }
   if (p.many) {
     p.row_tiles = (int)(rows * group / p.tr + n);
     p.many_items = (int64_t)p.row_tiles * KV;
     p.many_pieces = cut(p.many_items, span_of(p.tr), std::min(cus, kManyPieces), kManyChunk, &p.many_chunk);
-    if (p.many_pieces > 1) p.ws = std::max(p.ws, (size_t)(p.many_items * p.many_pieces * p.tr * per_row) * 4);
+    if (p.many_pieces > 1) p.many_ws = (size_t)(p.many_items * p.many_pieces * p.tr * per_row) * 4;
   }
   return p;
 }
@@ -169,13 +173,13 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
 // Workspace that is enough for every call of up to `rows` rows, any number of
 // sequences and `most` keys: an item has more than one piece only while all of
 // them together stay below the target.
-inline size_t reserve_bytes(int KV, int Dp, int cus, int64_t rows, int group, int64_t most) {
+inline size_t reserve_bytes(int Dp, int cus, int64_t rows, int group, int64_t most) {
   const int64_t per_row = (int64_t)Dp + 2;
-  (void)KV;
   size_t need = 0;
-  if (most > kFewChunk) need = (size_t)(kFewPieces * 16 * per_row) * 4;
-  if (most > kManyChunk && rows * group > 32)
-    need = std::max(need, (size_t)((int64_t)cus * many_tile(Dp) * per_row) * 4);
+  if (most > kFewWhole) need += (size_t)(kFewPieces * 16 * per_row) * 4;
+  // (calls with 256-row tiles have more items than CUs, which are not cut; those
+  // that have fewer items in 128-row tiles than CUs are)
+  if (most > kManyChunk && rows * group > 32) need += (size_t)((int64_t)std::min(cus, kManyPieces) * 128 * per_row) * 4;
   return need;
 }
 

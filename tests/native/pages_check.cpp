@@ -172,7 +172,7 @@ int main() {
     const bool starts = rnd(0, 1);
     const int64_t n = rnd(1, 1 << rnd(0, 10)), rows = starts ? rnd(1, 1 << rnd(0, 16)) : n;
     const Plan p = plan_of(KV, Dp, cus, starts, rows, n, A);
-    CHECK(p.ws <= reserve_bytes(KV, Dp, cus, rows + rnd(0, 9), A.group, std::min(1 << 30, A.most + rnd(0, 99))));
+    CHECK(p.few_ws + p.many_ws <= reserve_bytes(Dp, cus, rows + rnd(0, 9), A.group, std::min(1 << 30, A.most + rnd(0, 99))));
     CHECK(p.few || p.many);
     CHECK(!p.few || (p.few_chunk >= kFewChunk && p.few_chunk % 16 == 0));
     CHECK(!p.many || (p.many_chunk >= kManyChunk && p.many_chunk % 64 == 0));
