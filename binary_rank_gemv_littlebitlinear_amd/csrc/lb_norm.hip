@@ -11,9 +11,11 @@
 // normed as it was summed, before its own rounding, and out and x are rounded
 // once each.
 //
-// Bound by reading y and r and writing out and x, each once.  A thread holds
-// pieces of 8 neighbouring columns (16 bytes of fp16), so that a row is read
-// and written in wide accesses at any alignment.
+// Bound by reading y and r and writing out and x, each once (4096 rows of 8192
+// with a norm on each side: 403 MB in 78 us, 5.1 TB/s, a copy's rate); a single row
+// by latency (3.3 us of 4096, of which 2 are a launch).  A thread holds pieces of 8
+// neighbouring columns (16 bytes of fp16), so that a row is read and written in wide
+// accesses at any alignment.
 #include <hip/hip_fp16.h>
 
 #include <algorithm>
@@ -46,67 +48,109 @@ struct NormArgs {
 __device__ __forceinline__ float h2f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
 __device__ __forceinline__ uint32_t f2h(float v) { return __half_as_ushort(__float2half_rn(v)); }
 
-// Columns c .. c + 7 of a row at p (fp32 or fp16); those past the width are 0.
-__device__ __forceinline__ void load8(const void *p, int f32, int64_t row, int c, int width, float (&v)[8]) {
-  if (c + 8 <= width) {
-    if (f32) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 q = *LB_LOOSE((const float *)p + row + c + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(q[i]);
-      }
-    } else {
-      const u32x4 q = *LB_LOOSE((const uint16_t *)p + row + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = h2f((uint16_t)(q[i] & 0xffffu));
-        v[2 * i + 1] = h2f((uint16_t)(q[i] >> 16));
-      }
-    }
-    return;
+// A thread's piece: the 8 columns from `at` on, of which those from `own` on are
+// its own.  The row's last, incomplete piece begins further left instead, among
+// its neighbour's columns (a row of 1031 took 5.7 us with single loads for it), as
+// do pieces past the row, which own nothing.  A row of fewer than 8 columns is one
+// piece at 0.
+struct Piece {
+  int at, own;
+};
+__device__ __forceinline__ Piece piece_at(int c, int width) { return {max(0, min(c, width - 8)), c}; }
+
+// 8 fp16 numbers as they lie in memory.
+__device__ __forceinline__ u32x4 pack8(const uint16_t *p, int64_t row, Piece a, int width) {
+  if (width >= 8) return *LB_LOOSE(p + row + a.at);
+  u32x4 q = {0, 0, 0, 0};
+  for (int i = 0; i < width; ++i) {
+    const uint32_t v = (uint32_t)p[row + i] << (16 * (i & 1));
+    if (i < 2)
+      q[0] |= v;
+    else if (i < 4)
+      q[1] |= v;
+    else if (i < 6)
+      q[2] |= v;
+    else
+      q[3] |= v;
   }
+  return q;
+}
+__device__ __forceinline__ float unpack(const u32x4 &q, int i) { return h2f((uint16_t)(q[i >> 1] >> (16 * (i & 1)))); }
+
+// The piece of a row at p, fp32 or fp16.
+__device__ __forceinline__ void load8(const void *p, int f32, int64_t row, Piece a, int width, float (&v)[8]) {
+  if (!f32) {
+    const u32x4 q = pack8((const uint16_t *)p, row, a, width);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = 0.f;
-    if (c + i < width) v[i] = f32 ? ((const float *)p)[row + c + i] : h2f(((const uint16_t *)p)[row + c + i]);
+    for (int i = 0; i < 8; ++i) v[i] = unpack(q, i);
+  } else if (width >= 8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 q = *LB_LOOSE((const float *)p + row + a.at + 4 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < width ? ((const float *)p)[row + i] : 0.f;
   }
 }
 
-__device__ __forceinline__ void store8(void *p, int f32, int64_t row, int c, int width, const float (&v)[8]) {
-  if (c + 8 <= width) {
+// Whether column i of the piece is its own; ODD: the width is no multiple of 8.
+template <bool ODD>
+__device__ __forceinline__ bool owns(Piece a, int i, int width) {
+  return ODD ? a.at + i >= a.own && a.at + i < width : a.own < width;
+}
+
+__device__ __forceinline__ void store8(void *p, int f32, int64_t row, Piece a, int width, const float (&v)[8]) {
+  if (a.at == a.own && width >= 8) {
     if (f32) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         u32x4 q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(v[4 * h + i]);
-        *LB_LOOSE((float *)p + row + c + 4 * h) = q;
+        *LB_LOOSE((float *)p + row + a.at + 4 * h) = q;
       }
     } else {
       u32x4 q;
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = f2h(v[2 * i]) | (f2h(v[2 * i + 1]) << 16);
-      *LB_LOOSE((uint16_t *)p + row + c) = q;
+      *LB_LOOSE((uint16_t *)p + row + a.at) = q;
     }
     return;
   }
+  if (a.own >= width) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < width) {
+    if (owns<true>(a, i, width)) {
       if (f32)
-        ((float *)p)[row + c + i] = v[i];
+        ((float *)p)[row + a.at + i] = v[i];
       else
-        ((uint16_t *)p)[row + c + i] = (uint16_t)f2h(v[i]);
+        ((uint16_t *)p)[row + a.at + i] = (uint16_t)f2h(v[i]);
     }
+}
+
+// The sum over the wave by DPP moves, in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xf>(v);  // one, two, four and eight lanes down the row of 16
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);  // the last lane of a row to the next row
+  v = dpp_add<0x143, 0xc>(v);  // that of the first half to the second
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // The sum over the NT threads of a row.  part: NT / 64 floats of LDS, another
 // set for every call, so that one barrier is enough.
 template <int NT>
 __device__ __forceinline__ float row_sum(float v, float *part) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  v = wave_sum(v);
   if constexpr (NT > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -117,76 +161,89 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
   return v;
 }
 
-// v = N(v) w + b over the row.
+// A norm's weight and bias, requested with the row itself where registers allow
+// it (K < 4): behind the row's sums they would be waited for on their own.
+template <int K>
+struct Affine {
+  u32x4 w[K], b[K];
+};
 template <int NT, int K>
+__device__ __forceinline__ void load_affine(const uint16_t *w, const uint16_t *b, int t, int width, Affine<K> &f) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Piece a = piece_at((k * NT + t) * 8, width);
+    if (w) f.w[k] = pack8(w, 0, a, width);
+    if (b) f.b[k] = pack8(b, 0, a, width);
+  }
+}
+
+// v = N(v) w + b over the row.
+template <int NT, int K, bool ODD>
 __device__ __forceinline__ void norm_row(const NormArgs &A, float (&v)[K][8], const uint16_t *w, const uint16_t *b,
-                                         int t, float *part) {
+                                         Affine<K> &f, int t, float *part) {
   float mean = 0.f;
   if (A.layer) {
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[k][i];
+      for (int i = 0; i < 8; ++i) s += owns<ODD>(piece_at((k * NT + t) * 8, A.width), i, A.width) ? v[k][i] : 0.f;
     mean = row_sum<NT>(s, part) / (float)A.width;
     part += NT / 64;
   }
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * NT + t) * 8;
+    const Piece a = piece_at((k * NT + t) * 8, A.width);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float d = c + i < A.width ? v[k][i] - mean : 0.f;
+      const float d = v[k][i] - mean;
       v[k][i] = d;
-      s = fmaf(d, d, s);
+      if (owns<ODD>(a, i, A.width)) s = fmaf(d, d, s);
     }
   }
-  const float f = 1.f / sqrtf(row_sum<NT>(s, part) / (float)A.width + A.eps);
+  const float r = 1.f / sqrtf(row_sum<NT>(s, part) / (float)A.width + A.eps);
+  if constexpr (K >= 4) load_affine<NT, K>(w, b, t, A.width, f);
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * NT + t) * 8;
-    float a[8];
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] *= f;
-    if (w) {
-      load8(w, 0, 0, c, A.width, a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] *= a[i];
+    for (int i = 0; i < 8; ++i) {
+      v[k][i] *= r;
+      if (w) v[k][i] *= unpack(f.w[k], i);
+      if (b) v[k][i] += unpack(f.b[k], i);
     }
-    if (b) {
-      load8(b, 0, 0, c, A.width, a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] += a[i];
-    }
-  }
 }
 
 // NT threads a row, K pieces of 8 columns a thread; a workgroup of 64-thread
 // rows has four of them.
-template <int NT, int K>
+template <int NT, int K, bool ODD>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormArgs A) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
   __shared__ float part[4 * (NT / 64)];
   const int t = threadIdx.x % NT;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
   if (kRows > 1 && row >= A.rows) return;  // whole waves, which share nothing
+  Affine<K> before, after;
+  if constexpr (K < 4) {
+    if (A.post) load_affine<NT, K>(A.post_weight, A.post_bias, t, A.width, before);
+    if (A.x) load_affine<NT, K>(A.weight, A.bias, t, A.width, after);
+  }
   float u[K][8], r[K][8];
   if (A.y) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) load8(A.y, A.y32, row * A.ldy, (k * NT + t) * 8, A.width, u[k]);
+    for (int k = 0; k < K; ++k) load8(A.y, A.y32, row * A.ldy, piece_at((k * NT + t) * 8, A.width), A.width, u[k]);
   }
   if (A.r) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) load8(A.r, A.r32, row * A.ldr, (k * NT + t) * 8, A.width, r[k]);
+    for (int k = 0; k < K; ++k) load8(A.r, A.r32, row * A.ldr, piece_at((k * NT + t) * 8, A.width), A.width, r[k]);
   }
   if (A.y) {
-    if (A.post) norm_row<NT, K>(A, u, A.post_weight, A.post_bias, t, part);
+    if (A.post) norm_row<NT, K, ODD>(A, u, A.post_weight, A.post_bias, before, t, part);
     if (A.gate) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float g[8];
-        load8(A.gate, 0, row * A.ldg, (k * NT + t) * 8, A.width, g);
+        load8(A.gate, 0, row * A.ldg, piece_at((k * NT + t) * 8, A.width), A.width, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= g[i];
       }
@@ -205,18 +262,22 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormArgs A) {
   }
   if (A.out) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) store8(A.out, A.r32, row * A.ldo, (k * NT + t) * 8, A.width, u[k]);
+    for (int k = 0; k < K; ++k) store8(A.out, A.r32, row * A.ldo, piece_at((k * NT + t) * 8, A.width), A.width, u[k]);
   }
   if (!A.x) return;
-  norm_row<NT, K>(A, u, A.weight, A.bias, t, part + 2 * (NT / 64));
+  norm_row<NT, K, ODD>(A, u, A.weight, A.bias, after, t, part + 2 * (NT / 64));
 #pragma unroll
-  for (int k = 0; k < K; ++k) store8(A.x, 0, row * A.ldx, (k * NT + t) * 8, A.width, u[k]);
+  for (int k = 0; k < K; ++k) store8(A.x, 0, row * A.ldx, piece_at((k * NT + t) * 8, A.width), A.width, u[k]);
 }
 
 template <int NT, int K>
 hipError_t launch(const NormArgs &A, hipStream_t st) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  k_norm<NT, K><<<dim3((unsigned)((A.rows + kRows - 1) / kRows)), dim3(NT * kRows), 0, st>>>(A);
+  const dim3 grid((unsigned)((A.rows + kRows - 1) / kRows));
+  if (A.width % 8)
+    k_norm<NT, K, true><<<grid, dim3(NT * kRows), 0, st>>>(A);
+  else
+    k_norm<NT, K, false><<<grid, dim3(NT * kRows), 0, st>>>(A);
   return hipGetLastError();
 }
 
@@ -296,14 +357,24 @@ extern "C" lb_status lb_norm(int kind, const void *y, int y_type, int64_t ldy, i
     W.x = (uint16_t *)at(x, ldx, 2);
     hipStream_t st = (hipStream_t)stream;
     hipError_t e;
+    // Threads of a row x pieces of each: many threads share out the latency of few
+    // rows, few need less of the machine for many.  4096 wide, 1 row: 512 x 1 3.3 us,
+    // 256 x 2 3.8, 1024 x 1 4.0 (4096 rows: 31.7, 31.6, 35.8).  8192 wide with a norm
+    // on each side, 1 row: 1024 x 1 4.6, 512 x 2 4.8, 256 x 4 6.2; 1023 rows: 21.0,
+    // 18.0, 18.2; 4096 rows: 77.1, 76.6, 81.4.  1031 wide: 64 x 3 and 256 x 1 take 8.6
+    // and 7.7 for 1023 rows, 15.2 and 19.9 for 4096.
     if (width <= 512)
       e = launch<64, 1>(W, st);
+    else if (width <= 1536 && W.rows >= 2048)
+      e = launch<64, 3>(W, st);
     else if (width <= 2048)
       e = launch<256, 1>(W, st);
     else if (width <= 4096)
-      e = launch<256, 2>(W, st);
+      e = launch<512, 1>(W, st);
+    else if (width <= 8192 && W.rows >= 256)
+      e = launch<512, 2>(W, st);
     else if (width <= 8192)
-      e = launch<256, 4>(W, st);
+      e = launch<1024, 1>(W, st);
     else if (width <= 16384)
       e = launch<1024, 2>(W, st);
     else
