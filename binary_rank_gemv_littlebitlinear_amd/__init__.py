@@ -360,8 +360,10 @@ def _say(t) -> str:
 # device numbers (-1: not on a GPU) and leave the wording of errors to the failing case.
 def _rows(name, t, width, dtypes, dev):
     """(rows, row stride) of a 2-d tensor of `width` columns with unit column stride on GPU `dev`."""
-    if t.dim() == 2:
-        (rows, cols), (ld, unit) = t.shape, t.stride()
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        ld, unit = t.stride()
         if cols == width and (unit == 1 or width == 1) and t.dtype in dtypes and t.get_device() == dev:
             # a single row's stride is never used; torch leaves it arbitrary
             return rows, ld if rows > 1 else width
@@ -501,6 +503,14 @@ def lb_route_combine(y, row, weights, out, residual=None, stream=None):
 NORMS = {"rms": 0, "layer": 1}
 
 
+def _like(name, t, rows, width, dtypes, dev):
+    """(pointer, row stride) of a tensor that must have `rows` rows (see _rows)."""
+    n, ld = _rows(name, t, width, dtypes, dev)
+    if n != rows:
+        raise ValueError(f"{name} must have {rows} rows, not {n}")
+    return t.data_ptr(), ld
+
+
 def lb_norm(r, x=None, y=None, out=None, kind="rms", weight=None, bias=None, post=False, post_weight=None,
             post_bias=None, gate=None, scale=1.0, eps=1e-5, stream=None):
     """out = scale * r + gate * (norm of) y, x = its norm (see include/lb.h).
@@ -513,43 +523,42 @@ def lb_norm(r, x=None, y=None, out=None, kind="rms", weight=None, bias=None, pos
     dev = lead.get_device()
     if lead.dim() != 2 or dev < 0:
         raise ValueError("r and y must be 2-d device tensors")
-    try:
-        k = NORMS[kind]
-    except KeyError:
-        raise ValueError(f"kind must be one of {sorted(NORMS)}, not {kind!r}") from None
+    k = NORMS.get(kind)
+    if k is None:
+        raise ValueError(f"kind must be one of {sorted(NORMS)}, not {kind!r}")
     rows, width = lead.shape
     like = out if r is None else r
     rtype = _f16 if like is None else like.dtype
     if rtype is not _f16 and rtype is not _f32:
         raise ValueError(f"the residual must be {_f16} or {_f32}, not {rtype}")
-
-    def of(name, t, dtypes):
-        if t is None:
-            return None, 0
-        n, ld = _rows(name, t, width, dtypes, dev)
-        if n != rows:
-            raise ValueError(f"{name} must have {rows} rows, not {n}")
-        return t.data_ptr(), ld
-
-    def vec(name, t):
-        return None if t is None else _flat(name, t, (width,), _f16, dev)
-
-    py, ldy = of("y", y, _f16_f32)
-    pr, ldr = of("r", r, _f16_f32)
-    po, ldo = of("out", out, (rtype,))
-    px, ldx = of("x", x, _only_f16)
-    pg, ldg = None, 0
+    py = pr = po = px = pg = w = b = pw = pb = None
+    ldy = ldr = ldo = ldx = ldg = ytype = 0
+    if y is not None:
+        py, ldy = _like("y", y, rows, width, _f16_f32, dev)
+        ytype = LB_F32 if y.dtype is _f32 else LB_F16
+    if r is not None:
+        pr, ldr = _like("r", r, rows, width, _f16_f32, dev)
+    if out is not None:
+        po, ldo = _like("out", out, rows, width, (rtype,), dev)
+    if x is not None:
+        px, ldx = _like("x", x, rows, width, _only_f16, dev)
     if gate is not None:
         n, ldg = _rows("gate", gate, width, _only_f16, dev)
-        if n != rows and n != 1:
-            raise ValueError(f"gate must have 1 or {rows} rows, not {n}")
-        pg = gate.data_ptr()
         if n == 1:
             ldg = 0
-    _on_device(dev, load_library().lb_norm, k, py, LB_F32 if y is not None and y.dtype is _f32 else LB_F16, ldy,
-               1 if post else 0, vec("post_weight", post_weight), vec("post_bias", post_bias), pg, ldg, pr, ldr, scale,
-               LB_F32 if rtype is _f32 else LB_F16, vec("weight", weight), vec("bias", bias), eps, po, ldo, px, ldx, rows,
-               width, _stream_of(stream, dev))
+        elif n != rows:
+            raise ValueError(f"gate must have 1 or {rows} rows, not {n}")
+        pg = gate.data_ptr()
+    if weight is not None:
+        w = _flat("weight", weight, (width,), _f16, dev)
+    if bias is not None:
+        b = _flat("bias", bias, (width,), _f16, dev)
+    if post_weight is not None:
+        pw = _flat("post_weight", post_weight, (width,), _f16, dev)
+    if post_bias is not None:
+        pb = _flat("post_bias", post_bias, (width,), _f16, dev)
+    _on_device(dev, load_library().lb_norm, k, py, ytype, ldy, 1 if post else 0, pw, pb, pg, ldg, pr, ldr, scale,
+               LB_F32 if rtype is _f32 else LB_F16, w, b, eps, po, ldo, px, ldx, rows, width, _stream_of(stream, dev))
 
 
 def lb_cache_create(pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
@@ -571,63 +580,60 @@ def lb_cache_reserve(cache: int, rows: int, heads: int, sequences: int, max_leng
 
 def _sequences(rows, lengths, table, start, dev):
     """start, lengths, table, its row stride, columns, sequences, rows: the C order."""
-    _types()
     if table.dim() != 2 or table.dtype is not _i32 or table.get_device() != dev:
         raise ValueError(f"table must be a 2-d {_i32} tensor on GPU {dev}, not {_say(table)}")
     (n, columns), (ld, unit) = table.shape, table.stride()
     if unit != 1 and columns > 1:
         raise ValueError(f"table must have unit-stride columns, not {_say(table)}")
-    if start is None and rows != n:
+    if start is not None:
+        start = _flat("start", start, (n + 1,), _i32, dev)
+    elif rows != n:
         raise ValueError(f"without start there is a row for each sequence: {n}, not {rows}")
-    return (None if start is None else _flat("start", start, (n + 1,), _i32, dev), _flat("lengths", lengths, (n,), _i32, dev),
-            table.data_ptr(), ld if n > 1 else columns, columns, n, rows)
+    return start, _flat("lengths", lengths, (n,), _i32, dev), table.data_ptr(), ld if n > 1 else columns, columns, n, rows
 
 
 def _heads(name, t, dim, dev):
     """(pointer, row stride, rows, heads) of a 2-d tensor with `dim` columns for each head."""
-    if t.dim() != 2 or t.shape[1] % dim or not t.shape[1]:
+    width = t.shape[1] if t.dim() == 2 else 0
+    if not width or width % dim:
         raise ValueError(f"{name} must be 2-d with {dim} columns for each head, not {_say(t)}")
-    rows, ld = _rows(name, t, t.shape[1], _only_f16, dev)
-    return t.data_ptr(), ld, rows, t.shape[1] // dim
+    rows, ld = _rows(name, t, width, _only_f16, dev)
+    return t.data_ptr(), ld, rows, width // dim
 
 
 def lb_cache_append(cache, k, v, lengths, table, start=None, q=None, q_out=None, rope=None, interleaved=False,
                     stream=None):
     """``Cache`` owner and tensors: the rows of k and v into the pages of their sequences (see include/lb.h)."""
     _types()
-    dev, width = cache.device, cache.kv_heads * cache.head_dim
+    dev, width = cache.device, cache.width
     rows, ldk = _rows("k", k, width, _only_f16, dev)
-    vr, ldv = _rows("v", v, width, _only_f16, dev)
-    if vr != rows:
-        raise ValueError("k and v must have the same number of rows")
+    pv, ldv = _like("v", v, rows, width, _only_f16, dev)
     pq = po = pr = None
     ldq = ldo = heads = positions = rot = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         pq, ldq, qr, heads = _heads("q", q, cache.head_dim, dev)
-        po, ldo, wr, oh = _heads("q_out", q_out, cache.head_dim, dev)
-        if qr != rows or wr != rows or oh != heads:
-            raise ValueError("q and q_out must have k's rows and the same heads")
+        if qr != rows:
+            raise ValueError("q must have k's rows")
+        po, ldo = _like("q_out", q_out, rows, heads * cache.head_dim, _only_f16, dev)
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError("rope must be 2-d: positions x rot")
         positions, rot = rope.shape
         pr = _flat("rope", rope, (positions, rot), _f32, dev)
-    _check(_lib.lb_cache_append(cache.handle, k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, po, ldo, heads, pr, positions,
-                                rot, 1 if interleaved else 0, *_sequences(rows, lengths, table, start, dev),
+    _check(_lib.lb_cache_append(cache.handle, k.data_ptr(), ldk, pv, ldv, pq, ldq, po, ldo, heads, pr, positions, rot,
+                                1 if interleaved else 0, *_sequences(rows, lengths, table, start, dev),
                                 _stream_of(stream, dev)))
 
 
 def lb_cache_read(cache, k, v, lengths, table, start=None, stream=None):
     """``Cache`` owner and tensors: k and v receive the values of the sequences' last tokens (see include/lb.h)."""
     _types()
-    dev, width = cache.device, cache.kv_heads * cache.head_dim
+    dev, width = cache.device, cache.width
     rows, ldk = _rows("k", k, width, _only_f16, dev)
-    vr, ldv = _rows("v", v, width, _only_f16, dev)
-    if vr != rows:
-        raise ValueError("k and v must have the same number of rows")
-    _check(_lib.lb_cache_read(cache.handle, k.data_ptr(), ldk, v.data_ptr(), ldv,
+    pv, ldv = _like("v", v, rows, width, _only_f16, dev)
+    _check(_lib.lb_cache_read(cache.handle, k.data_ptr(), ldk, pv, ldv,
                               *_sequences(rows, lengths, table, start, dev), _stream_of(stream, dev)))
 
 
@@ -638,9 +644,7 @@ def lb_cache_attend(cache, q, out, lengths, table, start=None, max_length=None, 
     _types()
     dev = cache.device
     pq, ldq, rows, heads = _heads("q", q, cache.head_dim, dev)
-    po, ldo, wr, oh = _heads("out", out, cache.head_dim, dev)
-    if wr != rows or oh != heads:
-        raise ValueError("out must have q's rows and heads")
+    po, ldo = _like("out", out, rows, heads * cache.head_dim, _only_f16, dev)
     _check(_lib.lb_cache_attend(cache.handle, pq, ldq, heads, po, ldo, *_sequences(rows, lengths, table, start, dev),
                                 int(max_length or 0), cache.head_dim ** -0.5 if scale is None else scale,
                                 1 if causal else 0, window, _stream_of(stream, dev)))
@@ -802,6 +806,7 @@ class Cache:
         self.handle = None
         self.handle = lb_cache_create(pages, page_tokens, kv_heads, head_dim)
         self.pages, self.page_tokens, self.kv_heads, self.head_dim, self.device = lb_cache_shape(self.handle)
+        self.width = self.kv_heads * self.head_dim
 
     def reserve(self, rows: int, heads: int, sequences: int, max_length: int):
         lb_cache_reserve(self.handle, rows, heads, sequences, max_length)

@@ -39,6 +39,7 @@ struct AppendArgs {
   uint8_t *kc, *vc;
   float *ks, *vs;
   int heads, KV, D, Dp, P, lg, rot, inter;
+  int both;        // queries are whole heads of two partner halves, each a multiple of 8 dims
   int64_t items;   // page slots of the launch
   int64_t kvwgs;   // workgroups of keys and values; the others turn queries
   int qparts;      // waves a row of queries has
@@ -113,102 +114,136 @@ __device__ __forceinline__ float amax(float m, float v) {
   return v > m || v != v ? v : m;
 }
 
+// Dims 8 g .. 8 g + 7 of up to four new tokens, tok .. tok + 3 of the page; those
+// outside a .. e - 1 are 0.  x: the row of token a; cs: the table's row of its
+// position.
+template <bool KEYS>
+__device__ __forceinline__ void load_item(const AppendArgs &A, const uint16_t *x, const float *cs, int tok, int g, int a,
+                                          int e, float (&v)[4][8]) {
+  const int64_t ld = KEYS ? A.ldk : A.ldv;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = tok + j - a;
+    if (r >= 0 && tok + j < e) {
+      turn8(x + r * ld, g, A.D, KEYS ? cs + (int64_t)r * A.rot : nullptr, KEYS ? A.rot : 0, A.inter, v[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+    }
+  }
+}
+
+// Writes those tokens' bytes.  Keys: 8 bytes a token.  Values: 4 bytes a dim, of
+// which those of other tokens stay (earlier ones rounded again by f where grown).
+template <bool KEYS>
+__device__ __forceinline__ void store_item(const AppendArgs &A, uint8_t *out, int tok, int g, int a, int e, float s,
+                                           bool grown, float f, const float (&v)[4][8]) {
+  const int pairs = A.Dp / 64, c = g >> 3;
+  const bool full = c < pairs;
+  uint8_t *unit = out + (int64_t)(tok >> 4) * 16 * A.Dp + c * 1024;
+  if (KEYS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (tok + j < a || tok + j >= e) continue;
+      u32x2_t w = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i >> 2] |= to_byte(v[j][i], s) << (8 * (i & 3));
+      const int lane = (g & 3) * 16 + (tok & 15) + j;
+      *(u32x2_t *)(unit + (full ? lane * 16 + ((g >> 2) & 1) * 8 : lane * 8)) = w;
+    }
+    return;
+  }
+  const bool whole = tok >= a && tok + 4 <= e;
+  const int i = (g >> 1) & 3;  // of the tiles of 16 dims in a pair
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    const int lane = ((tok >> 2) & 3) * 16 + (g & 1) * 8 + d;
+    uint32_t *to = (uint32_t *)(unit + (full ? lane * 16 : lane * 8) + i * 4);
+    uint32_t w = 0;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= to_byte(v[j][d], s) << (8 * j);
+    } else {
+      const uint32_t was = *to;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t byte = (was >> (8 * j)) & 255u;
+        w |= (tok + j >= e ? byte : tok + j < a ? (grown ? again(byte, f) : byte) : to_byte(v[j][d], s)) << (8 * j);
+      }
+    }
+    *to = w;
+  }
+}
+
 // One head of one page, by NT threads: new tokens a .. e - 1 of the page, whose
-// first row is `row` (of token a).
+// first row is `row` (of token a, at position pos).  An item is 4 tokens x 8 dims;
+// a thread keeps its first one, and reads later ones again when the scale is known.
 template <int NT, bool KEYS>
 __device__ void append_block(const AppendArgs &A, int64_t page, int h, int a, int e, int64_t row, int pos, float *part) {
   const int t = threadIdx.x % NT;
   const uint16_t *x = (KEYS ? A.k : A.v) + row * (KEYS ? A.ldk : A.ldv) + (int64_t)h * A.D;
-  const int64_t ld = KEYS ? A.ldk : A.ldv;
-  const int groups = A.D / 8, rot = KEYS ? A.rot : 0;
-  float m = 0.f;
-  for (int i = t; i < (e - a) * groups; i += NT) {
-    const int tok = i / groups, g = i - tok * groups;
-    float o[8];
-    turn8(x + tok * ld, g, A.D, rot ? A.rope + (int64_t)(pos + tok) * rot : nullptr, rot, A.inter, o);
+  const float *cs = KEYS && A.rot ? A.rope + (int64_t)pos * A.rot : nullptr;
+  float *scale = (KEYS ? A.ks : A.vs) + page * A.KV + h;
+  const float before = a > 0 ? *scale : 0.f;
+  const int groups = A.D / 8, tok0 = a & ~3, n = ((e - tok0 + 3) >> 2) * groups;
+  float v[4][8];
+  float m = 0.f, bad = 0.f;  // bad: NaN once a number is not finite
+  const auto item = [&](int i, int &tok, int &g) {
+    tok = tok0 + (i / groups) * 4;
+    g = i % groups;
+  };
+  for (int i = t + (n - 1 - t) / NT * NT; i >= t; i -= NT) {  // the first last, to be kept
+    int tok, g;
+    item(i, tok, g);
+    load_item<KEYS>(A, x, cs, tok, g, a, e, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = amax(m, o[j]);
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m = fmaxf(m, fabsf(v[j][k]));
+        bad = fmaf(v[j][k], 0.f, bad);
+      }
   }
+  if (bad != bad) m = bad;
   m = wave_amax(m);
   if constexpr (NT > 64) {
     if ((t & 63) == 0) part[t >> 6] = m;
+    __builtin_amdgcn_s_waitcnt(0);  // every thread has its scale before one writes it
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT / 64; ++i) m = amax(m, part[i]);
   }
-  float *scale = (KEYS ? A.ks : A.vs) + page * A.KV + h;
-  const float before = a > 0 ? *scale : 0.f;
   float s = m / 127.f;
   if (!(s < INFINITY)) s = __uint_as_float(0x7fc00000u);
   if (!(s > before) && s == s) s = before;
   const bool grown = a > 0 && s > before;
   const float f = grown ? before / s : 1.f;
-  if constexpr (NT > 64) __syncthreads();  // every thread has read the scale
   if (t == 0) *scale = s;
 
-  // the page's bytes: pieces of 16 (a pair of 32 dims) and 8 (the odd 32)
   uint8_t *out = (KEYS ? A.kc : A.vc) + (page * A.KV + h) * (int64_t)A.P * A.Dp;
-  const int pairs = A.Dp / 64, odd = (A.Dp / 32) & 1, per = (pairs + odd) * 64;  // pieces of a unit
-  const int u0 = grown ? 0 : a >> 4, u1 = (e - 1) >> 4;
-  for (int i = t; i < (u1 - u0 + 1) * per; i += NT) {
-    const int u = u0 + i / per, piece = i % per, c = piece >> 6, lane = piece & 63, G = lane >> 4, xx = lane & 15;
-    const bool full = c < pairs;
-    uint8_t *to = out + (int64_t)u * 16 * A.Dp + (full ? piece * 16 : pairs * 1024 + lane * 8);
-    u32x4_t w = {0, 0, 0, 0};
-    if (KEYS) {
-      const int tok = u * 16 + xx;
-      if (tok >= e || (tok < a && !grown)) continue;
-      if (tok < a) {
-        if (full)
-          w = *(const u32x4_t *)to;
-        else
-          *(u32x2_t *)&w = *(const u32x2_t *)to;
+  for (int i = t; i < n; i += NT) {
+    int tok, g;
+    item(i, tok, g);
+    if (i != t) load_item<KEYS>(A, x, cs, tok, g, a, e, v);
+    store_item<KEYS>(A, out, tok, g, a, e, s, grown, f, v);
+  }
+  if (!grown) return;
+  // the page's earlier tokens, except values that share 4 bytes with new ones:
+  // pieces of 16 bytes (a pair of 32 dims) and 8 (the odd 32)
+  const int pairs = A.Dp / 64, odd = (A.Dp / 32) & 1, per = (pairs + odd) * 64;
+  for (int i = t; i < ((a + 15) >> 4) * per; i += NT) {
+    const int u = i / per, piece = i % per, c = piece >> 6, lane = piece & 63;
+    const int last = KEYS ? u * 16 + (lane & 15) : u * 16 + 4 * (lane >> 4) + 3;
+    if (last >= a) continue;
+    uint8_t *to = out + (int64_t)u * 16 * A.Dp + (c < pairs ? piece * 16 : pairs * 1024 + lane * 8);
+    uint32_t *word = (uint32_t *)to;
+    for (int d = 0; d < (c < pairs ? 4 : 2); ++d) {
+      const uint32_t was = word[d];
+      uint32_t w = 0;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t n = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) n |= again((w[d] >> (8 * j)) & 255u, f) << (8 * j);
-          w[d] = n;
-        }
-      } else {
-        const float *cs = rot ? A.rope + (int64_t)(pos + tok - a) * rot : nullptr;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int g = 8 * c + 4 * hh + G;
-          if ((!full && hh) || g >= groups) continue;
-          float o[8];
-          turn8(x + (tok - a) * ld, g, A.D, cs, rot, A.inter, o);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[2 * hh + (j >> 2)] |= to_byte(o[j], s) << (8 * (j & 3));
-        }
-      }
-    } else {
-      const int tok0 = u * 16 + 4 * G;
-      if (tok0 >= e || (tok0 + 3 < a && !grown)) continue;
-      if (tok0 < a || tok0 + 3 >= e) {  // bytes of other tokens stay
-        if (full)
-          w = *(const u32x4_t *)to;
-        else
-          *(u32x2_t *)&w = *(const u32x2_t *)to;
-      }
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii) {
-        const int d = 64 * c + 16 * ii + xx;
-        if ((!full && ii > 1) || d >= A.D) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int tok = tok0 + j;
-          const uint32_t was = (w[ii] >> (8 * j)) & 255u;
-          const uint32_t b = tok >= e ? was : tok < a ? (grown ? again(was, f) : was)
-                                                     : to_byte(h2f(x[(tok - a) * ld + d]), s);
-          w[ii] = (w[ii] & ~(255u << (8 * j))) | (b << (8 * j));
-        }
-      }
+      for (int j = 0; j < 4; ++j) w |= again((was >> (8 * j)) & 255u, f) << (8 * j);
+      word[d] = w;
     }
-    if (full)
-      *(u32x4_t *)to = w;
-    else
-      *(u32x2_t *)to = *(const u32x2_t *)&w;
   }
 }
 
@@ -241,8 +276,8 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       append_block<NT, true>(A, page, h, a, e, row, pos, part);
     return;
   }
-  // queries: a wave turns 4 x hpi heads of a row, hpi whole heads at a time, so
-  // that a group's partner is read in the same step (q may be turned in place)
+  // queries: a wave turns some heads of a row, whole heads at a time, so that a
+  // group's partner is read in the same step (q may be turned in place)
   const unsigned wv = (blockIdx.x - (unsigned)A.kvwgs) * 4 + wave_id();
   const unsigned row = wv / (unsigned)A.qparts;
   const int qp = (int)(wv - row * A.qparts), lane = threadIdx.x & 63, groups = A.D / 8, hpi = 64 / groups;
@@ -257,6 +292,35 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   const int pos = (int)row - q.row0 + (q.length - q.rows);
   if (pos < p0 || pos >= p1) return;
   const float *cs = A.rot ? A.rope + (int64_t)pos * A.rot : nullptr;
+  if (A.both) {  // a lane has a group and its partner: half of the loads
+    const int half = A.rot / 2, per = groups / 2, hl = lane / per, d = (lane - hl * per) * 8, hpi2 = 64 / per;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = (qp * 2 + i) * hpi2 + hl;
+      if (hl >= hpi2 || h >= A.heads) continue;
+      const uint16_t *x = A.q + row * A.ldq + (int64_t)h * A.D + d;
+      const u32x4_t lo = *LB_LOOSE128(x), hi = *LB_LOOSE128(x + half);
+      const float *cp = cs + d, *sp = cp + half;
+      u32x4_t wl, wh;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float l[2], g[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p = h2f((uint16_t)(lo[j] >> (16 * k))), q2 = h2f((uint16_t)(hi[j] >> (16 * k)));
+          const float c = cp[2 * j + k], sn = sp[2 * j + k];
+          l[k] = p * c - q2 * sn;
+          g[k] = p * sn + q2 * c;
+        }
+        wl[j] = f2h(l[0]) | (f2h(l[1]) << 16);
+        wh[j] = f2h(g[0]) | (f2h(g[1]) << 16);
+      }
+      uint16_t *to = A.qo + row * A.ldqo + (int64_t)h * A.D + d;
+      *LB_LOOSE128(to) = wl;
+      *LB_LOOSE128(to + half) = wh;
+    }
+    return;
+  }
   const int hl = lane / groups, g = lane - hl * groups;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -489,8 +553,9 @@ extern "C" lb_status lb_cache_append(lb_cache *C, const void *k, int64_t ldk, co
   const bool single = rows <= 2 * (int64_t)sequences;
   const int64_t blocks = A.items * 2 * C->KV;
   A.kvwgs = single ? (blocks + 3) / 4 : blocks;
-  const int hpi = 64 / (C->D / 8);
-  A.qparts = q ? (heads + 4 * hpi - 1) / (4 * hpi) : 0;
+  A.both = rot == C->D && rot % 16 == 0 && !interleaved;
+  const int per_wave = A.both ? 2 * (64 / (C->D / 16)) : 4 * (64 / (C->D / 8));  // heads
+  A.qparts = q ? (heads + per_wave - 1) / per_wave : 0;
   const int64_t qwgs = (rows * A.qparts + 3) / 4;
   if (A.kvwgs + qwgs > 0x7fffffff / 256 || blocks > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_append: too many rows and heads for one call");
