@@ -96,8 +96,10 @@ __device__ __forceinline__ uint32_t to_byte(float v, float s) {
   const float q = s > 0.f ? rintf(v / s) : 0.f;
   return (uint32_t)((int)fminf(fmaxf(q, -127.f), 127.f) + 128);
 }
-__device__ __forceinline__ uint32_t again(uint32_t byte, float f) {
-  return (uint32_t)((int)rintf((float)((int)byte - 128) * f) + 128);
+// A number rounded again for a scale that is 1 / f times larger.  In fp64: ratios of
+// the scales of 16-bit numbers make exact halves, which fp32 would send either way.
+__device__ __forceinline__ uint32_t again(uint32_t byte, double f) {
+  return (uint32_t)((int)rint((double)((int)byte - 128) * f) + 128);
 }
 
 __device__ __forceinline__ float wave_amax(float v) {
@@ -137,7 +139,7 @@ __device__ __forceinline__ void load_item(const AppendArgs &A, const uint16_t *x
 // which those of other tokens stay (earlier ones rounded again by f where grown).
 template <bool KEYS>
 __device__ __forceinline__ void store_item(const AppendArgs &A, uint8_t *out, int tok, int g, int a, int e, float s,
-                                           bool grown, float f, const float (&v)[4][8]) {
+                                           bool grown, double f, const float (&v)[4][8]) {
   const int pairs = A.Dp / 64, c = g >> 3;
   const bool full = c < pairs;
   uint8_t *unit = out + (int64_t)(tok >> 4) * 16 * A.Dp + c * 1024;
@@ -217,7 +219,7 @@ __device__ void append_block(const AppendArgs &A, int64_t page, int h, int a, in
   if (!(s < INFINITY)) s = __uint_as_float(0x7fc00000u);
   if (!(s > before) && s == s) s = before;
   const bool grown = a > 0 && s > before;
-  const float f = grown ? before / s : 1.f;
+  const double f = grown ? (double)before / (double)s : 1.0;
   if (t == 0) *scale = s;
 
   uint8_t *out = (KEYS ? A.kc : A.vc) + (page * A.KV + h) * (int64_t)A.P * A.Dp;

@@ -78,9 +78,10 @@ def turn(x, pos, rope, interleaved):
 class Cache:
     """Keys and values as the definition has them, page by page, in plain loops.
 
-    Numbers are rint(value / scale) with the scale and the quotient in fp32: without a rotation every step is a single
-    fp32 operation on fp16 inputs, so they are the library's bit for bit.  `error` bounds how far each number may be
-    from the value that was appended, in steps: half for each rounding.
+    Numbers are rint(value / scale) with the scale and the quotient in fp32, and rint(number * (scale / larger scale)) in
+    fp64 where a page's scale grows: without a rotation every step is a single operation on fp16 inputs or on its
+    results, so they are the library's bit for bit.  `error` bounds how far each number may be from the value that was
+    appended, in steps: half for each rounding.
     """
 
     def __init__(self, pages, page, kv_heads, dim):
@@ -122,7 +123,7 @@ class Cache:
             if np.isnan(old) or not (s > old or np.isnan(s)):
                 s = old
             elif first and not np.isnan(s):
-                num[:first, h] = np.rint((num[:first, h].astype(np.float32) * np.float32(old / s)).astype(np.float32))
+                num[:first, h] = np.rint(num[:first, h] * (float(old) / float(s)))
                 error[:first, h] = error[:first, h] * old / s + 0.5
             self.scale[name][page, h] = s
             for p, v in val.items():
