@@ -370,7 +370,7 @@ __device__ __forceinline__ void few_rows(const AttendArgs &A, int b, int h, int 
   l += other16(l);
   l += other32(l);
 
-  // the four waves' sums, in units of 1
+  // the waves' sums, in units of 1
   constexpr int kPitch = Dp + 4;
   const int rows = A.frows;
   float *sm = sh + few_floats(rows, Dp, W), *sl = sm + 16 * W;
@@ -1041,7 +1041,8 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   if (rows < 0 || rows > kMaxRows || sequences < 0 || sequences > kMaxRows)
     return refuse("rows and sequences must be in [0, 2^30]");
   if (heads < 1 || heads > 65536 || heads % C->KV) return refuse("heads must be a multiple of the cache's key heads");
-  if (!(scale >= 0.f) || !(scale < INFINITY)) return refuse("scale must be finite and not negative");
+  // (scores then stay far above kNothing)
+  if (!(scale >= 0.f) || scale > 1e6f) return refuse("scale must be in [0, 1e6]");
   if (window < 0 || (window && !causal)) return refuse("a window is not negative and needs causal");
   if (max_length < 0 || max_length > kMaxRows) return refuse("max_length must be in [0, 2^30]");
   if (rows == 0) return LB_OK;
@@ -1061,6 +1062,7 @@ extern "C" lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, in
   if (sequences == 0) return LB_OK;
   int64_t most = (int64_t)columns * C->P;
   if (max_length) most = std::min(most, max_length);
+  if (window >= kMaxTokens) window = 0;  // hides nothing, and a position less it passes 32 bits
   View view = {heads / C->KV, causal != 0, window, (int)most};
   if (rows * (int64_t)view.group > 0x7fffffff)
     return set_error(LB_EUNSUPPORTED, "lb_cache_attend: too many rows and heads for one call");

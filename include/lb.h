@@ -534,8 +534,9 @@ lb_status lb_norm(int kind, const void *y, int y_type, int64_t ldy, int post, co
  * value = number * scale, numbers -127 .. 127, scale = largest / 127.
  * Which page belongs to whom is the caller's: a call gets its sequences as
  *   table     device int32, sequences x columns, row stride ldt: the pages
- *             of every sequence in the order of its tokens.  Pages may be
- *             shared between sequences, but not written by two in one call
+ *             of every sequence in the order of its tokens.  A page may stand
+ *             in several places, but a call appends through one of them only
+ *             (otherwise the page's numbers are undefined)
  *   lengths   device int32: tokens of every sequence, the call's included
  *   start     device int32, sequences + 1 non-decreasing values in
  *             [0, rows]: rows start[b] .. start[b + 1] - 1 are the last tokens
@@ -596,6 +597,7 @@ lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int64_t sequenc
  *             h / (heads / kv_heads).  out must not overlap the inputs
  *   max_length  a bound on lengths that the call is cut up for (tokens past it
  *             are not seen), or 0: what the table can hold
+ *   scale     0 to 1e6
  *   causal    a row sees its sequence's tokens up to its own position;
  *             otherwise all of them
  *   window    with causal: the last `window` of those only; 0 for all

@@ -87,6 +87,29 @@ def test_one_sequence(lbm, rows):
         _run(lbm, cache, ref, c, rng, f"rows={rows} dim={dim} before={before} window 1", window=1)
 
 
+def test_widest_windows(lbm):
+    """Windows past every position, with rows before position 0 in the same tile."""
+    say("[case] attend widest windows")
+    rng = np.random.default_rng(17)
+    for new in (20, 90):
+        c = cacheref.Case(rng, [100, 95], [new, new], 16, 1, 1, 64)
+        cache, ref = _filled(lbm, c, rng)
+        for window in (2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1):
+            for lengths in (c.lengths, np.array([new - 7, 2], np.int32)):
+                _run(lbm, cache, ref, c, rng, f"new={new} window={window}", lengths=lengths, window=window)
+
+
+def test_scale_out_of_range(lbm):
+    torch = lbtest.torch_dev()
+    cache = lbm.Cache(1, 16, 1, 8)
+    q, out = torch.zeros((1, 8), dtype=torch.float16, device="cuda"), torch.ones((1, 8), dtype=torch.float16, device="cuda")
+    lengths, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    for scale in (-1.0, 1.1e6, float("inf"), float("nan")):
+        with pytest.raises(lbm.LBError):
+            cache.attend(q, out, lengths, table, scale=scale)
+    assert (out == 1).all()
+
+
 @pytest.mark.parametrize("length", [255, 256, 257, 512, 1023, 1025, 2048, 5000])
 def test_split_keys(lbm, length):
     """Keys split over workgroups and joined, for single tokens and for chunks, also through a window."""
