@@ -350,8 +350,11 @@ struct ReadArgs {
   int KV, D, Dp, lg;
 };
 
-// A wave has one unit of 16 tokens of one head, keys or values.
+// A wave has one unit of 16 tokens of one head, keys or values.  A lane has 8
+// neighbouring dims of a token's key, but of values 4 tokens of single dims: those
+// are put in order in LDS, 64 dims of all tokens at a time.
 __global__ void __launch_bounds__(256) k_cache_read(ReadArgs A) {
+  __shared__ __align__(16) uint16_t order[4][16][72];  // (8 more than it needs keep rows on different banks)
   const Sequences &S = A.S;
   const unsigned block = blockIdx.x * 4 + wave_id();
   const unsigned item = block / (unsigned)(2 * A.KV);
@@ -381,17 +384,25 @@ __global__ void __launch_bounds__(256) k_cache_read(ReadArgs A) {
     const auto value = [&](int i) { return f2h((float)((int)((w[i >> 2] >> (8 * (i & 3))) & 255u) - 128) * s); };
     const int parts = c < pairs ? 2 : 1;
     if (values) {
-      for (int i = 0; i < 2 * parts; ++i) {
-        const int d = 64 * c + 16 * i + x;
-        if (d >= A.D) continue;
+      uint16_t(*tile)[72] = order[wave_id()];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (4 * G + j < a || 4 * G + j >= e) continue;
-          uint32_t word = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
-          const float f = there ? (float)((int)((word >> (8 * j)) & 255u) - 128) * s : 0.f;
-          A.v[(row0 + 4 * G + j) * A.ldv + (int64_t)h * A.D + d] = (uint16_t)f2h(f);
-        }
+      for (int i = 0; i < 4; ++i) {
+        if (i >= 2 * parts) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tile[4 * G + j][16 * i + x] = there ? (uint16_t)value(4 * i + j) : 0;
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int lg = parts + 1;  // groups of 8 dims a token: 8 or 4
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i >= parts) break;
+        const int t = (lane + 64 * i) >> lg, d = 8 * (lane & ((1 << lg) - 1));
+        if (t >= a && t < e && 64 * c + d < A.D)
+          *LB_LOOSE128(A.v + (row0 + t) * A.ldv + (int64_t)h * A.D + 64 * c + d) = *(const u32x4_t *)&tile[t][d];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();  // before the next dims
     } else {
       if (x < a || x >= e) continue;
 #pragma unroll
