@@ -476,10 +476,14 @@ __global__ void __launch_bounds__(kFewWaves * 64, NC <= 4 ? 4 : 2) k_attend_few(
 
 // Nothing but an order: v is computed before what comes after.  (No
 // instruction reads it here, so a matrix instruction's result needs no wait.)
-template <typename T>
+// ACC: it lies in an accumulation register, and stays there.
+template <bool ACC = false, typename T>
 __device__ __forceinline__ void here(const T &v) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("" ::"v"(v));
+  if constexpr (ACC)
+    asm volatile("" ::"a"(v));
+  else
+    asm volatile("" ::"v"(v));
 #endif
 }
 
@@ -711,7 +715,7 @@ __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       zn = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[s % kAhead], q[s], zn, 0, 0, 0);
-      here(zn);
+      here<(NC > 4)>(zn);  // (with more than 256 registers the sums are in the others)
       if (s + kAhead < 2 * kSteps) ring[s % kAhead] = operand(kb, vb, s + kAhead);
 #pragma unroll
       for (int e = 2 * (s * 8 / kSteps); e < 2 * ((s + 1) * 8 / kSteps); e += 2) {
