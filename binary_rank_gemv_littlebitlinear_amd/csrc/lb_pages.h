@@ -114,8 +114,9 @@ struct Plan {
 
 constexpr int kFewWhole = 1024;   // keys that k_attend_few does not cut
 constexpr int kFewChunk = 256;    // keys of its smallest piece
+constexpr int kFewLong = 2048;    // and of one that only evens out the work
 constexpr int kManyChunk = 512;   // and of k_attend_many
-constexpr int kFewPieces = 256;  // pieces that a call of k_attend_few has, if it has fewer items
+constexpr int kFewPieces = 2048;  // the most of a call of k_attend_few
 constexpr int kManyPieces = 512;  // the most of a call of k_attend_many, which has one for each CU
 
 // Rows of a tile of k_attend_many: 256 where registers allow it (Dp <= 128) and
@@ -158,7 +159,18 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
   if (p.few) {
     p.few_items = n * KV * p.tiles;
     const int64_t span = span_of(p.frows);
-    p.few_pieces = cut(p.few_items, span, kFewPieces, span <= kFewWhole ? kFewWhole : kFewChunk, &p.few_chunk);
+    // Few items are cut to have one for each CU.  Then nothing is left that takes much
+    // longer than the rest, which pays only for long pieces.  64 heads of 128 on 8:
+    // 64 sequences of up to 4096 keys 49 us in pieces of 2048, 53 whole and 51 in pieces
+    // of 1024; of up to 16384 169, 200 and 169; 25 of up to 32768 140 and 207; but 30 of
+    // up to 4096 31 in pieces of 2048 and 29 whole, one of 131072 62 and 59 in 4096s.
+    p.few_pieces = cut(p.few_items, span, std::min(cus, kFewPieces), span <= kFewWhole ? kFewWhole : kFewChunk, &p.few_chunk);
+    int chunk;
+    const int pieces = cut(p.few_items, span, kFewPieces, p.few_items >= cus ? kFewLong : 2 * kFewLong, &chunk);
+    if (pieces > p.few_pieces) {
+      p.few_pieces = pieces;
+      p.few_chunk = chunk;
+    }
     if (p.few_pieces > 1) p.few_ws = (size_t)(p.few_items * p.few_pieces * p.frows * per_row) * 4;
   }
   if (p.many) {
@@ -176,7 +188,7 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
 inline size_t reserve_bytes(int Dp, int cus, int64_t rows, int group, int64_t most) {
   const int64_t per_row = (int64_t)Dp + 2;
   size_t need = 0;
-  if (most > kFewWhole) need += (size_t)(kFewPieces * 16 * per_row) * 4;
+  if (most > kFewWhole) need += (size_t)((most > kFewLong ? kFewPieces : std::min(cus, kFewPieces)) * 16 * per_row) * 4;
   // (calls with 256-row tiles have more items than CUs, which are not cut; those
   // that have fewer items in 128-row tiles than CUs are)
   if (most > kManyChunk && rows * group > 32) need += (size_t)((int64_t)std::min(cus, kManyPieces) * 128 * per_row) * 4;

@@ -284,6 +284,19 @@ def test_many_sequences(lbm):
     _run(lbm, cache, ref, c, rng, "200 single tokens", start=False)
 
 
+@pytest.mark.parametrize("sequences,heads,longest", [(70, 16, 5000), (300, 4, 4200), (9, 8, 12000)])
+def test_uneven_lengths(lbm, sequences, heads, longest):
+    """Single tokens of sequences of very different lengths, the long ones cut into long pieces."""
+    say(f"[case] attend uneven sequences={sequences}")
+    rng = np.random.default_rng(sequences)
+    lengths = rng.integers(0, 60, sequences)
+    lengths[[0, 5, sequences - 1]] = longest, longest // 2 + 3, longest - 17
+    c = cacheref.Case(rng, lengths, np.minimum(1, lengths), 64, 4, heads, 32)
+    cache, ref = _filled(lbm, c, rng)
+    _run(lbm, cache, ref, c, rng, "uneven", start=False)
+    _run(lbm, cache, ref, c, rng, "uneven, window", start=False, window=longest - 100)
+
+
 def test_shared_pages_and_repeats(lbm):
     """Two sequences with a common prefix read the same pages; the same call gives the same bits."""
     torch = lbtest.torch_dev()
