@@ -117,7 +117,8 @@ constexpr int kFewChunk = 256;    // keys of its smallest piece
 constexpr int kFewLong = 2048;    // and of one that only evens out the work
 constexpr int kManyChunk = 512;   // and of k_attend_many
 constexpr int kFewPieces = 2048;  // the most of a call of k_attend_few
-constexpr int kManyPieces = 512;  // the most of a call of k_attend_many, which has one for each CU
+constexpr int kManyLong = 1024;   // (again, one that evens out the work)
+constexpr int kManyPieces = 1024;  // the most of a call of k_attend_many
 
 // Rows of a tile of k_attend_many: 256 where registers allow it (Dp <= 128) and
 // such tiles fill the GPU twice, else 128 (two workgroups a CU).  32 heads of 128,
@@ -176,7 +177,20 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
   if (p.many) {
     p.row_tiles = (int)(rows * group / p.tr + n);
     p.many_items = (int64_t)p.row_tiles * KV;
-    p.many_pieces = cut(p.many_items, span_of(p.tr), std::min(cus, kManyPieces), kManyChunk, &p.many_chunk);
+    // The same here, while there is little more than an item for each CU (a CU has room
+    // for two) and keys enough to pay for joining.  In pieces of 1024 and whole: a prompt
+    // of 4096 with 8 heads of 128 91 us and 131, of 256 205 and 323; 6 chunks of 300 rows
+    // of up to 8000 keys, 32 heads on 8, 146 and 244; 500 rows of 9000 keys, 32 heads, 143
+    // and 159.  But a prompt of 1500 with 32 heads 75 and 59, the last 1500 rows of 4500
+    // keys (400 items) 196 and 167 in pieces of 2250.
+    const int64_t span = span_of(p.tr);
+    p.many_pieces = cut(p.many_items, span, std::min(cus, kManyPieces), kManyChunk, &p.many_chunk);
+    int chunk;
+    const int pieces = cut(p.many_items, span, kManyPieces, kManyLong, &chunk);
+    if (p.many_items <= cus * 5 / 4 && span >= 4 * kManyLong && pieces > p.many_pieces) {
+      p.many_pieces = pieces;
+      p.many_chunk = chunk;
+    }
     if (p.many_pieces > 1) p.many_ws = (size_t)(p.many_items * p.many_pieces * p.tr * per_row) * 4;
   }
   return p;
@@ -189,9 +203,9 @@ inline size_t reserve_bytes(int Dp, int cus, int64_t rows, int group, int64_t mo
   const int64_t per_row = (int64_t)Dp + 2;
   size_t need = 0;
   if (most > kFewWhole) need += (size_t)((most > kFewLong ? kFewPieces : std::min(cus, kFewPieces)) * 16 * per_row) * 4;
-  // (calls with 256-row tiles have more items than CUs, which are not cut; those
-  // that have fewer items in 128-row tiles than CUs are)
-  if (most > kManyChunk && rows * group > 32) need += (size_t)((int64_t)std::min(cus, kManyPieces) * 128 * per_row) * 4;
+  // (calls with 256-row tiles have more items than CUs and are not cut)
+  if (most > kManyChunk && rows * group > 32)
+    need += (size_t)((int64_t)(most > kManyLong ? kManyPieces : std::min(cus, kManyPieces)) * 128 * per_row) * 4;
   return need;
 }
 

@@ -177,7 +177,7 @@ int main() {
     CHECK(!p.few || (p.few_chunk >= kFewChunk && p.few_chunk % 16 == 0));
     CHECK(!p.many || (p.many_chunk >= kManyChunk && p.many_chunk % 64 == 0));
     CHECK((p.few_pieces > 1) <= (p.few_items * p.few_pieces <= kFewPieces));
-    CHECK((p.many_pieces > 1) <= (p.many_items * p.many_pieces <= cus));
+    CHECK((p.many_pieces > 1) <= (p.many_items * p.many_pieces <= kManyPieces));
   }
   printf("%d %ld %ld\n", calls, rows_seen, pieces_seen);
   return 0;
