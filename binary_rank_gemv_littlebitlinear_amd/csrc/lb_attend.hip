@@ -198,7 +198,15 @@ __device__ __forceinline__ float4_t load4(const float *p) {
 
 // ------------------------------------------------------------- few rows
 // 16 rows a workgroup, whose waves share out the keys of a piece and read them
-// from memory straight into operands; the waves' sums are joined in LDS.
+// from memory straight into operands; the waves' sums are joined in LDS.  A step of
+// a wave is 32 keys: their scores, weights and values while the next 32 are on
+// their way.  Bound by reading where there are keys enough (131072 keys of 8 heads
+// of 128, 64 query heads: 268 MB in 55 us, 4.9 TB/s), by latency where there are few
+// (512 keys of 32 heads 7.6 us), and between them by vector instructions, of which
+// the bytes' conversion to fp16 is nearly half: 64 sequences of 256 to 4096 keys take
+// 48 us, 191 MB at 4.0 TB/s.  Eight waves in 128 registers, two workgroups a CU (four
+// waves with more registers took 64 us for 131072 keys and 107 for 128 sequences, these
+// 63 and 96 at that time).
 // Row tile `tile` of key head h of sequence b, one piece of its keys, by W waves.
 template <int NC, int W>
 __device__ __forceinline__ void few_rows(const AttendArgs &A, int b, int h, int tile, int piece, float *sh) {
@@ -409,8 +417,8 @@ __device__ __forceinline__ void few_rows(const AttendArgs &A, int b, int h, int 
   }
   if (pieces == 1 || !A.count) return;
 
-  // The item's last workgroup to arrive joins its pieces (a launch of its own for
-  // that took 4 to 6 us more).  Partial sums go past the caches, every wave's before
+  // The item's last workgroup to arrive joins its pieces (with a launch for that 64
+  // sequences took 65 us, not 59).  Partial sums go past the caches, every wave's before
   // the workgroup counts itself, and are read the same way.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -496,6 +504,13 @@ __device__ __forceinline__ void here(const T &v) {
 // 2 t + 2 and values of halves 2 t and 2 t + 1, and write keys of the two halves
 // behind and values of tile t + 1: there is room for four halves of keys and two
 // tiles of values, so nothing is written that a slower wave may still read.
+//
+// Bound by vector instructions beside the matrix instructions.  A prompt of 4096 of
+// 32 heads of 128 takes 180 us (137 GFLOP, 763 TFLOP/s; all keys for all rows 326 us,
+// 833; a large library product reaches 1200).  Steps on the way there: 249 us with a
+// tile's scores, weights and sums one after the other, 195 with the next tile's scores
+// made meanwhile, 182 in halves with exponentials between the matrix instructions and
+// operands read four of those ahead.  16 heads: 160 wide 203 us, 192 234, 256 271.
 template <int NC, int NW>
 __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
   constexpr int Dp = NC * 32, kPairs = NC / 2, kOdd = NC & 1, kUnit = Dp * 16, NT = NC, TR = NW * 32;
