@@ -59,7 +59,8 @@ constexpr int kJoinHere = 64;  // pieces up to which the last workgroup of k_att
 __host__ __device__ constexpr int few_floats(int rows, int Dp, int waves) {
   return waves * rows * (Dp + 4) > 2 * kJoinHere * 16 ? waves * rows * (Dp + 4) : 2 * kJoinHere * 16;
 }
-constexpr int kJoinWave = 8;  // pieces of a row up to which a wave joins it, not a workgroup
+constexpr int kJoinShort = 8;  // pieces up to which k_attend_join_short joins them
+constexpr int kJoinRows = 32;  // rows that a workgroup of it has
 
 struct AttendArgs {
   Sequences S;
@@ -838,29 +839,27 @@ __global__ void __launch_bounds__(NW * 64, NC <= 4 ? 2 : 1) k_attend_many(Attend
 }
 
 // --------------------------------------------------------------- joining
-// The pieces of a row, by NT threads: their weights first, then each group of
+// The pieces of a row, by a workgroup: their weights first, then each group of
 // Dp / 4 threads adds up every so-manieth piece, and the groups meet in LDS.
 // TR = 16: of k_attend_few.  (One wave a row that went through the pieces in
 // turn took 127 us for 256 pieces of 64 rows of 128.)
-template <int TR, int NT>
+template <int TR>
 __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
-  constexpr int kPer = 256 / NT, kMost = TR == 16 ? kFewPieces : kManyPieces;
-  __shared__ float weight[kPer][NT == 64 ? kJoinWave : kMost];
+  __shared__ float weight[TR == 16 ? kFewPieces : kManyPieces];
   __shared__ float4_t sums[256];
   __shared__ float wave[2][4];
   const int rows = TR == 16 ? A.frows : TR;  // of an item's partial sums
-  const int t = threadIdx.x % NT, mine = threadIdx.x / NT;
-  const unsigned at = blockIdx.x * kPer + (NT == 64 ? wave_id() : 0);
-  const unsigned item = at / (unsigned)rows;
-  const int row = (int)(at - item * rows);
+  const int t = threadIdx.x;
+  const unsigned item = blockIdx.x / (unsigned)rows;
+  const int row = (int)(blockIdx.x - item * rows);
   Item it;
   if constexpr (TR == 16) {
     const unsigned bh = item / (unsigned)A.tiles, b = bh / (unsigned)A.KV;
-    if (b >= (unsigned)A.S.n || !few_item(A, (int)b, (int)(bh - b * A.KV), (int)(item - bh * A.tiles), it)) return;
+    if (!few_item(A, (int)b, (int)(bh - b * A.KV), (int)(item - bh * A.tiles), it)) return;
   } else {
     const unsigned slot = item / (unsigned)A.KV;
     int b;
-    if (slot >= (unsigned)A.row_tiles || !many_item<TR>(A, (int)slot, (int)(item - slot * A.KV), it, &b)) return;
+    if (!many_item<TR>(A, (int)slot, (int)(item - slot * A.KV), it, &b)) return;
   }
   const int pieces = pieces_of(it.lo, it.hi, TR == 16 ? A.few_chunk : A.chunk);
   if (pieces == 1 || row >= it.n) return;
@@ -868,35 +867,28 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
   const float *part = TR == 16 ? A.few_part + (int64_t)item * A.few_pieces * size : A.part + (int64_t)item * A.pieces * size;
   const float *ml = part + rows * Dp + 2 * row;
   float M = kNothing;
-  for (int p = t; p < pieces; p += NT) {
+  for (int p = t; p < pieces; p += 256) {
     const float v = ml[p * size];
-    weight[mine][p] = v;
+    weight[p] = v;
     M = fmaxf(M, v);
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) M = fmaxf(M, lane_xor(M, d));
-  if constexpr (NT > 64) {
-    if ((t & 63) == 0) wave[0][t >> 6] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(wave[0][0], wave[0][1]), fmaxf(wave[0][2], wave[0][3]));
-  }
+  if ((t & 63) == 0) wave[0][t >> 6] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(wave[0][0], wave[0][1]), fmaxf(wave[0][2], wave[0][3]));
   float L = 0.f;
-  for (int p = t; p < pieces; p += NT) {
-    const float f = __builtin_amdgcn_exp2f(weight[mine][p] - M);
-    weight[mine][p] = f;
+  for (int p = t; p < pieces; p += 256) {
+    const float f = __builtin_amdgcn_exp2f(weight[p] - M);
+    weight[p] = f;
     L += ml[p * size + 1] * f;
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) L += lane_xor(L, d);
-  if constexpr (NT > 64) {
-    if ((t & 63) == 0) wave[1][t >> 6] = L;
-    __syncthreads();
-    L = wave[1][0] + wave[1][1] + wave[1][2] + wave[1][3];
-  } else {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  }
-  const int per = Dp / 4, groups = NT / per, g = t / per, d = (t - g * per) * 4;
+  if ((t & 63) == 0) wave[1][t >> 6] = L;
+  __syncthreads();
+  L = wave[1][0] + wave[1][1] + wave[1][2] + wave[1][3];
+  const int per = Dp / 4, groups = 256 / per, g = t / per, d = (t - g * per) * 4;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
   if (g < groups) {
     const float *from = part + row * Dp + d;
@@ -906,29 +898,59 @@ __global__ void __launch_bounds__(256) k_attend_join(AttendArgs A, int Dp) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = *(const float4a_t *)(from + (p + i * groups) * size);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o += v[i] * weight[mine][p + i * groups];
+      for (int i = 0; i < 4; ++i) o += v[i] * weight[p + i * groups];
     }
-    for (; p < pieces; p += groups) o += *(const float4a_t *)(from + p * size) * weight[mine][p];
+    for (; p < pieces; p += groups) o += *(const float4a_t *)(from + p * size) * weight[p];
   }
-  sums[threadIdx.x] = o;
-  if constexpr (NT > 64) {
-    __syncthreads();
-  } else {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  }
+  sums[t] = o;
+  __syncthreads();
   if (g > 0) return;
-  for (int i = 1; i < groups; ++i) o += sums[threadIdx.x + i * per];
+  for (int i = 1; i < groups; ++i) o += sums[t + i * per];
   write4(A, it, row, d, o, L);
 }
 
+// The same of up to kJoinShort pieces of k_attend_many's items: a lane has four dims
+// of a row and all of its pieces.  (A wave a row took 18 us for 4096 rows of 8 heads of
+// 128 with up to 4 pieces, this 10; with 12 pieces of 64 rows it takes 3 us more than a
+// workgroup a row, with 32 of them 13 more.)
 template <int TR>
-hipError_t launch_join(const AttendArgs &A, int64_t rows, int Dp, hipStream_t st) {
-  if ((TR == 16 ? A.few_pieces : A.pieces) <= kJoinWave)
-    k_attend_join<TR, 64><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(A, Dp);
-  else
-    k_attend_join<TR, 256><<<dim3((unsigned)rows), dim3(256), 0, st>>>(A, Dp);
-  return hipGetLastError();
+__global__ void __launch_bounds__(256) k_attend_join_short(AttendArgs A, int Dp) {
+  static_assert(TR % kJoinRows == 0, "whole workgroups");
+  const unsigned item = blockIdx.x / (TR / kJoinRows), slot = item / (unsigned)A.KV;
+  const int r0 = (int)(blockIdx.x % (TR / kJoinRows)) * kJoinRows;
+  Item it;
+  int b;
+  if (!many_item<TR>(A, (int)slot, (int)(item - slot * A.KV), it, &b)) return;
+  const int pieces = pieces_of(it.lo, it.hi, A.chunk), end = min(it.n, r0 + kJoinRows);
+  const int lanes = Dp <= 128 ? 32 : 64, d = (threadIdx.x % lanes) * 4;
+  if (pieces == 1 || d >= Dp) return;
+  const int64_t size = (int64_t)TR * (Dp + 2);
+  const float *part = A.part + (int64_t)item * A.pieces * size;
+  for (int row = r0 + threadIdx.x / lanes; row < end; row += 256 / lanes) {
+    float2_t ml[kJoinShort];
+    float4_t v[kJoinShort];
+    float M = kNothing;
+#pragma unroll
+    for (int p = 0; p < kJoinShort; ++p) {
+      ml[p] = float2_t{kNothing, 0.f};
+      v[p] = float4_t{0.f, 0.f, 0.f, 0.f};
+      if (p >= pieces) continue;
+      const float *from = part + p * size;
+      ml[p] = *(const float2_t *)(from + TR * Dp + 2 * row);
+      v[p] = *(const float4a_t *)(from + row * Dp + d);
+    }
+#pragma unroll
+    for (int p = 0; p < kJoinShort; ++p) M = fmaxf(M, ml[p][0]);
+    float L = 0.f;
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < kJoinShort; ++p) {
+      const float w = __builtin_amdgcn_exp2f(ml[p][0] - M);
+      o += v[p] * w;
+      L += ml[p][1] * w;
+    }
+    write4(A, it, row, d, o, L);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1004,8 +1026,15 @@ hipError_t launch_many(AttendArgs A, const Plan &p, hipStream_t st) {
   A.blocks = (unsigned)(p.many_items * p.many_pieces);
   k_attend_many<NC, NW><<<dim3((unsigned)(A.blocks + p.few_items * p.few_pieces)), dim3(NW * 64), lds, st>>>(A);
   e = hipGetLastError();
-  if (e != hipSuccess || p.many_pieces == 1) return e;
-  return launch_join<NW * 32>(A, p.many_items * (NW * 32), NC * 32, st);
+  if constexpr (NW == 4) {  // (256-row tiles are not cut)
+    if (e != hipSuccess || p.many_pieces == 1) return e;
+    if (p.many_pieces <= kJoinShort)
+      k_attend_join_short<128><<<dim3((unsigned)(p.many_items * (128 / kJoinRows))), dim3(256), 0, st>>>(A, NC * 32);
+    else
+      k_attend_join<128><<<dim3((unsigned)(p.many_items * 128)), dim3(256), 0, st>>>(A, NC * 32);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 template <int NC>
@@ -1019,7 +1048,8 @@ hipError_t launch(const AttendArgs &A, const Plan &p, hipStream_t st) {
     e = launch_many<NC, 4>(A, p, st);
   }
   if (e != hipSuccess || !p.few || p.few_pieces == 1 || A.count) return e;
-  return launch_join<16>(A, p.few_items * p.frows, NC * 32, st);
+  k_attend_join<16><<<dim3((unsigned)(p.few_items * p.frows)), dim3(256), 0, st>>>(A, NC * 32);
+  return hipGetLastError();
 }
 
 // The chunk of 32 dims as a constant.

@@ -179,8 +179,8 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
     p.many_items = (int64_t)p.row_tiles * KV;
     // The same here, while there is little more than an item for each CU (a CU has room
     // for two) and keys enough to pay for joining.  In pieces of 1024 and whole: a prompt
-    // of 4096 with 8 heads of 128 91 us and 131, of 256 205 and 323; 6 chunks of 300 rows
-    // of up to 8000 keys, 32 heads on 8, 146 and 244; 500 rows of 9000 keys, 32 heads, 143
+    // of 4096 with 8 heads of 128 85 us and 131, of 256 200 and 323; 6 chunks of 300 rows
+    // of up to 8000 keys, 32 heads on 8, 140 and 244; 500 rows of 9000 keys, 32 heads, 138
     // and 159.  But a prompt of 1500 with 32 heads 75 and 59, the last 1500 rows of 4500
     // keys (400 items) 196 and 167 in pieces of 2250.
     const int64_t span = span_of(p.tr);
