@@ -297,6 +297,17 @@ def test_uneven_lengths(lbm, sequences, heads, longest):
     _run(lbm, cache, ref, c, rng, "uneven, window", start=False, window=longest - 100)
 
 
+@pytest.mark.parametrize("rows,length,kv,heads,dim", [(260, 4200, 24, 24, 32), (130, 9300, 24, 24, 40), (130, 5000, 12, 36, 160)])
+def test_chunks_of_long_pieces(lbm, rows, length, kv, heads, dim):
+    """Chunks with about a row tile for every third CU, whose keys are cut into long pieces: few and many of them."""
+    say(f"[case] attend long pieces rows={rows} length={length}")
+    rng = np.random.default_rng(rows)
+    c = cacheref.Case(rng, [length, 900], [rows, 1], 64, kv, heads, dim)
+    cache, ref = _filled(lbm, c, rng)
+    _run(lbm, cache, ref, c, rng, "long pieces")
+    _run(lbm, cache, ref, c, rng, "long pieces, window", window=4100)
+
+
 def test_shared_pages_and_repeats(lbm):
     """Two sequences with a common prefix read the same pages; the same call gives the same bits."""
     torch = lbtest.torch_dev()
