@@ -504,7 +504,8 @@ __device__ __forceinline__ void here(const T &v) {
 // h + 1.  Between two barriers (tile t) the waves read keys of halves 2 t + 1 and
 // 2 t + 2 and values of halves 2 t and 2 t + 1, and write keys of the two halves
 // behind and values of tile t + 1: there is room for four halves of keys and two
-// tiles of values, so nothing is written that a slower wave may still read.
+// tiles of values, so nothing is written that a slower wave may still read.  Half 0,
+// which is read before all of that, has a barrier of its own (walk_tiles).
 //
 // Bound by vector instructions beside the matrix instructions.  A prompt of 4096 of
 // 32 heads of 128 takes 180 us (137 GFLOP, 763 TFLOP/s; all keys for all rows 326 us,
@@ -608,14 +609,14 @@ __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
       const bool values = is_values(i);
-      const int part = 2 * tile + 1 + (su >> 1);  // of keys
-      char *to = smem + (values ? (2 + (tile & 1)) * kHalf : (part & 3) * (kHalf / 2));
+      const int part = put_half(tile) + (su >> 1);  // of keys
+      char *to = smem + (values ? (2 + values_place(tile)) * kHalf : keys_place(part) * (kHalf / 2));
       if (lane == 0) {
         // Keys: the factor of a score, tiny instead of 0 (of a page of zeros, whose
         // scores are 0) so that it keeps a masked -inf.  Values: log2 of the scale.
         float v = f[i].scale;
         if (v != kMissing) v = values ? __log2f(v) : v * A.qscale == 0.f ? 1e-30f : v * A.qscale;
-        scales[values ? 16 + (tile & 1) * 4 + su : (part & 7) * 2 + (su & 1)] = v;
+        scales[values ? 16 + values_place(tile) * 4 + su : keys_scale_place(part) * 2 + (su & 1)] = v;
       }
       if (!values) {
         // [dim / 8][key 32][8]
@@ -656,7 +657,7 @@ __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
     i -= kSteps;
     return *(const half8_t *)(vb + (i / NT * 2 * Dp + i % NT * 32) * 16);
   };
-  const auto keys_at = [&](int part) { return smem + (part & 3) * (kHalf / 2) + lane * 16; };
+  const auto keys_at = [&](int part) { return smem + keys_place(part) * (kHalf / 2) + lane * 16; };
   // The first product of half a tile (32 keys) alone.
   const auto score = [&](int part) {
     const char *kb = keys_at(part);
@@ -672,12 +673,12 @@ __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
   const auto step = [&](int tile, int half, float16_t z) {
     const int t0 = c0 + tile * 64 + half * 32, part = 2 * tile + half;
     if (t0 >= some_last || t0 + 32 <= some_first) return score(part + 1);
-    const char *kb = keys_at(part + 1), *vb = smem + (2 + (tile & 1)) * kHalf + ((half * 4 + G) * Dp + n) * 16;
+    const char *kb = keys_at(part + 1), *vb = smem + (2 + values_place(tile)) * kHalf + ((half * 4 + G) * Dp + n) * 16;
     half8_t ring[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) ring[i] = operand(kb, vb, i);
-    const float2_t ks = *(const float2_t *)(scales + (part & 7) * 2);
-    const float2_t vs = *(const float2_t *)(scales + 16 + (tile & 1) * 4 + half * 2);
+    const float2_t ks = *(const float2_t *)(scales + keys_scale_place(part) * 2);
+    const float2_t vs = *(const float2_t *)(scales + 16 + values_place(tile) * 4 + half * 2);
     // Units that are missing or have no finite scale are rare: the rest of the step
     // gets stand-ins for their scales.
     float2_t factor = ks, share = vs;
@@ -767,30 +768,29 @@ __device__ __forceinline__ void many_rows(const AttendArgs &A, char *smem) {
 
   float16_t z = none;
   int page[kKinds];
-  if (tiles > 0) {
-    int p0[kKinds];
-    look_up(-1, p0);
-    look_up(0, page);
-    fetch(-1, p0);  // keys of half 0 (and values of none)
-    put(-1);
-    fetch(0, page);
-    look_up(1, page);
-    put(0);
-    fetch(1, page);
-    look_up(2, page);
-  }
-  __syncthreads();
-  if (tiles > 0) z = score(0);
-  for (int tile = 0; tile < tiles; ++tile) {
-    z = step(tile, 0, z);
-    // here rather than before the barrier, so that one wave's conversions run
-    // beside another's matrix instructions
-    put(tile + 1);
-    fetch(tile + 2, page);
-    look_up(tile + 3, page);
-    z = step(tile, 1, z);
-    __syncthreads();
-  }
+  walk_tiles(
+      tiles,
+      [&] {
+        int p0[kKinds];
+        look_up(-1, p0);
+        look_up(0, page);
+        fetch(-1, p0);  // keys of half 0 (and values of none)
+        put(-1);
+        fetch(0, page);
+        look_up(1, page);
+        put(0);
+        fetch(1, page);
+        look_up(2, page);
+      },
+      [&](int part) { z = score(part); }, [&](int tile, int half) { z = step(tile, half, z); },
+      [&](int tile) {
+        // here rather than before the barrier, so that one wave's conversions run
+        // beside another's matrix instructions
+        put(tile);
+        fetch(tile + 1, page);
+        look_up(tile + 2, page);
+      },
+      [] { __syncthreads(); });
   l += other32(l);
   if (w * 32 + n >= it.n) return;
   const float r = __builtin_amdgcn_exp2f(lr);

@@ -99,6 +99,36 @@ LB_HD void keys_of_rows(const View &A, const Sequence &q, int r0, int n, int *lo
   if (*lo >= *hi) *lo = *hi = 0;
 }
 
+// Where k_attend_many keeps its tiles of 64 keys in LDS: halves of 32 keys (half h of
+// tile t is number 2 t + h) in four places and their scales in eight, tiles of values
+// and their scales in two.  Tile t of values is put there together with halves 2 t + 1
+// and 2 t + 2 of keys, of which the first product is a half ahead of the rest.
+LB_HD int keys_place(int half) { return half & 3; }
+LB_HD int keys_scale_place(int half) { return half & 7; }
+LB_HD int values_place(int tile) { return tile & 1; }
+LB_HD int put_half(int tile) { return 2 * tile + 1; }
+
+// The order of a workgroup's work on them.  `begin` puts half 0 and tile 0; `score` makes
+// a half's first product; `weigh` has the rest of a half, and the first product of the
+// half behind it; `put` puts a tile.  Between two barriers no wave puts what another may
+// still read: the one behind score(0) keeps put(1), whose half 4 takes the place of half
+// 0, behind the slowest wave's reading of that.
+template <typename Begin, typename Score, typename Weigh, typename Put, typename Barrier>
+LB_HD void walk_tiles(int tiles, const Begin &begin, const Score &score, const Weigh &weigh, const Put &put,
+                      const Barrier &barrier) {
+  if (tiles < 1) return;
+  begin();
+  barrier();
+  score(0);
+  barrier();
+  for (int tile = 0; tile < tiles; ++tile) {
+    weigh(tile, 0);
+    put(tile + 1);
+    weigh(tile, 1);
+    barrier();
+  }
+}
+
 LB_HD int pieces_of(int lo, int hi, int chunk) { return imax(1, (int)(((int64_t)hi - lo + chunk - 1) / chunk)); }
 
 // How an attention call is cut up.  A sequence of up to few_rows rows (tokens x
