@@ -972,7 +972,8 @@ lb_status grow(lb_cache *C, size_t need, const char *who, bool in_call, hipStrea
                                            "lb_cache_reserve first");
   }
   void *t = nullptr;
-  hipError_t e = hipMalloc(&t, kCountBytes + need);
+  const size_t bytes = grown_bytes(C->Dp, C->cus, C->ws_bytes, need);
+  hipError_t e = hipMalloc(&t, kCountBytes + bytes);
   if (e != hipSuccess) return set_error(LB_ENOMEM, pre + "hipMalloc: " + hipGetErrorString(e));
   k_attend_clear<<<dim3(1), dim3(1024), 0, st>>>((unsigned *)t);
   e = hipGetLastError();
@@ -991,7 +992,7 @@ lb_status grow(lb_cache *C, size_t need, const char *who, bool in_call, hipStrea
     }
   }
   C->ws = t;
-  C->ws_bytes = need;
+  C->ws_bytes = bytes;
   return LB_OK;
 }
 

@@ -239,4 +239,12 @@ inline size_t reserve_bytes(int Dp, int cus, int64_t rows, int group, int64_t mo
   return need;
 }
 
+// The size of the workspace that takes the place of one of `have` bytes when a call needs
+// more: twice that, up to what any call may need.  Outgrown ones are kept (captured graphs
+// use them), so a size that followed each call's need would pile up as lengths grow:
+// chunks of 16 tokens of a prompt of 131072 with 32 heads of 128 on one would keep 2.7 GB.
+inline size_t grown_bytes(int Dp, int cus, size_t have, size_t need) {
+  return std::max(need, std::min(2 * have, reserve_bytes(Dp, cus, kMaxTokens, 1, kMaxTokens)));
+}
+
 }  // namespace lbi
