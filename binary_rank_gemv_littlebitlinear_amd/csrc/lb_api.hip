@@ -24,6 +24,8 @@ static thread_local std::string g_last_error;
 
 static lb_status fail(lb_status st, const std::string &msg) {
   g_last_error = msg;
+  // told here: the runtime would tell the caller's next launch again
+  if (st == LB_EHIP || st == LB_ENOMEM) (void)hipGetLastError();
   return st;
 }
 

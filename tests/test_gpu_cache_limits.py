@@ -42,3 +42,18 @@ def test_rows_of_no_sequences(lbm, rows):
     fresh.read(back[2], back[3], *seq, start=lbtest.to_dev(c.start))
     assert torch.equal(back[0], back[2]) and torch.equal(back[1], back[3])
     torch.cuda.synchronize()
+
+
+def test_after_a_cache_that_does_not_fit(lbm):
+    """A cache of 8.8 TB is refused, and the calls behind it are not told of that."""
+    torch = lbtest.torch_dev()
+    say("[case] cache that does not fit")
+    r, x = torch.randn((2, 64), device="cuda"), torch.empty((2, 64), dtype=torch.float16, device="cuda")
+    for _ in range(2):
+        with pytest.raises(lbm.LBError) as ei:
+            lbm.Cache(2 ** 31 - 1, 16, 1, 256)
+        assert ei.value.status == lbm.LB_ENOMEM
+        lbm.lb_norm(r, x=x)
+    torch.cuda.synchronize()
+    want = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-5)
+    assert (x.float() - want).abs().max() < 1e-2  # (test_gpu_norm has its tolerances)
