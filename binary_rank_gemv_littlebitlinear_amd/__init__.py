@@ -561,9 +561,18 @@ def lb_norm(r, x=None, y=None, out=None, kind="rms", weight=None, bias=None, pos
                LB_F32 if rtype is _f32 else LB_F16, w, b, eps, po, ldo, px, ldx, rows, width, _stream_of(stream, dev))
 
 
+def _int32(name, v):
+    """A number for a C int, which ctypes would cut to its lower bits."""
+    v = int(v)
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} must fit 32 bits, not {v}")
+    return v
+
+
 def lb_cache_create(pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
     out = C.c_void_p()
-    _check(load_library().lb_cache_create(int(pages), int(page_tokens), int(kv_heads), int(head_dim), C.byref(out)))
+    _check(load_library().lb_cache_create(int(pages), _int32("page_tokens", page_tokens), _int32("kv_heads", kv_heads),
+                                          _int32("head_dim", head_dim), C.byref(out)))
     return out.value
 
 
@@ -575,7 +584,7 @@ def lb_cache_shape(cache: int):
 
 
 def lb_cache_reserve(cache: int, rows: int, heads: int, sequences: int, max_length: int):
-    _check(load_library().lb_cache_reserve(cache, int(rows), int(heads), int(sequences), int(max_length)))
+    _check(load_library().lb_cache_reserve(cache, int(rows), _int32("heads", heads), int(sequences), int(max_length)))
 
 
 def _sequences(rows, lengths, table, start, dev):
@@ -647,7 +656,8 @@ def lb_cache_attend(cache, q, out, lengths, table, start=None, max_length=None, 
     po, ldo = _like("out", out, rows, heads * cache.head_dim, _only_f16, dev)
     _check(_lib.lb_cache_attend(cache.handle, pq, ldq, heads, po, ldo, *_sequences(rows, lengths, table, start, dev),
                                 int(max_length or 0), cache.head_dim ** -0.5 if scale is None else scale,
-                                1 if causal else 0, window, _stream_of(stream, dev)))
+                                1 if causal else 0, max(-1, min(window, 0x7fffffff)),  # (any wider one hides nothing)
+                                _stream_of(stream, dev)))
 
 
 def lb_cache_destroy(cache: int):

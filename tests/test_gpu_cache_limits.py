@@ -57,3 +57,25 @@ def test_after_a_cache_that_does_not_fit(lbm):
     torch.cuda.synchronize()
     want = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-5)
     assert (x.float() - want).abs().max() < 1e-2  # (test_gpu_norm has its tolerances)
+
+
+def test_windows_past_32_bits(lbm):
+    """A window wider than any position hides nothing, whatever its lower bits; below zero there is none."""
+    torch = lbtest.torch_dev()
+    say("[case] windows past 32 bits")
+    rng = np.random.default_rng(3)
+    c = cacheref.Case(rng, [90, 40], [50, 1], 16, 1, 2, 64)
+    cache = lbm.Cache(c.pages, 16, 1, 64)
+    x, start = lbtest.to_dev(c.rows(rng, 130, 64)), lbtest.to_dev(np.array([0, 90, 130], np.int32))
+    seq = (lbtest.to_dev(c.lengths), lbtest.to_dev(c.table))
+    cache.append(x, x, *seq, start=start)
+    q = lbtest.to_dev(c.rows(rng, 51, 128))
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    cache.attend(q, want, *seq, start=lbtest.to_dev(c.start))
+    for window in (2 ** 31, 2 ** 32 - 1, 2 ** 32 + 5, 2 ** 63 - 1):
+        out.fill_(float("nan"))
+        cache.attend(q, out, *seq, start=lbtest.to_dev(c.start), window=window)
+        assert torch.equal(out, want), window
+    for window in (-2 ** 31, -2 ** 32 + 5, -2 ** 63):
+        with pytest.raises(lbm.LBError):
+            cache.attend(q, out, *seq, start=lbtest.to_dev(c.start), window=window)
