@@ -22,6 +22,7 @@
 #include <string>
 
 #include "lb_internal.h"
+#include "lb_norm.h"
 
 namespace {
 
@@ -357,28 +358,17 @@ extern "C" lb_status lb_norm(int kind, const void *y, int y_type, int64_t ldy, i
     W.x = (uint16_t *)at(x, ldx, 2);
     hipStream_t st = (hipStream_t)stream;
     hipError_t e;
-    // Threads of a row x pieces of each: many threads share out the latency of few
-    // rows, few need less of the machine for many.  4096 wide, 1 row: 512 x 1 3.3 us,
-    // 256 x 2 3.8, 1024 x 1 4.0 (4096 rows: 31.7, 31.6, 35.8).  8192 wide with a norm
-    // on each side, 1 row: 1024 x 1 4.6, 512 x 2 4.8, 256 x 4 6.2; 1023 rows: 21.0,
-    // 18.0, 18.2; 4096 rows: 77.1, 76.6, 81.4.  1031 wide: 64 x 3 and 256 x 1 take 8.6
-    // and 7.7 for 1023 rows, 15.2 and 19.9 for 4096.
-    if (width <= 512)
-      e = launch<64, 1>(W, st);
-    else if (width <= 1536 && W.rows >= 2048)
-      e = launch<64, 3>(W, st);
-    else if (width <= 2048)
-      e = launch<256, 1>(W, st);
-    else if (width <= 4096)
-      e = launch<512, 1>(W, st);
-    else if (width <= 8192 && W.rows >= 256)
-      e = launch<512, 2>(W, st);
-    else if (width <= 8192)
-      e = launch<1024, 1>(W, st);
-    else if (width <= 16384)
-      e = launch<1024, 2>(W, st);
-    else
-      e = launch<1024, 4>(W, st);
+    const NormShape shape = norm_shape(width, W.rows);
+    switch (shape.threads * 8 + shape.pieces) {
+      case 64 * 8 + 1: e = launch<64, 1>(W, st); break;
+      case 64 * 8 + 3: e = launch<64, 3>(W, st); break;
+      case 256 * 8 + 1: e = launch<256, 1>(W, st); break;
+      case 512 * 8 + 1: e = launch<512, 1>(W, st); break;
+      case 512 * 8 + 2: e = launch<512, 2>(W, st); break;
+      case 1024 * 8 + 1: e = launch<1024, 1>(W, st); break;
+      case 1024 * 8 + 2: e = launch<1024, 2>(W, st); break;
+      default: e = launch<1024, 4>(W, st);
+    }
     if (e != hipSuccess) return set_error(LB_EHIP, std::string("lb_norm: ") + hipGetErrorString(e));
   }
   return LB_OK;
