@@ -16,8 +16,10 @@
 // to be an fp16 operand: s_v / r, r the largest finite s_v so far (a change of
 // r scales the sums too), keeps it within 2^(kUp + kSlack), and 2^kUp lifts it
 // over fp16's small numbers.  The kernel for few rows, bound by reading the
-// keys, keeps it as two fp16 numbers (22 bits), so its result is that of fp32
-// arithmetic.  l is summed in fp32 from the weights before any rounding.
+// keys, keeps it as two fp16 numbers (22 bits), which leaves the scores' fp32
+// roundings as the larger ones.  The one for many rows, bound by matrix and vector
+// instructions, keeps one (off by up to 2^-11, the half step of out as well).  l is
+// summed in fp32 from the weights before any rounding.
 // Keys that a row does not see get weight 0 by selection, so that what lies
 // there (numbers of earlier owners, scales that are NaN) does not matter.
 //

@@ -591,7 +591,11 @@ lb_status lb_cache_read(const lb_cache *C, void *k, int64_t ldk, void *v, int64_
  * `sequences` sequences and max_length tokens, now. */
 lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int64_t sequences, int64_t max_length);
 
-/* out = softmax(scale * q K^T) V over the cache, fp32 inside, rounded once.
+/* out = softmax(scale * q K^T) V over the cache: exact products, scores,
+ * softmax and sums in fp32, out rounded once.  A weight times its page's scale
+ * of values enters the sum over V as two fp16 numbers (22 bits) where a
+ * sequence has up to 32 rows of a key head (or one token) in the call, and as
+ * one (11 bits) otherwise, lifted so that the largest is near 2^12.
  *   q, out    device fp16, rows x (heads * head_dim), row strides ldq, ldo;
  *             heads a multiple of kv_heads: head h reads key head
  *             h / (heads / kv_heads).  out must not overlap the inputs
