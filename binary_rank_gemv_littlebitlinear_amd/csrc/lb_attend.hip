@@ -165,10 +165,13 @@ __device__ __forceinline__ int64_t row_at(const AttendArgs &A, const Item &it, i
   return (int64_t)(it.q.row0 + tok) * ld + (int64_t)(it.h * A.view.group + j) * A.D;
 }
 
+// Infinities become NaN: the row's softmax is NaN either way, but scores of -inf alone
+// would look like those of a row that sees nothing.
 __device__ __forceinline__ half8_t load_q(const AttendArgs &A, int64_t at, int d) {
   u32x4_t w = {0, 0, 0, 0};
   if (d < A.D) w = *LB_LOOSE128(A.q + at + d);
-  return __builtin_bit_cast(half8_t, w);
+  const half8_t q = __builtin_bit_cast(half8_t, w);
+  return q + q * (_Float16)0.f;
 }
 
 // Four of a row's outputs, from its sum and weights.

@@ -605,7 +605,8 @@ lb_status lb_cache_reserve(lb_cache *C, int64_t rows, int heads, int64_t sequenc
  *   causal    a row sees its sequence's tokens up to its own position;
  *             otherwise all of them
  *   window    with causal: the last `window` of those only; 0 for all
- * A row that sees no token gets zeros. */
+ * A row that sees no token gets zeros; one that does, with an infinity or a
+ * NaN in its q, NaN. */
 lb_status lb_cache_attend(lb_cache *C, const void *q, int64_t ldq, int heads, void *out, int64_t ldo,
                           const int32_t *start, const int32_t *lengths, const int32_t *table, int64_t ldt,
                           int columns, int sequences, int64_t rows, int64_t max_length, float scale, int causal,
