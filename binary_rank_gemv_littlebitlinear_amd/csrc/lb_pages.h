@@ -150,11 +150,26 @@ constexpr int kFewPieces = 2048;  // the most of a call of k_attend_few
 constexpr int kManyLong = 1024;   // (again, one that evens out the work)
 constexpr int kManyPieces = 1024;  // the most of a call of k_attend_many
 
-// Rows of a tile of k_attend_many: 256 where registers allow it (Dp <= 128) and
-// such tiles fill the GPU twice, else 128 (two workgroups a CU).  32 heads of 128,
-// 256 against 128 rows: a prompt of 4096 (544 items of 256) 183 us against 205, of
-// 2048 (288) 87 against 78, of 1024 (160) 51 against 42, of 256 (64) 19 against 16.
-inline int many_tile(int Dp, int cus, int64_t items256) { return Dp <= 128 && items256 > 2 * cus ? 256 : 128; }
+// Rows of a tile of k_attend_many: 256 where registers allow it (Dp <= 128), the GPU has
+// more than two such tiles a CU and they are full of work, else 128 (two workgroups a CU).
+// 256 against 128 rows, us, 128 wide:
+//   tiles enough      32 heads: a prompt of 4096 (544 items of 256) 177 and 201, two of 4096
+//                     352 and 364; of 2048 (288 items) 87 and 78; 64 heads, 2048, 105 and 113
+//   rows enough, five tiles a sequence: a last tile is half empty on the average, every
+//                     sequence has a place in the grid, and those with few rows run in
+//                     workgroups of the same size.  32 heads: 16 prompts of 600 160 and 128,
+//                     16 chunks of 300 of 4096 keys 637 and 538, a prompt of 4096 beside 60
+//                     tokens 335 and 294; 64 heads on 8, 100 tokens beside 8 chunks of 100
+//                     103 and 75; but 16 chunks of 256 of 4096 358 and 379
+//   keys enough, 2048, a window 4096: of 256 rows' keys more are hidden from some of them.
+//                     32 heads: 8 prompts of 1024 148 and 139, 6 of 1500 192 and 190, 4 of
+//                     2048 206 and 212; one of 8192 644 and 675, with a window of 4096 512 and
+//                     529, of 2048 364 and 343, of 1024 232 and 215
+inline int many_tile(int KV, int Dp, int cus, int64_t rows, int64_t n, const View &A) {
+  const int64_t all = rows * A.group;
+  const bool full = (all / 256 + n) * KV > 2 * cus && all >= 5 * 256 * n;
+  return Dp <= 128 && full && A.most >= 2048 && (A.window == 0 || A.window >= 4096) ? 256 : 128;
+}
 
 // Pieces of an item's keys: about `target` for all items together, of `least`
 // keys or more; `span` bounds an item's keys.
@@ -169,7 +184,7 @@ inline Plan plan_of(int KV, int Dp, int cus, bool starts, int64_t rows, int64_t 
   Plan p;
   const int group = A.group;
   const int64_t per_row = (int64_t)Dp + 2;
-  p.tr = many_tile(Dp, cus, (rows * group / 256 + n) * KV);
+  p.tr = many_tile(KV, Dp, cus, rows, n, A);
   if (!starts) {
     p.few = true;
     p.few_rows = group;

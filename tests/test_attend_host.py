@@ -7,7 +7,8 @@ import subprocess
 import numpy as np
 import pytest
 
-from tests import attendcases
+from tests import attendcases, cacheref
+from tests.attendcases import WINDOWS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FLAGS = ["-std=c++17", "-O1", "-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-Wall", "-Wextra", "-Werror"]
@@ -35,12 +36,40 @@ def test_growing_lengths_keep_little(tmp_path):
 
 
 def test_calls_of_wide_tiles(tmp_path):
-    """The calls of test_gpu_attend_wide_tiles have tiles of 256 rows, not cut, for every padded width up to 128."""
+    """The calls of test_gpu_attend_wide_tiles have tiles of 256 rows, not cut, for every padded width up to 128; with
+    fewer rows a sequence, a narrower window or wider heads they would not have them."""
     widths = set()
     for name, kw in attendcases.WIDE.items():
         c = attendcases.wide(np.random.default_rng(0), **kw)
-        for window in (0, 1, 37, 48, 60, 150):
+        for window in WINDOWS + (4200,):
             args = attendcases.plan_arguments(c, window)
             assert native(tmp_path, "plan_print", *args).split()[:2] == ["256", "1"], (name, window)
         widths.add(args[1])
     assert widths == {32, 64, 96, 128}
+    assert native(tmp_path, "plan_print", *attendcases.plan_arguments(c, 4095)).split()[0] == "128"
+    c.dim = 136
+    assert native(tmp_path, "plan_print", *attendcases.plan_arguments(c)).split()[0] == "128"
+    # a batch with chunks of 600 rows on 33 heads, and a chunk among 127 tokens
+    for lengths, new, heads in (([3000] * 16, [600] * 16, 33), ([3000] * 128, [100] + [1] * 127, 8)):
+        c = cacheref.Case(np.random.default_rng(0), lengths, new, 64, heads, heads, 128)
+        assert native(tmp_path, "plan_print", *attendcases.plan_arguments(c)).split()[0] == "128"
+
+
+def test_reference_by_products():
+    """attendcases.attend is cacheref.attend."""
+    rng = np.random.default_rng(2)
+    c = cacheref.Case(rng, [60, 1, 33], [25, 1, 33], 16, 2, 4, 24)
+    ref = cacheref.Cache(c.pages, 16, 2, 24)
+    start = np.array([0, 60, 61, 94])
+    x = [c.rows(rng, 94, 48) for _ in range(2)]
+    x[0][5, 2], x[1][70, 40] = np.nan, np.inf
+    c.table[0, 2] = -1
+    with np.errstate(invalid="ignore"):
+        ref.append(*x, c.lengths, c.table, start)
+        q = c.rows(rng, 59, 96)
+        for kw in (dict(), dict(causal=False), dict(window=20)):
+            lengths = np.array([20, 1, 33]) if kw else c.lengths
+            a, b = (f(ref, q, lengths, c.table, c.start, **kw) for f in (cacheref.attend, attendcases.attend))
+            assert np.array_equal(np.isnan(a[0]), np.isnan(b[0])) and np.isnan(a[0]).any() and not np.isnan(a[0]).all()
+            good = ~np.isnan(a[0])
+            assert np.allclose(a[0][good], b[0][good], rtol=0, atol=1e-12) and np.allclose(a[1][good], b[1][good], rtol=1e-6)
