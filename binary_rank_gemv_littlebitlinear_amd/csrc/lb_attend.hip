@@ -143,7 +143,7 @@ __device__ __forceinline__ bool few_item(const AttendArgs &A, int b, int h, int 
 // Item of k_attend_many: row tile `slot` of all sequences' tiles of TR rows, head h.
 template <int TR>
 __device__ __forceinline__ bool many_item(const AttendArgs &A, int slot, int h, Item &it, int *b_out) {
-  constexpr int lg = TR == 256 ? 8 : TR == 128 ? 7 : 6;
+  constexpr int lg = TR == 256 ? 8 : 7;
   static_assert(TR == 1 << lg, "a power of two");
   int64_t first;
   const int b = find_sequence(A.S, slot, A.view.group, lg, 1, &first);
@@ -425,7 +425,9 @@ __device__ __forceinline__ void few_rows(const AttendArgs &A, int b, int h, int 
 
   // The item's last workgroup to arrive joins its pieces (with a launch for that 64
   // sequences took 65 us, not 59).  Partial sums go past the caches, every wave's before
-  // the workgroup counts itself, and are read the same way.
+  // the workgroup counts itself, and are read the same way.  That order is the hardware's
+  // (a store past the caches has arrived when its wait ends), not the memory model's,
+  // whose release would write the whole L2 back.
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
   int *flag = (int *)(sl + 16 * W);
