@@ -21,7 +21,9 @@
 // instructions, keeps one (off by up to 2^-11, the half step of out as well).  l is
 // summed in fp32 from the weights before any rounding.
 // Keys that a row does not see get weight 0 by selection, so that what lies
-// there (numbers of earlier owners, scales that are NaN) does not matter.
+// there (numbers of earlier owners, scales that are NaN) does not reach it.  A
+// finite s_v that its wave meets there may become r, 2^-37 of which is the finest
+// step of a weight times s_v (5e-7 for a page of 65504, 8 of fp16's smallest steps).
 //
 // Both kernels work on S^T = K Q^T and O^T = V^T P^T: a lane has one row of q
 // (column of S^T), its maximum and sum are the lane's own up to one or two
